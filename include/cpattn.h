@@ -66,7 +66,8 @@ extern "C" {
 typedef enum {
   CP_OK = 0,
   CP_ERR_INVALID_ARG = -1, /* null pointer, bad size, bad cu_seqlens        */
-  CP_ERR_ALIGNMENT = -2,   /* a length is not a multiple of 2*cp (striped: cp) */
+  CP_ERR_ALIGNMENT = -2,   /* a length is not a multiple of 2*cp (striped: cp);
+                              serving: a pointer or stride off 16 bytes    */
   CP_ERR_UNSUPPORTED = -3, /* head_dim, dtype or head grouping not built
                               (bf16 attention: head_dim 128 only), or
                               batch * seqlen >= 2^31 token rows           */
@@ -300,7 +301,8 @@ size_t cp_static_ws_capacity(void);
 
 /* Waits for `stream`, then reads and clears the library's device error word.
  * Returns CP_OK, or CP_ERR_TIMEOUT if a kernel gave up on a bounded wait since
- * the last call (its outputs are then invalid), or CP_ERR_CUDA. */
+ * the last call (its outputs are then invalid), CP_ERR_INVALID_ARG if a paged
+ * attention met a page number outside its cache, or CP_ERR_CUDA. */
 cp_status cp_get_device_error(void* stream);
 
 /* Failure-detection check: sets the cycle budget of the tcgen05 kernels'
@@ -385,6 +387,160 @@ cp_status cp_hybrid_schedule(const int32_t* lens, int32_t n, int32_t world, int6
 cp_status cp_ring_plan_tables(const cp_attn_desc* desc, int32_t which, int64_t* n_items, int64_t* n_segs,
                               int32_t* items, int32_t* segs);
 
+/* ------------------------------------------------------------------------
+ * Serving: the K/V of running requests live in the pages of a cache, and a
+ * step takes some new tokens of each request: cp_kv_extend gives them pages,
+ * slots and positions, cp_kv_append rotates them and writes their K/V into
+ * the cache, cp_paged_attn_fwd attends over the pages.  All lengths live in
+ * device memory and are read there: no call waits for the host, and each
+ * can be captured into a CUDA graph and replayed on new lengths.  Every call
+ * follows the shared conventions above (caller's memory, caller's stream,
+ * 16-byte aligned rows).
+ * ------------------------------------------------------------------------ */
+
+/* The pages of a cache, for K and V alike: element i of head g of token t of
+ * page n is at n * page_stride + t * token_stride + g * head_stride + i
+ * (strides in elements, multiples of 16 bytes; head_dim contiguous), so that
+ * [page][token][head] and [page][head][token] orders both fit, and so do K and
+ * V side by side in one allocation.  Slot n * page_size + t names a token. */
+typedef struct {
+  void* k;
+  void* v;
+  int32_t n_pages;
+  int32_t page_size;    /* a power of two, 8 to 256                          */
+  int32_t heads_kv;
+  int32_t head_dim;     /* 64 or 128                                         */
+  int64_t page_stride;
+  int64_t token_stride;
+  int64_t head_stride;
+  cp_dtype dtype;
+} cp_kv_cache;
+
+/* Block tables and slot maps from the lengths of the requests.
+ *  lens, add     [n_reqs] device: tokens that request r has in the cache, and
+ *                tokens that it brings; its pages are the first
+ *                ceil(lens / page_size) entries of its table row.
+ *  free_pages    [n_pool] device: numbers of unused pages, n_free [1] of them
+ *                counted from the front, taken from the back.
+ *  block_table   [n_reqs][max_blocks] device, in place: the new pages are
+ *                written behind the request's pages, nothing else changes.
+ *  lens_out      [n_reqs]: lens + add, cu_new [n_reqs + 1]: the first row of
+ *                each request's new tokens, n_free_out [1].
+ *  slots, pos    [max_rows]: slot and position of every new token; -1 and 0
+ *                behind the last.
+ * Requests are served in order: from the first one that does not fit (free
+ * pages, max_blocks, max_rows, a negative length) on, none is: their lengths
+ * stay and they own no row, which cu_new shows.  The outputs must not overlap
+ * the inputs.  n_reqs <= 16384, max_blocks * page_size <= 2^30.
+ * Errors: CP_ERR_INVALID_ARG (null pointers, sizes), CP_ERR_UNSUPPORTED. */
+cp_status cp_kv_extend(int32_t n_reqs, int32_t max_blocks, int32_t page_size, int64_t max_rows, int32_t n_pool,
+                       const int32_t* lens, const int32_t* add, const int32_t* free_pages, const int32_t* n_free,
+                       int32_t* block_table, int32_t* lens_out, int32_t* cu_new, int32_t* slots, int32_t* pos,
+                       int32_t* n_free_out, void* stream);
+
+/* Gives the pages of the requests with done[r] != 0 back: they are appended
+ * to free_pages (request by request, in table order; what n_pool cannot hold
+ * is dropped), their table entries become -1 and lens_out[r] = 0; the others
+ * keep theirs.  block_table and free_pages change in place. */
+cp_status cp_kv_release(int32_t n_reqs, int32_t max_blocks, int32_t page_size, int32_t n_pool, const int32_t* lens,
+                        const int32_t* done, int32_t* free_pages, const int32_t* n_free, int32_t* block_table,
+                        int32_t* lens_out, int32_t* n_free_out, void* stream);
+
+/* Rotary positions with n_axes axes (time, height, width of images and video;
+ * one axis is cp_permute_rope's embedding).  n = the sum of section pairs are
+ * rotated, the last head_dim - 2 n elements of a head are left as they are.
+ *  axis of pair i: section[0] pairs of axis 0, then section[1] of axis 1, ...;
+ *    interleaved: the axes take turns, those that have used up their section
+ *    are passed over.
+ *  angle of pair i: position on its axis times base^(-i / n); restart: times
+ *    base^(-j / section[axis]), j = the pairs of its axis before it.
+ *  pair i: elements (i, i + n), or with adjacent (2 i, 2 i + 1).
+ * n must be a multiple of 8. */
+typedef struct {
+  int32_t n_axes;       /* 1 to 4                                            */
+  int32_t section[4];   /* pairs of each axis                                */
+  int32_t interleaved;
+  int32_t restart;
+  int32_t adjacent;
+  float base;           /* > 0                                               */
+} cp_rope;
+
+/* Rotates q [rows][heads_q][head_dim] and, with heads_k > 0, k [rows][heads_k]
+ * [head_dim] by the positions pos [n_axes][rows] (device, any sign) in one
+ * launch; q_stride, k_stride: elements between rows of the inputs (slices of
+ * one projection), outputs contiguous.  inverse = 1 applies the transpose
+ * R(pos)^T, which is the gradient.  A contiguous input may be its own output.
+ * Angles are exact to 2^-64 turns before they are rounded to float32, for
+ * every int32 position up to the rounding of base^-e to 53 bits.
+ * Errors: CP_ERR_INVALID_ARG, CP_ERR_UNSUPPORTED (head_dim, n % 8 != 0),
+ * CP_ERR_ALIGNMENT (a pointer or stride off 16 bytes). */
+cp_status cp_rope_axes(const cp_rope* rope, const int32_t* pos, int64_t rows, int32_t head_dim, cp_dtype dtype,
+                       int32_t heads_q, const void* q, int64_t q_stride, void* q_out, int32_t heads_k, const void* k,
+                       int64_t k_stride, void* k_out, int32_t inverse, void* stream);
+
+/* Writes k and v [rows][heads_kv][head_dim] (row strides in elements) into the
+ * slots [rows] (device) of the cache.  With rope, k is rotated by pos on the way, and q (heads_q > 0)
+ * into q_out [rows][heads_q][head_dim] in the same launch.  A row
+ * whose slot is negative or behind the last page is left out: nothing of it
+ * is written, q_out's row neither.  Slots that are named twice hold one of
+ * the rows, or 16-byte pieces of both.  Errors as above. */
+cp_status cp_kv_append(const cp_kv_cache* cache, const int32_t* slots, int64_t rows, const void* k, int64_t k_stride,
+                       const void* v, int64_t v_stride, const cp_rope* rope, const int32_t* pos, int32_t heads_q,
+                       const void* q, int64_t q_stride, void* q_out, void* stream);
+
+/* Attention over a paged cache.  The cache holds every visible token, the
+ * new ones among them (cp_kv_append comes first). */
+typedef struct {
+  cp_kv_cache kv;
+  int32_t heads_q;      /* a multiple of kv.heads_kv                         */
+  int32_t max_new;      /* about how many new tokens a request brings at most:
+                           chooses the kernel, any number is computed right; 0: many */
+  int32_t causal;       /* 1: new token i of n, at position len - n + i, sees
+                           the keys up to its own; 0: all of its request     */
+  int32_t window;       /* W > 0: keys at positions > own - W only; 0: none   */
+  float softmax_scale;  /* 0 -> 1/sqrt(head_dim)                              */
+} cp_paged_desc;
+
+/* Host-only check of a descriptor (the errors that the calls below return). */
+cp_status cp_validate_paged_desc(const cp_paged_desc* desc);
+
+/* Bytes of workspace of cp_paged_attn_fwd: fixed by the descriptor, whatever
+ * the lengths.  0 if it is invalid.  256-byte aligned. */
+size_t cp_paged_attn_workspace_bytes(const cp_paged_desc* desc);
+
+/* For request r, with new tokens in rows cu_new[r] .. cu_new[r + 1] - 1 of q
+ * and kv_lens[r] cached tokens (new ones included) in the pages that its row of
+ * block_table [n_reqs][max_blocks] names:
+ *   o [rows][heads_q][head_dim] (kv.dtype), lse [rows][heads_q] float32, natural
+ * log, as cp_tile_attn_fwd gives them (0 and -inf where a row sees no key), so
+ * that they merge with other partial states by cp_merge_partials.
+ * q: [rows][heads_q][head_dim], q_stride elements between rows.  Rows from
+ * cu_new[n_reqs] on are left as they were.
+ * Lengths are clamped to the table and to the rows of q.  Only pages with a visible key are
+ * looked at: entries behind the last key, or in front of every row's window, may
+ * hold anything, and so may the rest of the last page.  A page number outside
+ * the cache where a key is visible reads as zeros and is reported: cp_get_device_error then
+ * returns CP_ERR_INVALID_ARG.  A K/V value that is not finite reaches every
+ * row whose tile of keys holds it, as in the other attention calls.
+ * Results do not depend on timing: the same call gives the same bits.
+ * Calls that share a workspace must not overlap on the GPU.
+ * Errors: CP_ERR_INVALID_ARG, CP_ERR_UNSUPPORTED (sizes, heads), CP_ERR_ALIGNMENT,
+ * CP_ERR_WORKSPACE. */
+cp_status cp_paged_attn_fwd(const cp_paged_desc* desc, int32_t n_reqs, int64_t rows, int32_t max_blocks,
+                            const void* q, int64_t q_stride, const int32_t* block_table, const int32_t* cu_new,
+                            const int32_t* kv_lens, void* o, float* lse, void* ws, size_t ws_bytes, void* stream);
+
+/* Host only: how cp_paged_attn_fwd divides a call with these lengths (HOST
+ * arrays cu_new [n_reqs + 1] and kv_lens [n_reqs]) over the *grid blocks of its
+ * launch, for tests and tools.  pieces [*n][8] int32, in the order of the
+ * blocks: block, request, kv-head, first packed row of the tile (token * group + head
+ * in group, counted in the request), packed rows, first key and end of the
+ * piece's keys, and the slot of its partial state (-1: the tile is whole and goes to
+ * the outputs).  Pass null arrays to read the sizes first. */
+cp_status cp_paged_schedule(const cp_paged_desc* desc, int32_t n_reqs, int64_t rows, int32_t max_blocks,
+                            const int32_t* cu_new, const int32_t* kv_lens, int32_t* grid, int64_t* n,
+                            int32_t* pieces);
+
 /* Kernel classes reported by cp_profile_read. */
 typedef enum {
   CP_K_PARTITION = 0, /* partition index kernel                          */
@@ -396,7 +552,11 @@ typedef enum {
   CP_K_CONVERT = 6,   /* float32 accumulator -> output dtype             */
   CP_K_TABLES = 7,    /* task-graph table upload (pinned host -> workspace) */
   CP_K_ROPE = 8,      /* token gather with rotary position embedding     */
-  CP_K_COUNT = 9
+  CP_K_KV_TABLES = 9, /* request tables of a paged cache                 */
+  CP_K_HEAD_ROWS = 10, /* multi-axis rotation, rows into a paged cache   */
+  CP_K_PAGED = 11,    /* attention over a paged cache                    */
+  CP_K_PAGED_MERGE = 12, /* join of its cut tiles                        */
+  CP_K_COUNT = 13
 } cp_kernel_class;
 
 /* Benchmark instrumentation (no effect on results).  With timing on, every

@@ -30,8 +30,11 @@ EXPORTS = ("cp_status_string", "cp_validate_desc", "cp_partition_indices", "cp_p
            "cp_ring_attn_fwd", "cp_ring_attn_bwd", "cp_get_device_error", "cp_ring_plan_stats",
            "cp_profile_enable", "cp_profile_read", "cp_ring_attn_fwd_static_ws",
            "cp_static_ws_capacity", "cp_ring_bwd_schedule", "cp_permute_rope", "cp_hybrid_schedule",
-           "cp_ring_plan_tables", "cp_token_seq_pos", "cp_debug_set_wait_limit")
-KERNEL_CLASSES = ("partition", "permute", "tile_fwd", "merge", "delta", "tile_bwd", "convert", "tables", "rope")
+           "cp_ring_plan_tables", "cp_token_seq_pos", "cp_debug_set_wait_limit",
+           "cp_kv_extend", "cp_kv_release", "cp_rope_axes", "cp_kv_append", "cp_validate_paged_desc",
+           "cp_paged_attn_workspace_bytes", "cp_paged_attn_fwd", "cp_paged_schedule")
+KERNEL_CLASSES = ("partition", "permute", "tile_fwd", "merge", "delta", "tile_bwd", "convert", "tables", "rope",
+                  "kv_tables", "head_rows", "paged", "paged_merge")
 
 
 class CpError(RuntimeError):
@@ -61,6 +64,43 @@ class CpAttnDesc(ctypes.Structure):
         ("seq_rank0_host", ctypes.c_void_p),
         ("seq_cp_dev", ctypes.c_void_p),
         ("seq_rank0_dev", ctypes.c_void_p),
+    ]
+
+
+class CpRope(ctypes.Structure):
+    _fields_ = [
+        ("n_axes", ctypes.c_int32),
+        ("section", ctypes.c_int32 * 4),
+        ("interleaved", ctypes.c_int32),
+        ("restart", ctypes.c_int32),
+        ("adjacent", ctypes.c_int32),
+        ("base", ctypes.c_float),
+    ]
+
+
+class CpKvCache(ctypes.Structure):
+    _fields_ = [
+        ("k", ctypes.c_void_p),
+        ("v", ctypes.c_void_p),
+        ("n_pages", ctypes.c_int32),
+        ("page_size", ctypes.c_int32),
+        ("heads_kv", ctypes.c_int32),
+        ("head_dim", ctypes.c_int32),
+        ("page_stride", ctypes.c_int64),
+        ("token_stride", ctypes.c_int64),
+        ("head_stride", ctypes.c_int64),
+        ("dtype", ctypes.c_int32),
+    ]
+
+
+class CpPagedDesc(ctypes.Structure):
+    _fields_ = [
+        ("kv", CpKvCache),
+        ("heads_q", ctypes.c_int32),
+        ("max_new", ctypes.c_int32),
+        ("causal", ctypes.c_int32),
+        ("window", ctypes.c_int32),
+        ("softmax_scale", ctypes.c_float),
     ]
 
 
@@ -99,6 +139,15 @@ def lib():
             "cp_ring_plan_tables": ([D, I32, P, P, P, P], I32),
             "cp_token_seq_pos": ([D, P, P, P], I32),
             "cp_debug_set_wait_limit": ([I64], I32),
+            "cp_kv_extend": ([I32, I32, I32, I64, I32] + [P] * 11, I32),
+            "cp_kv_release": ([I32, I32, I32, I32] + [P] * 8, I32),
+            "cp_rope_axes": ([ctypes.POINTER(CpRope), P, I64, I32, I32, I32, P, I64, P, I32, P, I64, P, I32, P], I32),
+            "cp_kv_append": ([ctypes.POINTER(CpKvCache), P, I64, P, I64, P, I64, ctypes.POINTER(CpRope), P, I32, P, I64,
+                              P, P], I32),
+            "cp_validate_paged_desc": ([ctypes.POINTER(CpPagedDesc)], I32),
+            "cp_paged_schedule": ([ctypes.POINTER(CpPagedDesc), I32, I64, I32, P, P, P, P, P], I32),
+            "cp_paged_attn_workspace_bytes": ([ctypes.POINTER(CpPagedDesc)], SZ),
+            "cp_paged_attn_fwd": ([ctypes.POINTER(CpPagedDesc), I32, I64, I32, P, I64, P, P, P, P, P, P, SZ, P], I32),
         }
         for name, (args, res) in sig.items():
             fn = getattr(L, name)
@@ -339,6 +388,223 @@ def ring_attn_bwd(p: Problem, q, k, v, o, lse, dout, ws: torch.Tensor | None = N
                                   _ptr(dq), _ptr(dk), _ptr(dv), _ptr(ws), ws.numel(), _stream()),
            "cp_ring_attn_bwd")
     return dq, dk, dv
+
+
+# ---------------------------------------------------------------- serving ---
+class PagedKV:
+    """The pages of a K/V cache: two [n_pages, page_size, heads_kv, head_dim]
+    views of the same strides (any order of pages, tokens and heads in memory,
+    head_dim contiguous), kept alive here."""
+
+    def __init__(self, k_cache: torch.Tensor, v_cache: torch.Tensor):
+        if k_cache.dim() != 4 or k_cache.shape != v_cache.shape or k_cache.stride() != v_cache.stride():
+            raise ValueError("k_cache and v_cache are [n_pages, page_size, heads_kv, head_dim] views of the same strides")
+        if k_cache.dtype != v_cache.dtype or k_cache.device != v_cache.device or k_cache.stride(3) != 1:
+            raise ValueError("k_cache and v_cache share their type and device, head_dim contiguous")
+        self.k_cache, self.v_cache = k_cache, v_cache
+        self.n_pages, self.page_size, self.heads_kv, self.head_dim = k_cache.shape
+        self.dtype, self.device = k_cache.dtype, k_cache.device
+        s = k_cache.stride()
+        self._desc = CpKvCache(k_cache.data_ptr(), v_cache.data_ptr(), *k_cache.shape, s[0], s[1], s[2],
+                               _dtype_code(k_cache.dtype))
+        self._ref = ctypes.byref(self._desc)
+
+
+class Rope:
+    """Rotary positions with several axes (cp_rope): pairs of each axis."""
+
+    def __init__(self, sections, base: float = 10000.0, interleaved: bool = False, restart: bool = False,
+                 adjacent: bool = False):
+        self.sections = [int(x) for x in sections]
+        if not 1 <= len(self.sections) <= 4:
+            raise ValueError("one to four axes")
+        self._desc = CpRope(len(self.sections), (ctypes.c_int32 * 4)(*self.sections), int(interleaved), int(restart),
+                            int(adjacent), float(base))
+        self._ref = ctypes.byref(self._desc)
+
+
+class PagedProblem:
+    """Attention over a paged cache (cp_paged_desc)."""
+
+    def __init__(self, kv: PagedKV, heads_q: int, max_new: int = 0, causal: bool = True, window: int = 0,
+                 softmax_scale: float = 0.0):
+        self.kv, self.heads_q = kv, int(heads_q)
+        self._desc = CpPagedDesc(kv._desc, self.heads_q, int(max_new), int(bool(causal)), int(window),
+                                 float(softmax_scale))
+        self._ref = ctypes.byref(self._desc)
+
+
+def _rows(x: torch.Tensor, what: str, shape, dtype, device):
+    """Row stride (elements) of a [rows, heads, head_dim] tensor whose rows are contiguous."""
+    if x.shape[1:] != shape or x.dim() != 3 or x.dtype != dtype or x.device != device:
+        raise ValueError(f"{what} is a [rows, {shape[0]}, {shape[1]}] {dtype} tensor on {device}")
+    s = x.stride()
+    if s[2] != 1 or (s[1] != shape[1] and shape[0] > 1):
+        raise ValueError(f"{what}: the heads of a row are contiguous")
+    return s[0] if x.shape[0] > 1 else shape[0] * shape[1]
+
+
+def _ints(x: torch.Tensor, what: str, shape, device):
+    if x.dtype != torch.int32 or tuple(x.shape) != shape or not x.is_contiguous() or x.device != device:
+        raise ValueError(f"{what} is a contiguous {list(shape)} int32 tensor on {device}")
+    return x.data_ptr()
+
+
+def _new(out, what, shape, dtype, device):
+    """The caller's output tensor (contiguous, of that shape and type), or a new one."""
+    if out is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if tuple(out.shape) != tuple(shape) or out.dtype != dtype or out.device != device or not out.is_contiguous():
+        raise ValueError(f"{what} is a contiguous {list(shape)} {dtype} tensor on {device}")
+    return out
+
+
+def _stream_of(device):
+    """The current stream of the device that holds the tensors (it has to be the current device)."""
+    if device.type != "cuda" or device.index != torch.cuda.current_device():
+        raise ValueError(f"the tensors are on {device}: make it the current CUDA device")
+    return torch.cuda.current_stream().cuda_stream
+
+
+def kv_extend(page_size: int, block_table, lens, add, free_pages, n_free, max_rows: int):
+    """Pages, slots and positions for `add` new tokens of every request (cp_kv_extend).
+
+    block_table [n_reqs, max_blocks] changes in place; returns (lens, cu_new,
+    slots, pos, n_free) as new tensors."""
+    if block_table.dim() != 2:
+        raise ValueError("block_table is [n_reqs, max_blocks]")
+    n, width = block_table.shape
+    dev = block_table.device
+    pool = free_pages.numel()
+    args = [_ints(lens, "lens", (n,), dev), _ints(add, "add", (n,), dev), _ints(free_pages, "free_pages", (pool,), dev),
+            _ints(n_free, "n_free", (1,), dev), _ints(block_table, "block_table", (n, width), dev)]
+    s = _stream_of(dev)
+    out = torch.empty(2 * n + 2 + 2 * max_rows, dtype=torch.int32, device=dev)
+    lens_out, cu, n_free_out, slots, pos = out.split((n, n + 1, 1, max_rows, max_rows))
+    base = out.data_ptr()
+    _check(lib().cp_kv_extend(n, width, page_size, max_rows, pool, *args, base, base + 4 * n, base + 4 * (2 * n + 2),
+                              base + 4 * (2 * n + 2 + max_rows), base + 4 * (2 * n + 1), s), "cp_kv_extend")
+    return lens_out, cu, slots, pos, n_free_out
+
+
+def kv_release(page_size: int, block_table, lens, done, free_pages, n_free):
+    """Gives the pages of the requests with done != 0 back (cp_kv_release);
+    block_table and free_pages change in place; returns (lens, n_free)."""
+    if block_table.dim() != 2:
+        raise ValueError("block_table is [n_reqs, max_blocks]")
+    n, width = block_table.shape
+    dev = block_table.device
+    pool = free_pages.numel()
+    args = [_ints(lens, "lens", (n,), dev), _ints(done, "done", (n,), dev), _ints(free_pages, "free_pages", (pool,), dev),
+            _ints(n_free, "n_free", (1,), dev), _ints(block_table, "block_table", (n, width), dev)]
+    s = _stream_of(dev)
+    lens_out, n_free_out = torch.empty_like(lens), torch.empty_like(n_free)
+    _check(lib().cp_kv_release(n, width, page_size, pool, *args, lens_out.data_ptr(), n_free_out.data_ptr(), s),
+           "cp_kv_release")
+    return lens_out, n_free_out
+
+
+def _positions(rope: Rope, pos: torch.Tensor, rows: int, device):
+    axes = len(rope.sections)
+    return _ints(pos, "pos", (rows,) if axes == 1 and pos.dim() == 1 else (axes, rows), device)
+
+
+def rope_axes(rope: Rope, pos, q, k=None, inverse: bool = False, q_out=None, k_out=None):
+    """Rotates q [rows, heads, head_dim] (and k) by pos [axes, rows] (cp_rope_axes);
+    inverse: the transpose, which is the gradient."""
+    dev, dt = q.device, q.dtype
+    if q.dim() != 3 or (k is not None and k.dim() != 3):
+        raise ValueError("q and k are [rows, heads, head_dim]")
+    rows, hq, d = q.shape
+    qs = _rows(q, "q", (hq, d), dt, dev)
+    hk, ks = (0, 0) if k is None else (k.shape[1], _rows(k, "k", (k.shape[1], d), dt, dev))
+    if k is not None and k.shape[0] != rows:
+        raise ValueError("q and k have the same rows")
+    p, s = _positions(rope, pos, rows, dev), _stream_of(dev)
+    q_out = _new(q_out, "q_out", (rows, hq, d), dt, dev)
+    if k is not None:
+        k_out = _new(k_out, "k_out", (rows, hk, d), dt, dev)
+    _check(lib().cp_rope_axes(rope._ref, p, rows, d, _dtype_code(dt), hq, q.data_ptr(), qs, q_out.data_ptr(), hk,
+                              None if k is None else k.data_ptr(), ks, None if k is None else k_out.data_ptr(),
+                              int(inverse), s), "cp_rope_axes")
+    return q_out if k is None else (q_out, k_out)
+
+
+def kv_append(kv: PagedKV, slots, k, v, rope: Rope | None = None, pos=None, q=None, q_out=None):
+    """Writes k and v [rows, heads_kv, head_dim] into the slots of the cache
+    (cp_kv_append); with rope, k is rotated by pos on the way and q into the
+    returned q_out."""
+    dev, dt, shape = kv.device, kv.dtype, (kv.heads_kv, kv.head_dim)
+    rows = k.shape[0]
+    ks, vs = _rows(k, "k", shape, dt, dev), _rows(v, "v", shape, dt, dev)
+    if v.shape[0] != rows:
+        raise ValueError("k and v have the same rows")
+    if (rope is None) != (pos is None) or (q is not None and rope is None):
+        raise ValueError("rope, pos and q: positions come with a rotation, q is rotated")
+    hq, qs = 0, 0
+    if q is not None:
+        if q.dim() != 3 or q.shape[0] != rows:
+            raise ValueError("q is [rows, heads_q, head_dim]")
+        hq = q.shape[1]
+        qs = _rows(q, "q", (hq, kv.head_dim), dt, dev)
+        q_out = _new(q_out, "q_out", (rows, hq, kv.head_dim), dt, dev)
+    p = None if rope is None else _positions(rope, pos, rows, dev)
+    s = _stream_of(dev)
+    _check(lib().cp_kv_append(kv._ref, _ints(slots, "slots", (rows,), dev), rows, k.data_ptr(), ks, v.data_ptr(), vs,
+                              None if rope is None else rope._ref, p, hq, None if q is None else q.data_ptr(), qs,
+                              None if q is None else q_out.data_ptr(), s), "cp_kv_append")
+    return None if q is None else q_out
+
+
+def validate_paged(p: PagedProblem) -> int:
+    return int(lib().cp_validate_paged_desc(p._ref))
+
+
+def paged_workspace_bytes(p: PagedProblem) -> int:
+    return int(lib().cp_paged_attn_workspace_bytes(p._ref))
+
+
+def paged_workspace(p: PagedProblem) -> torch.Tensor:
+    n = paged_workspace_bytes(p)
+    if n == 0:
+        raise CpError(validate_paged(p), "cp_paged_attn_workspace_bytes")
+    return torch.empty(n, dtype=torch.uint8, device=p.kv.device)
+
+
+def paged_schedule(p: PagedProblem, cu_new, kv_lens, rows: int, max_blocks: int):
+    """The pieces [n, 8] of a call with these lengths (host only): block, request,
+    kv-head, first packed row, packed rows, first key, end of its keys, slot
+    (-1: the outputs); and the number of blocks."""
+    cu, lens = (np.ascontiguousarray(np.asarray(x, dtype=np.int32)) for x in (cu_new, kv_lens))
+    n, grid = ctypes.c_int64(0), ctypes.c_int32(0)
+    args = (p._ref, len(lens), rows, max_blocks, cu.ctypes.data, lens.ctypes.data)
+    _check(lib().cp_paged_schedule(*args, ctypes.byref(grid), ctypes.byref(n), None), "cp_paged_schedule")
+    out = np.zeros((n.value, 8), dtype=np.int32)
+    _check(lib().cp_paged_schedule(*args, None, None, out.ctypes.data), "cp_paged_schedule")
+    return out, grid.value
+
+
+def paged_attn_fwd(p: PagedProblem, q, block_table, cu_new, kv_lens, ws: torch.Tensor | None = None, out=None,
+                   lse=None):
+    """Attention of the new tokens q [rows, heads_q, head_dim] over the pages of
+    their requests (cp_paged_attn_fwd) -> (o, lse).  Rows behind the last
+    request's are left as they were (unset in a new o and lse)."""
+    kv = p.kv
+    dev = kv.device
+    qs = _rows(q, "q", (p.heads_q, kv.head_dim), kv.dtype, dev)
+    if block_table.dim() != 2:
+        raise ValueError("block_table is [n_reqs, max_blocks]")
+    n, width = block_table.shape
+    tables = (_ints(block_table, "block_table", (n, width), dev), _ints(cu_new, "cu_new", (n + 1,), dev),
+              _ints(kv_lens, "kv_lens", (n,), dev))
+    s = _stream_of(dev)
+    ws = paged_workspace(p) if ws is None else ws
+    rows = q.shape[0]
+    out = _new(out, "out", (rows, p.heads_q, kv.head_dim), kv.dtype, dev)
+    lse = _new(lse, "lse", (rows, p.heads_q), torch.float32, dev)
+    _check(lib().cp_paged_attn_fwd(p._ref, n, rows, width, q.data_ptr(), qs, *tables, out.data_ptr(), lse.data_ptr(),
+                                   ws.data_ptr(), ws.nbytes, s), "cp_paged_attn_fwd")
+    return out, lse
 
 
 def device_error() -> int:

@@ -6,6 +6,7 @@
 
 #include "device_util.cuh"
 #include "internal.h"
+#include "paged.h"
 #include "tmap.h"
 #include "tc_util.cuh"
 
@@ -51,7 +52,7 @@ cp_status read_and_clear_device_error(cudaStream_t s) {
   if (v != 0) {
     const int zero = 0;
     if (cudaMemcpyToSymbol(g_cp_device_error, &zero, sizeof(int)) != cudaSuccess) return CP_ERR_CUDA;
-    return CP_ERR_TIMEOUT;
+    return v == kErrBadPage ? CP_ERR_INVALID_ARG : CP_ERR_TIMEOUT;
   }
   return CP_OK;
 }
