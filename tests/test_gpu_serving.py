@@ -335,6 +335,9 @@ ATTN = [
     ("few_new", [3, 1, 8, 2], [3, 200, 77, 1000], 8, 4, True, 0),
     ("chunks", [70, 129, 1, 33], [70, 300, 129, 700], 4, 2, True, 0),
     ("wide_chunk", [260], [777], 28, 4, True, 0),
+    ("tile_ends_in_the_last_page", [65, 129, 66], [65, 190, 1100], 8, 2, True, 0),
+    ("window_in_chunks", [200, 70, 1, 300], [900, 70, 500, 301], 8, 2, True, 77),
+    ("ends_of_pages", [64, 70, 70, 70, 70], [128, 129, 192, 255, 257], 4, 1, True, 0),
     ("no_new_and_empty", [0, 2, 0, 5, 0], [9, 0, 0, 5, 33], 4, 1, True, 0),
     ("more_new_than_cached", [20, 3], [7, 50], 4, 2, True, 0),
     ("window", [1, 40, 5, 1], [600, 333, 5, 20], 8, 2, True, 50),

@@ -65,3 +65,25 @@ def test_wait_limit_argument_checks():
     assert e.value.code == -1
     api.set_wait_limit(-5)                               # <= 0: the default
     api.set_wait_limit(0)
+
+
+def test_wait_limit_of_the_paged_kernel():
+    b, s, H, d, page = 1, 512, 4, 128, 64
+    q, k, v, _ = make_inputs(b, s, H, H, d, seed=18, dtype=torch.bfloat16, with_do=True)
+    kv = api.PagedKV(k[0].view(-1, page, H, d).to(DEV), v[0].view(-1, page, H, d).to(DEV))
+    table = torch.arange(s // page, dtype=torch.int32, device=DEV)[None]
+    cu, lens = (torch.tensor(x, dtype=torch.int32, device=DEV) for x in ([0, s], [s]))
+    p = api.PagedProblem(kv, H, max_new=s)
+    qd = q[0].to(DEV)
+    try:
+        api.set_wait_limit(1)
+        api.paged_attn_fwd(p, qd, table, cu, lens)
+        assert api.device_error() == CP_ERR_TIMEOUT
+    finally:
+        api.set_wait_limit(0)
+    assert api.device_error() == 0
+    o, l = api.paged_attn_fwd(p, qd, table, cu, lens)
+    assert api.device_error() == 0
+    ro, rl = A.attention_forward_bshd(f64(q), f64(k), f64(v))
+    assert max_abs(f64(o), ro[0]) <= TOL_O_BF16
+    assert max_abs(f64(l), rl[0]) <= TOL_LSE_BF16

@@ -196,6 +196,9 @@ inline int paged_rows(PagedKernel k, int G) {
 cp_status launch_paged_slice(const PagedArgs& a, PagedKernel k, cudaStream_t s);
 cp_status launch_paged_merge(const PagedArgs& a, PagedKernel k, cudaStream_t s);
 int paged_slice_grid();
+cp_status launch_paged_pair(const PagedArgs& a, cudaStream_t s);
+// Pairs of SMs that can run at once (sets the kernel up on the first call).
+cp_status paged_pair_grid(int32_t* pairs);
 
 // Rotation of the pairs of a head (cp_rope): turns per position of every
 // pair as 64-bit binary fractions, and the pair's axis.

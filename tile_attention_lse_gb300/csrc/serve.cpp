@@ -75,10 +75,12 @@ PagedKernel pick_kernel(const cp_paged_desc& d) {
   const int64_t G = d.heads_q / d.kv.heads_kv;
   const int64_t rows = d.max_new > 0 ? G * d.max_new : INT64_MAX;
   if (d.kv.dtype == CP_F32) return rows <= 4 ? kPagedSlice4 : kPagedSlice16;
-  return rows <= 16 ? kPagedSlice16 : kPagedSlice32;
+  if (rows <= 16) return kPagedSlice16;
+  return d.kv.head_dim == 128 && G <= kPairRows ? kPagedPair : kPagedSlice32;
 }
 
-int paged_grid(PagedKernel) { return paged_slice_grid(); }
+// Blocks (pairs of blocks) that a launch has at most.
+int paged_grid(PagedKernel k) { return k == kPagedPair ? paged_slice_grid() / 2 : paged_slice_grid(); }
 
 cp_status check_paged(const cp_paged_desc* d) {
   if (!d) return CP_ERR_INVALID_ARG;
@@ -362,10 +364,14 @@ cp_status cp_paged_attn_fwd(const cp_paged_desc* desc, int32_t n_reqs, int64_t r
   a.dtype = c.dtype;
   a.grid = paged_grid(kern);
   a.err = device_error_ptr();
+  if (kern == kPagedPair) {
+    const cp_status r = tc_available() ? paged_pair_grid(&a.grid) : CP_ERR_UNSUPPORTED;
+    if (r != CP_OK) return r;
+  }
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   {
     ProfScope ps(CP_K_PAGED, s);
-    const cp_status r = launch_paged_slice(a, kern, s);
+    const cp_status r = kern == kPagedPair ? launch_paged_pair(a, s) : launch_paged_slice(a, kern, s);
     if (r != CP_OK) return r;
   }
   ProfScope ps(CP_K_PAGED_MERGE, s);
