@@ -9,14 +9,19 @@
 //
 // What bounds it: a single token per request reads 4 d bytes (bf16) of K and V
 // per key and kv-head and does 8 d G flops on them, so HBM is the bound; the
-// kernel's job is to keep enough loads in flight on every SM.  Each warp walks
-// its own slices of 16 keys (slices w, w + W, ... of the block's piece) through a
-// ring of its own, filled by 16-byte asynchronous copies: no block barrier
-// stands between a load and its use.  The ring runs on across pieces, so the
-// next tile's keys are on their way while a finished tile's warps join their
-// states.  Keys behind the request's last, in front of a window or on a page
-// number outside the cache are zero-filled without being read, so whatever
-// the rest of a page holds cannot reach a sum.
+// kernel's job is to keep enough loads in flight on every SM.  Warps have parts:
+//   producer  walks the block's share, up to four pieces ahead, and loads it: Q
+//             by 16-byte copies, K and V by TMA, a box per page and 128 bytes
+//             of the head, into a ring of stages of 32 KB (head_dim 64: 16 KB);
+//   workers   four take each stage, the other four the next; a worker has its own
+//             slice of a stage's keys and its own running maximum, sum and O, so
+//             no barrier stands between them; at the end of a piece it leaves its state
+//             in shared memory and goes on with the next one;
+//   joiner    joins the workers' states of a piece and writes it out meanwhile.
+// Pages that no row sees are loaded from outside the map: zeros, without
+// touching memory.  Keys outside a tile's range that share a page with others
+// are masked out of S, and their V is masked to zero before the second product (0 times
+// what the rest of a page holds need not be 0).
 //
 // bf16: mma.sync m16n8k16, rows of the tile on M (16 or 32, G query heads of a
 //   kv-head packed), so K and V are read once for all of them; P is rounded
@@ -24,8 +29,8 @@
 //   precision), its row sum is taken in float32 before that.  The legacy
 //   tensor path is chosen here because these tiles have too few rows to be
 //   bound by it.
-// float32: FFMA throughout.  A lane pair owns a key (half of the head each) in
-//   the first product, a lane 4 columns of the head in the second.
+// float32: FFMA throughout.  Four lanes own a key (a quarter of the head each)
+//   in the first product, a lane 4 columns of the head in the second.
 #include <cuda_bf16.h>
 
 #include <atomic>
@@ -33,6 +38,7 @@
 
 #include "device_util.cuh"
 #include "paged_dev.cuh"
+#include "paged_tmap.h"
 #include "tc_util.cuh"
 #include "tmap.h"
 
@@ -40,13 +46,10 @@ namespace cpattn {
 
 namespace {
 
-constexpr int kKeys = 16;  // keys of a slice
-
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool read) {
   const int n = read ? 16 : 0;
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
 }
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
@@ -77,19 +80,13 @@ struct PieceInfo {
   int32_t q0, row0, nrows, h;  // first row of the request in q, tile rows, kv-head
   int32_t pos0;                // position of the request's first new token
   int32_t kv;
-  int32_t key0, n;             // first slice's first key, slices
+  int32_t key0, n;             // first stage's first key, stages
   int32_t lo, hi;              // keys that some row sees
   int32_t full_lo, full_hi;    // keys that every row sees
   int32_t slot;
 };
 
-__device__ __forceinline__ void slices_of(const PagedPiece& p, int32_t& key0, int32_t& n) {
-  const int a = (p.tile.b0 + p.ua) * kSliceUnit, b = (p.tile.b0 + p.ub) * kSliceUnit;
-  key0 = max(a, p.tile.lo & ~(kKeys - 1));
-  const int end = min(b, p.tile.hi);
-  n = end > key0 ? (end - key0 + kKeys - 1) / kKeys : 0;
-}
-
+template <int kStageKeys>
 __device__ __forceinline__ PieceInfo piece_info(const PagedArgs& a, const PagedPiece& p) {
   PieceInfo i;
   i.valid = 1;
@@ -99,7 +96,9 @@ __device__ __forceinline__ PieceInfo piece_info(const PagedArgs& a, const PagedP
   i.h = p.h;
   i.pos0 = p.q.kv - p.q.nq;
   i.kv = p.q.kv;
-  slices_of(p, i.key0, i.n);
+  i.key0 = (p.tile.b0 + p.ua) * kSliceUnit;
+  const int end = min((p.tile.b0 + p.ub) * kSliceUnit, p.tile.hi);
+  i.n = end > i.key0 ? (end - i.key0 + kStageKeys - 1) / kStageKeys : 0;
   i.lo = p.tile.lo;
   i.hi = p.tile.hi;
   const int first = i.pos0 + i.row0 / a.G, last = i.pos0 + (i.row0 + i.nrows - 1) / a.G;
@@ -113,20 +112,25 @@ __device__ __forceinline__ PieceInfo piece_info(const PagedArgs& a, const PagedP
 template <int D, int R>
 struct SliceBf16 {
   using T = __nv_bfloat16;
-  static constexpr int kWarps = 8, kStages = 2;
+  static constexpr int kWarps = 8, kKeys = 16, kStages = D == 128 ? 4 : 8;
+  static constexpr int kStageKeys = 4 * kKeys;
   static constexpr int MT = R / 16, NT = D / 8;
   static constexpr int kAcc = MT * NT * 4, kRows = MT * 2;  // accumulators and rows of a thread
   static constexpr int kQBytes = R * D * 2;
   static constexpr int kScratch = 0;
+  static constexpr int kState = (kAcc / 4 + kRows / 2) * 32;  // float4s of a worker's state
+  static constexpr int kPieces = 4;  // pieces that the scheduler is ahead
   static constexpr bool kKeepQ = MT == 1;
   float acc[kAcc];
   float m[kRows], l[kRows];
   uint32_t qf[kKeepQ ? D / 16 : 1][4];
   int32_t lo[kRows], hi[kRows];
 
-  // 16-byte chunk c of row r
-  static __device__ __forceinline__ uint32_t at(int r, int c) { return uint32_t(r * D * 2 + ((c ^ (r & 7)) << 4)); }
-  static __device__ __forceinline__ uint32_t q_at(int r, int c) { return at(r, c); }
+  // 16-byte chunk c of row r: of Q, and of a stage (128-byte columns of all its keys, swizzled by TMA)
+  static __device__ __forceinline__ uint32_t q_at(int r, int c) { return uint32_t(r * D * 2 + ((c ^ (r & 7)) << 4)); }
+  static __device__ __forceinline__ uint32_t at(int r, int c) {
+    return uint32_t((c >> 3) * (kStageKeys * 128) + r * 128 + (((c ^ r) & 7) << 4));
+  }
 
   __device__ __forceinline__ void begin(const PagedArgs& a, const PieceInfo& p, uint32_t sq, int lane) {
 #pragma unroll
@@ -141,12 +145,13 @@ struct SliceBf16 {
     }
     if constexpr (kKeepQ) {
 #pragma unroll
-      for (int k = 0; k < D / 16; ++k) ldm4(sq + at(lane & 15, 2 * k + (lane >> 4)), qf[k]);
+      for (int k = 0; k < D / 16; ++k) ldm4(sq + q_at(lane & 15, 2 * k + (lane >> 4)), qf[k]);
     }
   }
 
-  __device__ __forceinline__ void slice(const PagedArgs& a, uint32_t sq, uint32_t sk, uint32_t sv, float*, int key,
-                                        bool full, int lane) {
+  // One slice: the keys from `key` on, in rows `srow` .. of the stage at sk and sv; klo, khi: the tile's keys.
+  __device__ __forceinline__ void slice(const PagedArgs& a, uint32_t sq, uint32_t sk, uint32_t sv, int srow, float*,
+                                        int key, bool full, int klo, int khi, int lane) {
     float s[MT][2][4];
 #pragma unroll
     for (int i = 0; i < MT; ++i)
@@ -157,7 +162,7 @@ struct SliceBf16 {
 #pragma unroll
     for (int k = 0; k < D / 16; ++k) {
       uint32_t b[4];
-      ldm4(sk + at((lane & 7) + ((lane >> 4) << 3), 2 * k + ((lane >> 3) & 1)), b);
+      ldm4(sk + at(srow + (lane & 7) + ((lane >> 4) << 3), 2 * k + ((lane >> 3) & 1)), b);
 #pragma unroll
       for (int i = 0; i < MT; ++i) {
         uint32_t f[4];
@@ -165,7 +170,7 @@ struct SliceBf16 {
 #pragma unroll
           for (int e = 0; e < 4; ++e) f[e] = qf[k][e];
         } else {
-          ldm4(sq + at(16 * i + (lane & 15), 2 * k + (lane >> 4)), f);
+          ldm4(sq + q_at(16 * i + (lane & 15), 2 * k + (lane >> 4)), f);
         }
         mma16816(s[i][0], f, b[0], b[1]);
         mma16816(s[i][1], f, b[2], b[3]);
@@ -228,10 +233,20 @@ struct SliceBf16 {
         p[i][2 + h] = tc::pack_bf16x2(e[2], e[3]);
       }
     }
+    uint32_t keep0 = 0xffffffffu, keep1 = 0xffffffffu;  // this lane's keys of V: j0, j0 + 1 and 8 further
+    if (!full) {
+      auto in = [&](int j) { return j >= klo && j < khi; };
+      keep0 = (in(j0) ? 0xffffu : 0u) | (in(j0 + 1) ? 0xffff0000u : 0u);
+      keep1 = (in(j0 + 8) ? 0xffffu : 0u) | (in(j0 + 9) ? 0xffff0000u : 0u);
+    }
 #pragma unroll
     for (int n = 0; n < D / 16; ++n) {
       uint32_t b[4];
-      ldm4t(sv + at(lane & 15, 2 * n + (lane >> 4)), b);
+      ldm4t(sv + at(srow + (lane & 15), 2 * n + (lane >> 4)), b);
+      b[0] &= keep0;
+      b[1] &= keep1;
+      b[2] &= keep0;
+      b[3] &= keep1;
 #pragma unroll
       for (int i = 0; i < MT; ++i) {
         mma16816(acc + (i * NT + 2 * n) * 4, p[i], b[0], b[1]);
@@ -248,23 +263,66 @@ struct SliceBf16 {
       l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
     }
   }
-  static __device__ __forceinline__ int row_of(int i) { return (i / (NT * 4)) * 2 + ((i >> 1) & 1); }
 
-  // f(row, column, values of two columns), lse(row, value)
+  // Joins the workers' states at `st` (float4s [worker][kAcc / 4 + kRows / 2][lane]):
+  // f(row, column, two columns' values), g(row, log2 of the sum of 2^scores).
   template <typename FO, typename FL>
-  __device__ __forceinline__ void write(int lane, FO f, FL g) {
+  static __device__ __forceinline__ void join(const float4* st, int lane, FO f, FL g) {
+    float c[kWarps][kRows], inv[kRows], top[kRows];
 #pragma unroll
     for (int r = 0; r < kRows; ++r) {
-      const int row = (lane >> 2) + 8 * r;
-      const float inv = l[r] > 0.f ? 1.f / l[r] : 0.f;
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        const int i = ((r >> 1) * NT + n) * 4 + 2 * (r & 1);
-        const float x[2] = {acc[i] * inv, acc[i + 1] * inv};
-        f.template operator()<2>(row, 8 * n + 2 * (lane & 3), x);
-      }
-      if ((lane & 3) == 0) g(row, l[r] > 0.f ? m[r] + tc::lg2(l[r]) : -INFINITY);
+      top[r] = -INFINITY;
+      inv[r] = 0.f;
     }
+    // a float4 of rows: m and l of rows 2 i, 2 i + 1
+#pragma unroll
+    for (int i = 0; i < kRows / 2; ++i) {
+      float4 x[kWarps];
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        x[w] = st[w * kState + (kAcc / 4 + i) * 32 + lane];
+        top[2 * i] = fmaxf(top[2 * i], x[w].x);
+        top[2 * i + 1] = fmaxf(top[2 * i + 1], x[w].y);
+      }
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        c[w][2 * i] = x[w].x == -INFINITY ? 0.f : tc::ex2(x[w].x - top[2 * i]);
+        c[w][2 * i + 1] = x[w].y == -INFINITY ? 0.f : tc::ex2(x[w].y - top[2 * i + 1]);
+        inv[2 * i] = fmaf(x[w].z, c[w][2 * i], inv[2 * i]);
+        inv[2 * i + 1] = fmaf(x[w].w, c[w][2 * i + 1], inv[2 * i + 1]);
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) {
+      if ((lane & 3) == 0) g((lane >> 2) + 8 * r, inv[r] > 0.f ? top[r] + tc::lg2(inv[r]) : -INFINITY);
+      inv[r] = inv[r] > 0.f ? 1.f / inv[r] : 0.f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) c[w][r] *= inv[r];
+    }
+#pragma unroll
+    for (int i = 0; i < kAcc / 4; ++i) {
+      const int r = 2 * (i / NT), n = i % NT;
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float4 x = st[w * kState + i * 32 + lane];
+        o.x = fmaf(x.x, c[w][r], o.x);
+        o.y = fmaf(x.y, c[w][r], o.y);
+        o.z = fmaf(x.z, c[w][r + 1], o.z);
+        o.w = fmaf(x.w, c[w][r + 1], o.w);
+      }
+      const float a0[2] = {o.x, o.y}, a1[2] = {o.z, o.w};
+      f.template operator()<2>((lane >> 2) + 8 * r, 8 * n + 2 * (lane & 3), a0);
+      f.template operator()<2>((lane >> 2) + 8 * (r + 1), 8 * n + 2 * (lane & 3), a1);
+    }
+  }
+  __device__ __forceinline__ void leave(float4* st, int warp, int lane) const {
+    float4* x = st + warp * kState + lane;
+#pragma unroll
+    for (int i = 0; i < kAcc / 4; ++i) x[i * 32] = make_float4(acc[4 * i], acc[4 * i + 1], acc[4 * i + 2], acc[4 * i + 3]);
+#pragma unroll
+    for (int i = 0; i < kRows / 2; ++i)
+      x[(kAcc / 4 + i) * 32] = make_float4(m[2 * i], m[2 * i + 1], l[2 * i], l[2 * i + 1]);
   }
 };
 
@@ -272,19 +330,22 @@ struct SliceBf16 {
 template <int D, int R>
 struct SliceF32 {
   using T = float;
-  static constexpr int kWarps = 4, kStages = 2;
-  static constexpr int kAcc = 4 * R, kRows = R;
-  static constexpr int kQStride = (D + 4) * 4;  // the second half of a row sits 16 bytes on: other banks
+  static constexpr int kWarps = 8, kKeys = 8, kStages = D == 128 ? 4 : 8;
+  static constexpr int kStageKeys = 4 * kKeys;
+  static constexpr int kAcc = 4 * R;
+  static constexpr int kQStride = (D + 16) * 4;  // each quarter of a row sits 16 bytes on: other banks
   static constexpr int kQBytes = R * kQStride;
-  static constexpr int kScratch = kKeys * R * 4;  // P of a warp's slice
+  static constexpr int kScratch = kKeys * R * 4;  // P of a worker's slice
+  static constexpr int kState = kAcc / 4 * 32 + R / 2;  // float4s of a worker's state; m and l are the same in every lane
+  static constexpr int kPieces = D == 128 ? 2 : 4;      // pieces that the scheduler is ahead (their Q fills the rest of shared memory)
   float acc[kAcc];
   float m[R], l[R];
   int32_t pos0, row0, kv;
 
-  static __device__ __forceinline__ uint32_t at(int r, int c) { return uint32_t(r * D * 4 + ((c ^ (r & 7)) << 4)); }
-  static __device__ __forceinline__ uint32_t q_at(int r, int c) {
-    return uint32_t(r * kQStride + ((c + (c >= D / 8 ? 1 : 0)) << 4));
+  static __device__ __forceinline__ uint32_t at(int r, int c) {
+    return uint32_t((c >> 3) * (kStageKeys * 128) + r * 128 + (((c ^ r) & 7) << 4));
   }
+  static __device__ __forceinline__ uint32_t q_at(int r, int c) { return uint32_t(r * kQStride + ((c + c / (D / 16)) << 4)); }
   static __device__ __forceinline__ float4 lds4(uint32_t addr) {
     float4 v;
     asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
@@ -307,19 +368,19 @@ struct SliceF32 {
     kv = p.kv;
   }
 
-  __device__ __forceinline__ void slice(const PagedArgs& a, uint32_t sq, uint32_t sk, uint32_t sv, float* sp, int key,
-                                        bool full, int lane) {
-    const int kx = lane & 15, half = lane >> 4;
+  __device__ __forceinline__ void slice(const PagedArgs& a, uint32_t sq, uint32_t sk, uint32_t sv, int srow, float* sp,
+                                        int key, bool full, int klo, int khi, int lane) {
+    const int kx = lane & 7, quarter = lane >> 3;
     float s[R];
 #pragma unroll
     for (int r = 0; r < R; ++r) s[r] = 0.f;
-#pragma unroll 4
-    for (int c0 = 0; c0 < D / 8; ++c0) {
-      const int c = half * (D / 8) + c0;
-      const float4 k = lds4(sk + at(kx, c));
+#pragma unroll
+    for (int c0 = 0; c0 < D / 16; ++c0) {
+      const int c = quarter * (D / 16) + c0;
+      const float4 k = lds4(sk + at(srow + kx, c));
 #pragma unroll
       for (int r = 0; r < R; ++r) {
-        const float4 q = lds4(sq + uint32_t(r * kQStride + ((c + half) << 4)));
+        const float4 q = lds4(sq + uint32_t(r * kQStride + ((c + quarter) << 4)));
         s[r] = fmaf(q.x, k.x, s[r]);
         s[r] = fmaf(q.y, k.y, s[r]);
         s[r] = fmaf(q.z, k.z, s[r]);
@@ -331,6 +392,7 @@ struct SliceF32 {
     float up[R];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
+      s[r] += __shfl_xor_sync(0xffffffffu, s[r], 8);
       s[r] += __shfl_xor_sync(0xffffffffu, s[r], 16);
       if (!full) {
         const int pos = pos0 + (row0 + r) / a.G;
@@ -339,7 +401,7 @@ struct SliceF32 {
       }
       float v = s[r];
 #pragma unroll
-      for (int o = 1; o < 16; o <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+      for (int o = 1; o < 8; o <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
       up[r] = v * a.scale_log2;
       grow |= up[r] > m[r] + 8.f;
     }
@@ -358,21 +420,22 @@ struct SliceF32 {
     for (int r = 0; r < R; ++r) {
       const float base = m[r] == -INFINITY ? 0.f : m[r];
       s[r] = exp2f(fmaf(s[r], a.scale_log2, -base));
-      if (half == 0) l[r] += s[r];
+      l[r] += s[r];  // four lanes of a key hold the same
     }
-    if (half == 0) {
+    // the four lanes of a key store a quarter of its rows each
 #pragma unroll
-      for (int r = 0; r < R; r += 4)
+    for (int r = 0; r < R; r += 4)
+      if ((r / 4) % 4 == quarter || R == 4)
         *reinterpret_cast<float4*>(sp + kx * R + r) = make_float4(s[r], s[r + 1], s[r + 2], s[r + 3]);
-    }
     __syncwarp();
     // head_dim 128: 32 lanes x 4 columns; 64: 16 lanes x 4 columns, each half of the warp half of the keys
     constexpr int kn = D == 128 ? kKeys : kKeys / 2;
-    const int c = D == 128 ? lane : kx;
-#pragma unroll 4
+    const int c = D == 128 ? lane : lane & 15;
+#pragma unroll
     for (int i = 0; i < kn; ++i) {
-      const int x = D == 128 ? i : half * kn + i;
-      const float4 v = lds4(sv + at(x, c));
+      const int x = D == 128 ? i : (lane >> 4) * kn + i;
+      float4 v = lds4(sv + at(srow + x, c));
+      if (!full && (key + x < klo || key + x >= khi)) v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int r = 0; r < R; r += 4) {
         const float4 p = *reinterpret_cast<const float4*>(sp + x * R + r);
@@ -391,22 +454,68 @@ struct SliceF32 {
 
   __device__ __forceinline__ void end() {
 #pragma unroll
-    for (int r = 0; r < R; ++r) l[r] = warp_sum(l[r]);
+    for (int r = 0; r < R; ++r) {
+#pragma unroll
+      for (int o = 1; o < 8; o <<= 1) l[r] += __shfl_xor_sync(0xffffffffu, l[r], o);
+    }
     if (D == 64) {
 #pragma unroll
       for (int i = 0; i < kAcc; ++i) acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], 16);
     }
   }
-  static __device__ __forceinline__ int row_of(int i) { return i >> 2; }
 
   template <typename FO, typename FL>
-  __device__ __forceinline__ void write(int lane, FO f, FL g) {
+  static __device__ __forceinline__ void join(const float4* st, int lane, FO f, FL g) {
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-      const float inv = l[r] > 0.f ? 1.f / l[r] : 0.f;
-      const float x[4] = {acc[4 * r] * inv, acc[4 * r + 1] * inv, acc[4 * r + 2] * inv, acc[4 * r + 3] * inv};
-      if (4 * lane < D) f.template operator()<4>(r, 4 * lane, x);
-      if (lane == 0) g(r, l[r] > 0.f ? m[r] + log2f(l[r]) : -INFINITY);
+    for (int i = 0; i < R / 2; ++i) {  // rows 2 i, 2 i + 1
+      float4 x[kWarps];
+      float t0 = -INFINITY, t1 = -INFINITY, l0 = 0.f, l1 = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        x[w] = st[w * kState + kAcc / 4 * 32 + i];
+        t0 = fmaxf(t0, x[w].x);
+        t1 = fmaxf(t1, x[w].y);
+      }
+      float o0[4] = {}, o1[4] = {};
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float c0 = x[w].x == -INFINITY ? 0.f : exp2f(x[w].x - t0);
+        const float c1 = x[w].y == -INFINITY ? 0.f : exp2f(x[w].y - t1);
+        l0 = fmaf(x[w].z, c0, l0);
+        l1 = fmaf(x[w].w, c1, l1);
+        const float4 y = st[w * kState + (2 * i) * 32 + lane], z = st[w * kState + (2 * i + 1) * 32 + lane];
+        o0[0] = fmaf(y.x, c0, o0[0]);
+        o0[1] = fmaf(y.y, c0, o0[1]);
+        o0[2] = fmaf(y.z, c0, o0[2]);
+        o0[3] = fmaf(y.w, c0, o0[3]);
+        o1[0] = fmaf(z.x, c1, o1[0]);
+        o1[1] = fmaf(z.y, c1, o1[1]);
+        o1[2] = fmaf(z.z, c1, o1[2]);
+        o1[3] = fmaf(z.w, c1, o1[3]);
+      }
+      const float v0 = l0 > 0.f ? 1.f / l0 : 0.f, v1 = l1 > 0.f ? 1.f / l1 : 0.f;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        o0[e] *= v0;
+        o1[e] *= v1;
+      }
+      if (4 * lane < D) {
+        f.template operator()<4>(2 * i, 4 * lane, o0);
+        f.template operator()<4>(2 * i + 1, 4 * lane, o1);
+      }
+      if (lane == 0) {
+        g(2 * i, l0 > 0.f ? t0 + log2f(l0) : -INFINITY);
+        g(2 * i + 1, l1 > 0.f ? t1 + log2f(l1) : -INFINITY);
+      }
+    }
+  }
+  __device__ __forceinline__ void leave(float4* st, int warp, int lane) const {
+    float4* x = st + warp * kState + lane;
+#pragma unroll
+    for (int i = 0; i < kAcc / 4; ++i) x[i * 32] = make_float4(acc[4 * i], acc[4 * i + 1], acc[4 * i + 2], acc[4 * i + 3]);
+    if (lane == 0) {
+#pragma unroll
+      for (int i = 0; i < R / 2; ++i) x[kAcc / 4 * 32 + i] = make_float4(m[2 * i], m[2 * i + 1], l[2 * i], l[2 * i + 1]);
     }
   }
 };
@@ -433,221 +542,214 @@ struct SliceOut {
 
 template <typename S, int D, int R>
 struct SliceLayout {
-  static constexpr int kStageBytes = 2 * kKeys * D * int(sizeof(typename S::T));
+  static constexpr int kStageBytes = 2 * S::kStageKeys * D * int(sizeof(typename S::T));
   static constexpr int kOffRing = 0;
-  static constexpr int kOffJoin = kOffRing + S::kWarps * S::kStages * kStageBytes;
-  static constexpr int kJoinBytes = 32 * (S::kAcc + 2 * S::kRows) * 4;  // one warp's state
-  static constexpr int kOffQ = kOffJoin + (S::kWarps / 2) * kJoinBytes;
+  static constexpr int kOffState = kOffRing + S::kStages * kStageBytes;
+  static constexpr int kStateBytes = S::kState * 16;  // one worker's
+  static constexpr int kOffQ = kOffState + S::kWarps * kStateBytes;
   static constexpr int kQBytes = (S::kQBytes + 127) & ~127;
-  static constexpr int kOffP = kOffQ + 2 * kQBytes;
+  static constexpr int kOffP = kOffQ + S::kPieces * kQBytes;
   static constexpr int kBytes = kOffP + S::kWarps * S::kScratch;
+  static constexpr int kThreads = (S::kWarps + 2) * 32;
   static_assert(kBytes + 2048 <= 232448, "shared memory of one block");
 };
 
+struct SliceParams {
+  CUtensorMap tmk, tmv;  // the cache (make_tmap_pages)
+  PagedArgs a;
+  int32_t box_shift;     // log2 keys of a box
+  int32_t head_inner;    // the head dimension comes before the token dimension
+};
+
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int c0, int c1, int c2,
+                                            int c3) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar)
+      : "memory");
+}
+
 template <typename S, int D, int R>
-__global__ void __launch_bounds__(S::kWarps * 32, 1) paged_slice_kernel(const __grid_constant__ PagedArgs a) {
+__global__ void __launch_bounds__(SliceLayout<S, D, R>::kThreads, 1)
+    paged_slice_kernel(const __grid_constant__ SliceParams sp) {
   using T = typename S::T;
   using L = SliceLayout<S, D, R>;
-  constexpr int W = S::kWarps, NS = S::kStages, kThreads = W * 32;
-  constexpr int V = 16 / int(sizeof(T));   // elements of a copy
-  constexpr int CH = D / V;                // copies of a row
-  constexpr int KPI = 32 / CH > 0 ? 32 / CH : 1;  // keys of one step of a warp's copies
-  static_assert(CH <= 32, "a row fits a warp's copies");
+  constexpr int W = S::kWarps, NS = S::kStages, kKeys = S::kKeys, SK = S::kStageKeys, kPieces = S::kPieces;
+  constexpr int V = 16 / int(sizeof(T));           // elements of a Q copy
+  constexpr int CH = D / V;                        // Q copies of a row
+  constexpr int CB = D * int(sizeof(T)) / 128;     // 128-byte columns of a row
+  static_assert(NS % 2 == 0, "a worker's stages keep their slots");
   extern __shared__ __align__(1024) uint8_t smem[];
   __shared__ int64_t s_scan[34];
   __shared__ PagedStart s_start[2];
-  __shared__ PieceInfo s_piece[4];
-  __shared__ PagedWalk<kSliceUnit, kSliceExtra> s_walk;
+  __shared__ PieceInfo s_piece[kPieces];
+  // piece published, its Q landed, its states joined (per entry); stage landed, stage read; all workers' states left
+  __shared__ uint64_t s_bar[3 * kPieces + 2 * NS + 1];
+  __shared__ int s_abort;
+  const PagedArgs& a = sp.a;
   const uint32_t sbase = tc::smem_u32(smem);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  auto bar_piece = [&](int k) { return tc::smem_u32(s_bar + (k % kPieces)); };
+  auto bar_q = [&](int k) { return tc::smem_u32(s_bar + kPieces + (k % kPieces)); };
+  auto bar_joined = [&](int k) { return tc::smem_u32(s_bar + 2 * kPieces + (k % kPieces)); };
+  auto bar_full = [&](uint32_t g) { return tc::smem_u32(s_bar + 3 * kPieces + g % NS); };
+  auto bar_empty = [&](uint32_t g) { return tc::smem_u32(s_bar + 3 * kPieces + NS + g % NS); };
+  const uint32_t bar_state = tc::smem_u32(s_bar + 3 * kPieces + 2 * NS);
+  auto phase = [](int k) { return uint32_t(k / kPieces) & 1u; };
+  // whole-warp bounded wait; false: some wait of the block gave up
+  auto wait = [&](uint32_t bar, uint32_t parity) -> bool {
+    return __all_sync(0xffffffffu, tc::mbar_wait(bar, parity, &s_abort, a.err));
+  };
+  if (sbase & 1023) {  // the swizzled layouts need a 1 KB aligned base
+    if (tid == 0 && a.err) atomicCAS(a.err, 0, 2);
+    return;
+  }
 
   grid_launch_dependents();
-  int64_t u0, u1;
-  {
-    const int64_t total = paged_locate<kSliceUnit, kSliceExtra, kThreads>(a, s_scan, s_start, [&](int64_t t, int k) {
-      return k == 0 ? paged_first_unit(t, blockIdx.x, a.grid) : t;
-    });
-    u0 = paged_first_unit(total, blockIdx.x, a.grid);
-    u1 = paged_first_unit(total, blockIdx.x + 1, a.grid);
+  if (tid == 0) {
+    for (int i = 0; i < 3 * kPieces; ++i) tc::mbar_init(tc::smem_u32(s_bar + i), i / kPieces == 1 ? 32 : 1);
+    for (int i = 0; i < NS; ++i) {
+      tc::mbar_init(bar_full(i), 1);
+      tc::mbar_init(bar_empty(i), W / 2);
+    }
+    tc::mbar_init(bar_state, W);
+    s_abort = 0;
+    tc::fence_mbar_init();
+    tc::prefetch_tmap(&sp.tmk);
+    tc::prefetch_tmap(&sp.tmv);
   }
+  const int64_t total = paged_locate<kSliceUnit, kSliceExtra, L::kThreads>(
+      a, s_scan, s_start, [&](int64_t t, int k) { return k == 0 ? paged_first_unit(t, blockIdx.x, a.grid) : t; });
+  const int64_t u0 = paged_first_unit(total, blockIdx.x, a.grid), u1 = paged_first_unit(total, blockIdx.x + 1, a.grid);
   if (u1 <= u0) return;
 
-  // ---- this warp's copies: a walk of its own, ahead of the products ----
-  PagedWalk<kSliceUnit, kSliceExtra> wp;
-  wp.start(a, s_start[0], u1 - u0, blockIdx.x);
-  int32_t p_r = 0, p_h = 0, p_key0 = 0, p_n = 0, p_s = 0, p_lo = 0, p_hi = 0;
-  bool more = true;
-  int32_t pg[2] = {-1, -1};
-  auto look_up = [&]() {  // the pages of the slice that is copied next
-    const int32_t key = p_key0 + p_s * kKeys;
-    const int32_t* row = a.table + int64_t(p_r) * a.max_blocks;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int32_t k8 = key + 8 * i;
-      pg[i] = k8 < p_hi && k8 + 8 > p_lo ? row[k8 >> a.page_shift] : -1;
-    }
-  };
-  auto advance = [&](int step) {
-    p_s += step;
-    while (p_s >= p_n) {
+  if (warp == W + 1) {
+    // ---------------------------------------------------------- producer --
+    PagedWalk<kSliceUnit, kSliceExtra> walk;
+    walk.start(a, s_start[0], u1 - u0, blockIdx.x);
+    const int bs = sp.box_shift, box = 1 << bs;
+    uint32_t g = 0;
+    bool ok = true;
+    for (int k = 0; ok; ++k) {
       PagedPiece p;
-      if (!wp.next(a, p)) {
-        more = false;
-        return;
+      PieceInfo i;
+      i.valid = 0;
+      i.nrows = 0;
+      if (walk.next(a, p)) i = piece_info<SK>(a, p);
+      // page of the box that lane l < 8 (16 for K, V) loads in the stage of key0: n_pages where no row sees a key of it
+      auto seen = [&](int key) { return key < i.hi && key + box > i.lo; };
+      const int sub = (lane & 15) / CB, col = (lane & 15) % CB;  // this lane's box: K on lanes 0 .. 15, V on 16 .. 31
+      const bool mine = (sub << bs) < SK;
+      auto page = [&](int key0) -> int32_t {
+        const int key = key0 + (sub << bs);
+        return mine && seen(key) ? a.table[int64_t(p.r) * a.max_blocks + (key >> a.page_shift)] : a.n_pages;
+      };
+      int32_t pg = i.valid && i.n > 0 ? page(i.key0) : a.n_pages;
+      if (k >= kPieces && !wait(bar_joined(k), phase(k) ^ 1)) break;
+      if (lane == 0) {
+        s_piece[k % kPieces] = i;
+        tc::mbar_arrive(bar_piece(k));
       }
-      slices_of(p, p_key0, p_n);
-      p_r = p.r;
-      p_h = p.h;
-      p_lo = p.tile.lo;
-      p_hi = p.tile.hi;
-      p_s = warp;
-    }
-    look_up();
-  };
-  uint32_t issued = 0;
-  auto issue = [&]() {
-    if (more) {
-      const uint32_t dst = sbase + L::kOffRing + (warp * NS + issued % NS) * L::kStageBytes;
-      const int32_t key = p_key0 + p_s * kKeys;
-      const int ck = lane % CH;
-#pragma unroll
-      for (int i = 0; i < kKeys / KPI; ++i) {
-        const int kx = i * KPI + lane / CH;
-        const int32_t j = key + kx;
-        const int32_t page = kx < 8 ? pg[0] : pg[1];
-        const bool wanted = j >= p_lo && j < p_hi;
-        const bool ok = wanted && uint32_t(page) < uint32_t(a.n_pages);
-        if (wanted && !ok && a.err) atomicCAS(a.err, 0, kErrBadPage);
-        const int64_t off = ok ? page * a.page_stride + int64_t(j & ((1 << a.page_shift) - 1)) * a.token_stride +
-                                     p_h * a.head_stride + ck * V
-                               : 0;
-        cp_async16(dst + S::at(kx, ck), static_cast<const T*>(a.k) + off, ok);
-        cp_async16(dst + L::kStageBytes / 2 + S::at(kx, ck), static_cast<const T*>(a.v) + off, ok);
+      if (!i.valid) break;
+      for (int e = lane; e < R * CH; e += 32) {  // Q, zeros behind the tile's rows
+        const int r = e / CH, c = e % CH, row = i.row0 + r;
+        const bool in = r < i.nrows;
+        const int64_t off = in ? int64_t(i.q0 + row / a.G) * a.q_stride + int64_t(i.h * a.G + row % a.G) * D + c * V : 0;
+        cp_async16(sbase + L::kOffQ + (k % kPieces) * L::kQBytes + S::q_at(r, c), static_cast<const T*>(a.q) + off, in);
       }
-      advance(W);
-    }
-    cp_async_commit();
-    ++issued;
-  };
-  p_s = warp;  // p_n = 0: the first advance takes the first piece
-  advance(0);
-#pragma unroll
-  for (int i = 0; i < NS; ++i) issue();
-
-  // ---- pieces: one thread walks, two ahead ----
-  auto walk = [&](int k) {
-    PagedPiece p;
-    PieceInfo i;
-    i.valid = 0;
-    if (s_walk.next(a, p)) i = piece_info(a, p);
-    s_piece[k & 3] = i;
-  };
-  // Q of a tile, 16 bytes per thread and step, zeros behind its rows
-  constexpr int kQSteps = (R * CH + kThreads - 1) / kThreads;
-  uint4 qv[kQSteps];
-  auto load_q = [&](const PieceInfo& p) {
-#pragma unroll
-    for (int i = 0; i < kQSteps; ++i) {
-      const int e = tid + i * kThreads, r = e / CH, c = e % CH;
-      qv[i] = make_uint4(0, 0, 0, 0);
-      if (p.valid && r < R && r < p.nrows) {
-        const int row = p.row0 + r;
-        qv[i] = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) + int64_t(p.q0 + row / a.G) * a.q_stride +
-                                                int64_t(p.h * a.G + row % a.G) * D + c * V);
+      asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar_q(k)) : "memory");
+      for (int t = 0; t < i.n; ++t, ++g) {
+        const int key0 = i.key0 + t * SK;
+        const int32_t now = pg;
+        if (t + 1 < i.n) pg = page(key0 + SK);
+        ok = wait(bar_empty(g), ((g / NS) & 1) ^ 1);
+        if (!ok) break;
+        if (lane == 0) tc::mbar_arrive_expect_tx(bar_full(g), L::kStageBytes);
+        __syncwarp();
+        if (mine) {
+          const int key = key0 + (sub << bs);
+          int32_t at = now;
+          if (uint32_t(at) >= uint32_t(a.n_pages)) {
+            if (seen(key) && a.err) atomicCAS(a.err, 0, kErrBadPage);
+            at = a.n_pages;
+          }
+          const int token = key & ((1 << a.page_shift) - 1);
+          const uint32_t dst = sbase + L::kOffRing + (g % NS) * L::kStageBytes +
+                               (lane < 16 ? 0 : L::kStageBytes / 2) + col * (SK * 128) + ((sub << bs) * 128);
+          const CUtensorMap* map = lane < 16 ? &sp.tmk : &sp.tmv;
+          tma_load_4d(dst, map, bar_full(g), col * (128 / int(sizeof(T))), sp.head_inner ? i.h : token,
+                      sp.head_inner ? token : i.h, at);
+        }
       }
     }
-  };
-  auto store_q = [&](int k) {
-#pragma unroll
-    for (int i = 0; i < kQSteps; ++i) {
-      const int e = tid + i * kThreads, r = e / CH, c = e % CH;
-      if (r < R) *reinterpret_cast<uint4*>(smem + L::kOffQ + (k & 1) * L::kQBytes + S::q_at(r, c)) = qv[i];
+    // Every copy has landed before the block ends (the workers wait for theirs
+    // unless a wait gave up).
+    if (!ok && lane == 0) {
+      volatile int never = 0;
+      for (uint32_t s = g > uint32_t(NS) ? g - NS : 0; s < g; ++s) tc::mbar_wait(bar_full(s), (s / NS) & 1, &never, nullptr);
     }
-  };
-  if (tid == 0) {
-    s_walk.start(a, s_start[0], u1 - u0, blockIdx.x);
-    walk(0);
-    walk(1);
+    cp_async_wait<0>();
+    return;
   }
-  __syncthreads();
-  load_q(s_piece[0]);
-  store_q(0);
-  __syncthreads();
 
-  float* join = reinterpret_cast<float*>(smem + L::kOffJoin);
-  constexpr int kState = S::kAcc + 2 * S::kRows;
-  float* sp = reinterpret_cast<float*>(smem + L::kOffP + warp * S::kScratch);
-  uint32_t used = 0;
-  S st;
-  for (int k = 0;; ++k) {
-    const PieceInfo& p = s_piece[k & 3];
-    if (!p.valid) break;
-    load_q(s_piece[(k + 1) & 3]);
-    if (tid == kThreads - 32) walk(k + 2);
-    const uint32_t sq = sbase + L::kOffQ + (k & 1) * L::kQBytes;
-    st.begin(a, p, sq, lane);
-    const int key0 = p.key0, n = p.n, full_lo = p.full_lo, full_hi = p.full_hi;
-    for (int s = warp; s < n; s += W) {
-      cp_async_wait<NS - 1>();
-      __syncwarp();
-      const uint32_t sk = sbase + L::kOffRing + (warp * NS + used % NS) * L::kStageBytes;
-      const int key = key0 + s * kKeys;
-      st.slice(a, sq, sk, sk + L::kStageBytes / 2, sp, key, key >= full_lo && key + kKeys <= full_hi, lane);
-      __syncwarp();
-      ++used;
-      issue();
-    }
-    st.end();
-    // ---- the warps' states join pairwise; a writer's region was last read by itself ----
-    __syncthreads();
-#pragma unroll
-    for (int half = W / 2; half >= 1; half >>= 1) {
-      if (warp >= half && warp < 2 * half) {
-        float* x = join + (half == W / 2 ? warp - half : warp) * (L::kJoinBytes / 4) + lane;
-#pragma unroll
-        for (int i = 0; i < S::kAcc; ++i) x[i * 32] = st.acc[i];
-#pragma unroll
-        for (int r = 0; r < S::kRows; ++r) {
-          x[(S::kAcc + r) * 32] = st.m[r];
-          x[(S::kAcc + S::kRows + r) * 32] = st.l[r];
-        }
-      }
-      if (half == W / 2) store_q(k + 1);
-      __syncthreads();
-      if (warp < half) {
-        const float* x = join + (half == W / 2 ? warp : warp + half) * (L::kJoinBytes / 4) + lane;
-        float c0[S::kRows], c1[S::kRows];
-#pragma unroll
-        for (int r = 0; r < S::kRows; ++r) {
-          const float mo = x[(S::kAcc + r) * 32], lo = x[(S::kAcc + S::kRows + r) * 32];
-          const float t = fmaxf(st.m[r], mo);
-          c0[r] = st.m[r] == -INFINITY ? 0.f : exp2f(st.m[r] - t);
-          c1[r] = mo == -INFINITY ? 0.f : exp2f(mo - t);
-          st.m[r] = t;
-          st.l[r] = st.l[r] * c0[r] + lo * c1[r];
-        }
-#pragma unroll
-        for (int i = 0; i < S::kAcc; ++i) {
-          const int r = S::row_of(i);
-          st.acc[i] = st.acc[i] * c0[r] + x[i * 32] * c1[r];
-        }
-      }
-    }
-    if (warp == 0) {
-      const int G = a.G, slot = p.slot, nrows = p.nrows;
-      const int64_t q0 = p.q0;
-      const int row0 = p.row0, h0 = p.h * G;
-      const SliceOut<T, D, R> out{a, slot, nrows, G, row0, h0, q0};
-      st.write(lane, out, [&](int r, float v) {
+  float4* states = reinterpret_cast<float4*>(smem + L::kOffState);
+  if (warp == W) {
+    // ------------------------------------------------------------ joiner --
+    for (int k = 0;; ++k) {
+      if (!wait(bar_piece(k), phase(k))) break;
+      const PieceInfo& p = s_piece[k % kPieces];
+      if (!p.valid) break;
+      const int nrows = p.nrows, slot = p.slot;
+      const SliceOut<T, D, R> out{a, slot, nrows, a.G, p.row0, p.h * a.G, p.q0};
+      if (!wait(bar_state, uint32_t(k) & 1u)) break;
+      S::join(states, lane, out, [&](int r, float v) {
         if (r >= nrows) return;
         if (slot < 0)
           a.lse[out.row(r)] = v * 0.69314718055994531f;
         else
           a.part_l[int64_t(slot) * R + r] = v;
       });
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(bar_joined(k));
     }
+    return;
   }
-  cp_async_wait<0>();
+
+  // -------------------------------------------------------------- worker --
+  float* scratch = reinterpret_cast<float*>(smem + L::kOffP + warp * S::kScratch);
+  const int srow = (warp & 3) * kKeys;
+  uint32_t g = 0;
+  bool ok = true;
+  S st;
+  for (int k = 0; ok; ++k) {
+    if (!wait(bar_piece(k), phase(k))) break;
+    const PieceInfo& p = s_piece[k % kPieces];
+    if (!p.valid) break;
+    if (!wait(bar_q(k), phase(k))) break;
+    const uint32_t sq = sbase + L::kOffQ + (k % kPieces) * L::kQBytes;
+    st.begin(a, p, sq, lane);
+    const int n = p.n, lo = p.lo, hi = p.hi, full_lo = p.full_lo, full_hi = p.full_hi;
+    int key = p.key0 + srow;
+    for (int t = 0; t < n; ++t, ++g, key += SK) {
+      if (int(g & 1) != (warp >> 2)) continue;  // the other four workers' stage
+      ok = wait(bar_full(g), (g / NS) & 1);
+      if (!ok) break;
+      const uint32_t sk = sbase + L::kOffRing + (g % NS) * L::kStageBytes;
+      if (key < hi && key + kKeys > lo)
+        st.slice(a, sq, sk, sk + L::kStageBytes / 2, srow, scratch, key, key >= full_lo && key + kKeys <= full_hi, lo,
+                 hi, lane);
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(bar_empty(g));
+    }
+    if (!ok) break;
+    st.end();
+    // the state's place is free once the piece before it is joined
+    if (k > 0 && !wait(bar_joined(k - 1), phase(k - 1))) break;
+    st.leave(states, warp, lane);
+    __syncwarp();
+    if (lane == 0) tc::mbar_arrive(bar_state);
+  }
 }
 
 // ---------------------------------------------------------------- merge ---
@@ -733,7 +835,14 @@ cp_status run_slice(const PagedArgs& a, cudaStream_t s) {
       return CP_ERR_CUDA;
     ready[dev].store(true, std::memory_order_release);
   }
-  kern<<<unsigned(a.grid), S::kWarps * 32, L::kBytes, s>>>(a);
+  SliceParams p;
+  const int page = 1 << a.page_shift, box = page < S::kStageKeys ? page : S::kStageKeys;
+  p.head_inner = a.head_stride <= a.token_stride;
+  if (!make_tmap_pages(&p.tmk, a.k, a, box) || !make_tmap_pages(&p.tmv, a.v, a, box)) return CP_ERR_CUDA;
+  p.a = a;
+  p.box_shift = 0;
+  while ((1 << p.box_shift) < box) ++p.box_shift;
+  kern<<<unsigned(a.grid), L::kThreads, L::kBytes, s>>>(p);
   return cuda_status(cudaGetLastError());
 }
 
@@ -761,7 +870,7 @@ cp_status launch_paged_slice(const PagedArgs& a, PagedKernel k, cudaStream_t s) 
     if (k == kPagedSlice16)
       return a.d == 128 ? run_slice<SliceBf16<128, 16>, 128, 16>(a, s) : run_slice<SliceBf16<64, 16>, 64, 16>(a, s);
     if (k == kPagedSlice32)
-      return a.d == 128 ? run_slice<SliceBf16<128, 32>, 128, 32>(a, s) : run_slice<SliceBf16<64, 32>, 64, 32>(a, s);
+      return a.d == 64 ? run_slice<SliceBf16<64, 32>, 64, 32>(a, s) : CP_ERR_UNSUPPORTED;
     return CP_ERR_UNSUPPORTED;
   }
   if (k == kPagedSlice4)

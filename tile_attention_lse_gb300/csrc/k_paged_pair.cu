@@ -31,6 +31,7 @@
 #include "internal.h"
 #include "pair_util.cuh"
 #include "paged_dev.cuh"
+#include "paged_tmap.h"
 #include "tc_util.cuh"
 #include "tmap.h"
 
@@ -597,25 +598,6 @@ __global__ void __launch_bounds__(kThreads, 1) paged_pair_kernel(const __grid_co
   if (warp == 1) tc::tmem_dealloc_pair(tmem, 512);
 }
 
-// Map of a cache: token and head dimensions in ascending order of stride,
-// box of 64 columns, one head and `box` tokens of one page.
-bool make_tmap_pages(CUtensorMap* map, const void* base, const PagedArgs& a, int box, bool head_inner) {
-  auto enc = tmap_encoder();
-  if (!enc) return false;
-  const cuuint64_t page = cuuint64_t(1) << a.page_shift;
-  const cuuint64_t dims[4] = {128, head_inner ? cuuint64_t(a.Hkv) : page, head_inner ? page : cuuint64_t(a.Hkv),
-                              cuuint64_t(a.n_pages)};
-  const cuuint64_t hs = cuuint64_t(a.head_stride) * 2, ts = cuuint64_t(a.token_stride) * 2;
-  cuuint64_t ps = cuuint64_t(a.page_stride) * 2;
-  if (a.n_pages == 1 && ps == 0) ps = page * ts;
-  const cuuint64_t strides[3] = {head_inner ? hs : ts, head_inner ? ts : hs, ps};
-  const cuuint32_t b[4] = {64, head_inner ? 1u : cuuint32_t(box), head_inner ? cuuint32_t(box) : 1u, 1};
-  const cuuint32_t es[4] = {1, 1, 1, 1};
-  return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, b, es,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 // Map of q: box of 64 columns, the G heads of a kv-head and `tokens` rows.
 bool make_tmap_packed(CUtensorMap* map, const PagedArgs& a, int tokens) {
   auto enc = tmap_encoder();
@@ -677,14 +659,13 @@ cp_status launch_paged_pair(const PagedArgs& a, cudaStream_t s) {
   if (a.dtype != CP_BF16 || a.d != 128 || a.G > kPairRows) return CP_ERR_UNSUPPORTED;
   Params p;
   const int page = 1 << a.page_shift, box = page < 64 ? page : 64;
-  const bool head_inner = a.head_stride <= a.token_stride;
-  if (!make_tmap_packed(&p.tmq, a, kPairRows / a.G) || !make_tmap_pages(&p.tmk, a.k, a, box, head_inner) ||
-      !make_tmap_pages(&p.tmv, a.v, a, box, head_inner))
+  if (!make_tmap_packed(&p.tmq, a, kPairRows / a.G) || !make_tmap_pages(&p.tmk, a.k, a, box) ||
+      !make_tmap_pages(&p.tmv, a.v, a, box))
     return CP_ERR_CUDA;
   p.a = a;
   p.box_shift = 0;
   while ((1 << p.box_shift) < box) ++p.box_shift;
-  p.head_inner = head_inner;
+  p.head_inner = a.head_stride <= a.token_stride;
   p.wait_limit = wait_limit_cycles();
   cudaLaunchAttribute attr[1];
   const cudaLaunchConfig_t cfg = pair_config(attr, a.grid, s);

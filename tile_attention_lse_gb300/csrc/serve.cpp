@@ -76,7 +76,8 @@ PagedKernel pick_kernel(const cp_paged_desc& d) {
   const int64_t rows = d.max_new > 0 ? G * d.max_new : INT64_MAX;
   if (d.kv.dtype == CP_F32) return rows <= 4 ? kPagedSlice4 : kPagedSlice16;
   if (rows <= 16) return kPagedSlice16;
-  return d.kv.head_dim == 128 && G <= kPairRows ? kPagedPair : kPagedSlice32;
+  if (d.kv.head_dim == 64) return kPagedSlice32;
+  return G <= kPairRows ? kPagedPair : kPagedSlice16;
 }
 
 // Blocks (pairs of blocks) that a launch has at most.
