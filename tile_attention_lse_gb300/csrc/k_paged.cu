@@ -108,6 +108,35 @@ __device__ __forceinline__ PieceInfo piece_info(const PagedArgs& a, const PagedP
   return i;
 }
 
+// Where a row of a tile goes: the outputs, or its partial state.
+template <typename T, int D, int R>
+struct SliceOut {
+  T* o;         // final O, or
+  float* part;  // partial O
+  float* lse;
+  bool in, whole;
+  __device__ __forceinline__ SliceOut(const PagedArgs& a, const PieceInfo& p, int r) {
+    in = r < p.nrows;
+    whole = p.slot < 0;
+    const int x = p.row0 + r;
+    const int64_t row = int64_t(p.q0 + x / a.G) * a.H + p.h * a.G + x % a.G, prow = int64_t(p.slot) * R + r;
+    o = static_cast<T*>(a.o) + row * D;
+    part = a.part_o + prow * D;
+    lse = whole ? a.lse + row : a.part_l + prow;
+  }
+  template <int N>
+  __device__ __forceinline__ void put(int c, const float* x) const {
+    if (!in) return;
+    if (whole)
+      store_vec<T, N>(o + c, x);
+    else
+      store_vec<float, N>(part + c, x);
+  }
+  __device__ __forceinline__ void put_lse(float log2_sum) const {
+    if (in) *lse = whole ? log2_sum * 0.69314718055994531f : log2_sum;
+  }
+};
+
 // ------------------------------------------------- bf16: mma.sync tiles ---
 template <int D, int R>
 struct SliceBf16 {
@@ -264,56 +293,51 @@ struct SliceBf16 {
     }
   }
 
-  // Joins the workers' states at `st` (float4s [worker][kAcc / 4 + kRows / 2][lane]):
-  // f(row, column, two columns' values), g(row, log2 of the sum of 2^scores).
-  template <typename FO, typename FL>
-  static __device__ __forceinline__ void join(const float4* st, int lane, FO f, FL g) {
-    float c[kWarps][kRows], inv[kRows], top[kRows];
-#pragma unroll
-    for (int r = 0; r < kRows; ++r) {
-      top[r] = -INFINITY;
-      inv[r] = 0.f;
-    }
-    // a float4 of rows: m and l of rows 2 i, 2 i + 1
-#pragma unroll
-    for (int i = 0; i < kRows / 2; ++i) {
-      float4 x[kWarps];
+  // Joins the workers' states at `st` (float4s [worker][kAcc / 4 + kRows / 2][lane])
+  // and writes them out.  Loops stay loops: one warp runs this once per
+  // piece, and unrolled it waited for its own instructions (4 to 9 us a piece, 1 us so).
+  static __device__ __forceinline__ void join(const PagedArgs& a, const PieceInfo& p, const float4* st, int lane) {
+#pragma unroll 1
+    for (int i = 0; i < MT; ++i) {  // this lane's rows 8 * 2 i + lane / 4 and 8 further
+      const SliceOut<T, D, R> out0(a, p, (lane >> 2) + 16 * i), out1(a, p, (lane >> 2) + 16 * i + 8);
+      float c0[kWarps], c1[kWarps], t0 = -INFINITY, t1 = -INFINITY, l0 = 0.f, l1 = 0.f;
+      float4 x[kWarps];  // m and l of the two rows
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
         x[w] = st[w * kState + (kAcc / 4 + i) * 32 + lane];
-        top[2 * i] = fmaxf(top[2 * i], x[w].x);
-        top[2 * i + 1] = fmaxf(top[2 * i + 1], x[w].y);
+        t0 = fmaxf(t0, x[w].x);
+        t1 = fmaxf(t1, x[w].y);
       }
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
-        c[w][2 * i] = x[w].x == -INFINITY ? 0.f : tc::ex2(x[w].x - top[2 * i]);
-        c[w][2 * i + 1] = x[w].y == -INFINITY ? 0.f : tc::ex2(x[w].y - top[2 * i + 1]);
-        inv[2 * i] = fmaf(x[w].z, c[w][2 * i], inv[2 * i]);
-        inv[2 * i + 1] = fmaf(x[w].w, c[w][2 * i + 1], inv[2 * i + 1]);
+        c0[w] = x[w].x == -INFINITY ? 0.f : tc::ex2(x[w].x - t0);
+        c1[w] = x[w].y == -INFINITY ? 0.f : tc::ex2(x[w].y - t1);
+        l0 = fmaf(x[w].z, c0[w], l0);
+        l1 = fmaf(x[w].w, c1[w], l1);
       }
-    }
-#pragma unroll
-    for (int r = 0; r < kRows; ++r) {
-      if ((lane & 3) == 0) g((lane >> 2) + 8 * r, inv[r] > 0.f ? top[r] + tc::lg2(inv[r]) : -INFINITY);
-      inv[r] = inv[r] > 0.f ? 1.f / inv[r] : 0.f;
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) c[w][r] *= inv[r];
-    }
-#pragma unroll
-    for (int i = 0; i < kAcc / 4; ++i) {
-      const int r = 2 * (i / NT), n = i % NT;
-      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        const float4 x = st[w * kState + i * 32 + lane];
-        o.x = fmaf(x.x, c[w][r], o.x);
-        o.y = fmaf(x.y, c[w][r], o.y);
-        o.z = fmaf(x.z, c[w][r + 1], o.z);
-        o.w = fmaf(x.w, c[w][r + 1], o.w);
+      if ((lane & 3) == 0) {
+        out0.put_lse(l0 > 0.f ? t0 + tc::lg2(l0) : -INFINITY);
+        out1.put_lse(l1 > 0.f ? t1 + tc::lg2(l1) : -INFINITY);
       }
-      const float a0[2] = {o.x, o.y}, a1[2] = {o.z, o.w};
-      f.template operator()<2>((lane >> 2) + 8 * r, 8 * n + 2 * (lane & 3), a0);
-      f.template operator()<2>((lane >> 2) + 8 * (r + 1), 8 * n + 2 * (lane & 3), a1);
+      const float v0 = l0 > 0.f ? 1.f / l0 : 0.f, v1 = l1 > 0.f ? 1.f / l1 : 0.f;
+#pragma unroll 2
+      for (int n = 0; n < NT; ++n) {
+        float o0[2] = {}, o1[2] = {};
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+          const float4 y = st[w * kState + (i * NT + n) * 32 + lane];
+          o0[0] = fmaf(y.x, c0[w], o0[0]);
+          o0[1] = fmaf(y.y, c0[w], o0[1]);
+          o1[0] = fmaf(y.z, c1[w], o1[0]);
+          o1[1] = fmaf(y.w, c1[w], o1[1]);
+        }
+        o0[0] *= v0;
+        o0[1] *= v0;
+        o1[0] *= v1;
+        o1[1] *= v1;
+        out0.template put<2>(8 * n + 2 * (lane & 3), o0);
+        out1.template put<2>(8 * n + 2 * (lane & 3), o1);
+      }
     }
   }
   __device__ __forceinline__ void leave(float4* st, int warp, int lane) const {
@@ -464,10 +488,10 @@ struct SliceF32 {
     }
   }
 
-  template <typename FO, typename FL>
-  static __device__ __forceinline__ void join(const float4* st, int lane, FO f, FL g) {
-#pragma unroll
+  static __device__ __forceinline__ void join(const PagedArgs& a, const PieceInfo& p, const float4* st, int lane) {
+#pragma unroll 1
     for (int i = 0; i < R / 2; ++i) {  // rows 2 i, 2 i + 1
+      const SliceOut<T, D, R> out0(a, p, 2 * i), out1(a, p, 2 * i + 1);
       float4 x[kWarps];
       float t0 = -INFINITY, t1 = -INFINITY, l0 = 0.f, l1 = 0.f;
 #pragma unroll
@@ -500,12 +524,12 @@ struct SliceF32 {
         o1[e] *= v1;
       }
       if (4 * lane < D) {
-        f.template operator()<4>(2 * i, 4 * lane, o0);
-        f.template operator()<4>(2 * i + 1, 4 * lane, o1);
+        out0.template put<4>(4 * lane, o0);
+        out1.template put<4>(4 * lane, o1);
       }
       if (lane == 0) {
-        g(2 * i, l0 > 0.f ? t0 + log2f(l0) : -INFINITY);
-        g(2 * i + 1, l1 > 0.f ? t1 + log2f(l1) : -INFINITY);
+        out0.put_lse(l0 > 0.f ? t0 + log2f(l0) : -INFINITY);
+        out1.put_lse(l1 > 0.f ? t1 + log2f(l1) : -INFINITY);
       }
     }
   }
@@ -517,26 +541,6 @@ struct SliceF32 {
 #pragma unroll
       for (int i = 0; i < R / 2; ++i) x[kAcc / 4 * 32 + i] = make_float4(m[2 * i], m[2 * i + 1], l[2 * i], l[2 * i + 1]);
     }
-  }
-};
-
-// Where a tile's rows go: the outputs, or its partial state.
-template <typename T, int D, int R>
-struct SliceOut {
-  const PagedArgs& a;
-  int slot, nrows, G, row0, h0;
-  int64_t q0;
-  __device__ __forceinline__ int64_t row(int r) const {
-    const int x = row0 + r;
-    return (q0 + x / G) * a.H + h0 + x % G;
-  }
-  template <int N>
-  __device__ __forceinline__ void operator()(int r, int c, const float* x) const {
-    if (r >= nrows) return;
-    if (slot < 0)
-      store_vec<T, N>(static_cast<T*>(a.o) + row(r) * D + c, x);
-    else
-      store_vec<float, N>(a.part_o + (int64_t(slot) * R + r) * D + c, x);
   }
 };
 
@@ -581,8 +585,8 @@ __global__ void __launch_bounds__(SliceLayout<S, D, R>::kThreads, 1)
   constexpr int CB = D * int(sizeof(T)) / 128;     // 128-byte columns of a row
   static_assert(NS % 2 == 0, "a worker's stages keep their slots");
   extern __shared__ __align__(1024) uint8_t smem[];
-  __shared__ int64_t s_scan[34];
-  __shared__ PagedStart s_start[2];
+  __shared__ int64_t s_scan[32];
+  __shared__ PagedStart s_start;
   __shared__ PieceInfo s_piece[kPieces];
   // piece published, its Q landed, its states joined (per entry); stage landed, stage read; all workers' states left
   __shared__ uint64_t s_bar[3 * kPieces + 2 * NS + 1];
@@ -619,15 +623,14 @@ __global__ void __launch_bounds__(SliceLayout<S, D, R>::kThreads, 1)
     tc::prefetch_tmap(&sp.tmk);
     tc::prefetch_tmap(&sp.tmv);
   }
-  const int64_t total = paged_locate<kSliceUnit, kSliceExtra, L::kThreads>(
-      a, s_scan, s_start, [&](int64_t t, int k) { return k == 0 ? paged_first_unit(t, blockIdx.x, a.grid) : t; });
-  const int64_t u0 = paged_first_unit(total, blockIdx.x, a.grid), u1 = paged_first_unit(total, blockIdx.x + 1, a.grid);
+  const PagedShare share = paged_locate<kSliceUnit, kSliceExtra, L::kThreads>(a, s_scan, &s_start, blockIdx.x);
+  const int64_t u0 = share.first(blockIdx.x), u1 = share.first(blockIdx.x + 1);
   if (u1 <= u0) return;
 
   if (warp == W + 1) {
     // ---------------------------------------------------------- producer --
     PagedWalk<kSliceUnit, kSliceExtra> walk;
-    walk.start(a, s_start[0], u1 - u0, blockIdx.x);
+    walk.start(a, s_start, u1 - u0, blockIdx.x);
     const int bs = sp.box_shift, box = 1 << bs;
     uint32_t g = 0;
     bool ok = true;
@@ -700,16 +703,8 @@ __global__ void __launch_bounds__(SliceLayout<S, D, R>::kThreads, 1)
       if (!wait(bar_piece(k), phase(k))) break;
       const PieceInfo& p = s_piece[k % kPieces];
       if (!p.valid) break;
-      const int nrows = p.nrows, slot = p.slot;
-      const SliceOut<T, D, R> out{a, slot, nrows, a.G, p.row0, p.h * a.G, p.q0};
       if (!wait(bar_state, uint32_t(k) & 1u)) break;
-      S::join(states, lane, out, [&](int r, float v) {
-        if (r >= nrows) return;
-        if (slot < 0)
-          a.lse[out.row(r)] = v * 0.69314718055994531f;
-        else
-          a.part_l[int64_t(slot) * R + r] = v;
-      });
+      S::join(a, p, states, lane);
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(bar_joined(k));
     }
@@ -756,66 +751,66 @@ __global__ void __launch_bounds__(SliceLayout<S, D, R>::kThreads, 1)
 // One tile that starts in block c and goes on behind it: its partial states
 // are the blocks' from c on.  O = sum_e w_e O_e / sum_e w_e, w_e = 2^(L_e - max L),
 // L in log2 units, a warp per row; what bounds it is the launch (about 2 us).
-constexpr int kMergeThreads = 128, kMergeRows = 8;
+constexpr int kMergeThreads = 128, kMergeRows = 16;
 
 template <typename T, int D, int U, int E>
 __global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const __grid_constant__ PagedArgs a) {
-  __shared__ int64_t s_scan[34];
-  __shared__ PagedStart s_start[2];
+  __shared__ int64_t s_scan[32];
+  __shared__ PagedStart s_start;
   const int c = blockIdx.x;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t total = paged_locate<U, E, kMergeThreads>(a, s_scan, s_start, [&](int64_t t, int k) {
-    return k == 0 ? paged_first_unit(t, c + 1, a.grid) : t;
-  });
+  const PagedShare share = paged_locate<U, E, kMergeThreads>(a, s_scan, &s_start, c + 1);
+  const int64_t u0 = share.first(c), u1 = share.first(c + 1);
+  const PagedStart st = s_start;
+  // cut here, and started in this block
+  const bool work = u1 > u0 && u1 < share.total && st.off > 0 && u1 - st.off >= u0;
+  PagedReq q{};
+  PagedTile t{};
+  int last = c, slot0 = 0;
+  if (work) {
+    q = paged_req(a, st.r);
+    t = paged_tile<U>(a, q, st.t);
+    const int64_t begin = u1 - st.off, end = begin + t.n + E;
+    // blocks c .. last hold a piece (a block without units cannot lie between
+    // two of them: the first ones have the more), c's in its first or second slot
+    last = c + 1;
+    while (share.first(last + 1) < end) ++last;
+    slot0 = 2 * c + (begin == u0 ? 0 : 1);
+  }
   grid_wait();
-  const int64_t u0 = paged_first_unit(total, c, a.grid), u1 = paged_first_unit(total, c + 1, a.grid);
-  if (u1 <= u0 || u1 >= total) return;
-  const PagedStart st = s_start[0];
-  if (st.off == 0 || u1 - st.off < u0) return;  // not cut here, or it started in an earlier block
-  const PagedReq q = paged_req(a, st.r);
-  const PagedTile t = paged_tile<U>(a, q, st.t);
-  const int64_t begin = u1 - st.off, end = begin + t.n + E;
-  // blocks c .. c + n - 1 hold a piece, the first in its first or second slot
-  int last = c + 1;
-  while (paged_first_unit(total, last + 1, a.grid) < end) ++last;
-  // a block without units leaves no state
-  const int first_slot = 2 * c + (begin == u0 ? 0 : 1);
+  if (!work) return;
+  const int n = last - c + 1;
+  auto slot = [&](int e) { return int64_t(e == 0 ? slot0 : 2 * (c + e)); };
+  constexpr int N = D / 32;
   for (int i = warp; i < kMergeRows; i += kMergeThreads / 32) {
     const int r = blockIdx.y * kMergeRows + i;
     if (r >= t.nrows) break;
     float top = -INFINITY;
-    for (int e = c + lane; e <= last; e += 32) {
-      if (paged_first_unit(total, e + 1, a.grid) <= paged_first_unit(total, e, a.grid)) continue;
-      const int slot = e == c ? first_slot : 2 * e;
-      top = fmaxf(top, a.part_l[int64_t(slot) * a.R + r]);
-    }
+    const float first = lane < n ? a.part_l[slot(lane) * a.R + r] : -INFINITY;  // the whole of it, up to 32 pieces
+    top = first;
+    for (int e = 32 + lane; e < n; e += 32) top = fmaxf(top, a.part_l[slot(e) * a.R + r]);
     top = warp_max(top);
-    constexpr int N = D / 32;
     float acc[N] = {};
     float sum = 0.f;
     if (top != -INFINITY) {
-      for (int e0 = c; e0 <= last; e0 += 32) {
-        float w = 0.f;
-        const int e = e0 + lane;
-        if (e <= last && paged_first_unit(total, e + 1, a.grid) > paged_first_unit(total, e, a.grid))
-          w = exp2f(a.part_l[int64_t(e == c ? first_slot : 2 * e) * a.R + r] - top);
-        const int m = min(32, last - e0 + 1);
-#pragma unroll 4
-        for (int i2 = 0; i2 < m; ++i2) {
-          const float we = __shfl_sync(0xffffffffu, w, i2);
-          if (we == 0.f) continue;  // an empty state's O was not written
-          const int slot = e0 + i2 == c ? first_slot : 2 * (e0 + i2);
+      for (int e0 = 0; e0 < n; e0 += 32) {
+        const float l = e0 == 0 ? first : (e0 + lane < n ? a.part_l[slot(e0 + lane) * a.R + r] : -INFINITY);
+        const float w = exp2f(l - top);
+        const int m = min(32, n - e0);
+#pragma unroll 8
+        for (int j = 0; j < m; ++j) {
+          const float we = __shfl_sync(0xffffffffu, w, j);
           float x[N];
-          load_vec<float, N>(a.part_o + (int64_t(slot) * a.R + r) * D + N * lane, x);
+          load_vec<float, N>(a.part_o + (slot(e0 + j) * a.R + r) * D + N * lane, x);  // an empty state's O is 0
           sum += we;
 #pragma unroll
-          for (int j = 0; j < N; ++j) acc[j] = fmaf(we, x[j], acc[j]);
+          for (int v = 0; v < N; ++v) acc[v] = fmaf(we, x[v], acc[v]);
         }
       }
     }
     const float inv = sum > 0.f ? 1.f / sum : 0.f;
 #pragma unroll
-    for (int j = 0; j < N; ++j) acc[j] *= inv;
+    for (int v = 0; v < N; ++v) acc[v] *= inv;
     const int row = t.row0 + r;
     const int64_t out = int64_t(q.q0 + row / a.G) * a.H + st.h * a.G + row % a.G;
     store_vec<T, N>(static_cast<T*>(a.o) + out * D + N * lane, acc);

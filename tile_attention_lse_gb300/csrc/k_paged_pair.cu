@@ -54,7 +54,7 @@ constexpr int kOffV = kOffK + kKStages * kKBytes;
 constexpr int kOffBar = kOffV + kVStages * kVBytes;
 constexpr int kOffX = kOffBar + 512;  // running max [2 tile parities][128], row-sum base and sum [2 warps][2][128]
 constexpr int kOffScan = kOffX + (2 * 128 + 2 * 2 * 128) * 4;
-constexpr int kSmemBytes = kOffScan + 34 * 8 + 2 * int(sizeof(PagedStart));
+constexpr int kSmemBytes = kOffScan + 32 * 8 + int(sizeof(PagedStart));
 static_assert(kSmemBytes <= 232448, "shared memory budget of one CTA");
 
 // Barrier slots, the same layout in both CTAs.  "even": only the even CTA's
@@ -148,10 +148,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_pair_kernel(const __grid_co
   // this pair's share of the units
   const int pair = int(tc::cluster_id_x());
   int64_t* s_scan = reinterpret_cast<int64_t*>(smem + kOffScan);
-  PagedStart* s_start = reinterpret_cast<PagedStart*>(smem + kOffScan + 34 * 8);
-  const int64_t total = paged_locate<kPairUnit, kPairExtra, kThreads>(
-      a, s_scan, s_start, [&](int64_t t, int k) { return k == 0 ? paged_first_unit(t, pair, a.grid) : t; });
-  const int64_t units = paged_first_unit(total, pair + 1, a.grid) - paged_first_unit(total, pair, a.grid);
+  PagedStart* s_start = reinterpret_cast<PagedStart*>(smem + kOffScan + 32 * 8);
+  const PagedShare share = paged_locate<kPairUnit, kPairExtra, kThreads>(a, s_scan, s_start, pair);
+  const int64_t units = share.first(pair + 1) - share.first(pair);
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < B_COUNT; ++i) {
@@ -175,7 +174,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_pair_kernel(const __grid_co
   const uint32_t tmem = *tmem_slot;
 
   Walk w;
-  w.start(a, units > 0 ? s_start[0] : PagedStart{0, 0, 0, 0}, units, pair);
+  w.start(a, units > 0 ? *s_start : PagedStart{0, 0, 0, 0}, units, pair);
   const int half_rows = a.R >> 1;  // packed rows of a CTA
 
   if (warp < 4) {

@@ -8,7 +8,8 @@
 // of R rows.  A tile's visible keys are walked in units of U keys and cost n
 // units plus E for its start and its end.  The units of all (request,
 // kv-head, tile) triples, in that order, form one axis, and block c of N takes
-// units [c T / N, (c + 1) T / N) of the T: equal shares whatever the lengths.  A tile
+// the c-th of N runs of it (T / N units, the first T % N blocks one more):
+// equal shares whatever the lengths.  A tile
 // whose units fall to one block is written to the outputs by it; a tile that
 // is cut leaves one partial state (O, L) per block in the workspace, at most
 // two per block (its first and its last piece), and the merge kernel joins
@@ -74,15 +75,15 @@ struct PagedTile {
 };
 
 CPATTN_HD int32_t paged_tiles(const PagedArgs& a, const PagedReq& q) {
-  return int32_t((int64_t(q.nq) * a.G + a.R - 1) / a.R);
+  return int32_t((uint32_t(q.nq) * uint32_t(a.G) + uint32_t(a.R) - 1) / uint32_t(a.R));  // rows * G < 2^31 - R
 }
 
 template <int U>
 CPATTN_HD PagedTile paged_tile(const PagedArgs& a, const PagedReq& q, int t) {
   PagedTile x;
   x.row0 = t * a.R;
-  const int64_t left = int64_t(q.nq) * a.G - x.row0;
-  x.nrows = int32_t(left < a.R ? left : a.R);
+  const int32_t left = q.nq * a.G - x.row0;
+  x.nrows = left < a.R ? left : a.R;
   const int32_t pos0 = q.kv - q.nq + x.row0 / a.G, pos1 = q.kv - q.nq + (x.row0 + x.nrows - 1) / a.G;
   x.hi = a.causal ? (pos1 + 1 < q.kv ? pos1 + 1 : q.kv) : q.kv;
   if (x.hi < 0) x.hi = 0;
@@ -102,7 +103,17 @@ CPATTN_HD int64_t paged_req_units(const PagedArgs& a, const PagedReq& q) {
   return s;
 }
 
-CPATTN_HD int64_t paged_first_unit(int64_t total, int c, int grid) { return total * c / grid; }
+// Quotient of values below 2^62; the 32-bit division where both fit is several times faster.
+CPATTN_HD int64_t paged_div(int64_t x, int64_t y) {
+  return ((x | y) >> 31) == 0 ? int64_t(uint32_t(x) / uint32_t(y)) : x / y;
+}
+
+// The shares of the blocks.
+struct PagedShare {
+  int64_t total, each, more;  // block c: `each` units, one more for c < more
+  CPATTN_HD PagedShare(int64_t t, int grid) : total(t), each(paged_div(t, grid)), more(t - each * grid) {}
+  CPATTN_HD int64_t first(int c) const { return each * c + (c < more ? c : more); }
+};
 
 // Where a unit lies: its tile and the units of the tile before it.
 struct PagedStart {

@@ -5,12 +5,11 @@
 
 namespace cpattn {
 
-// Finds where units `u` and `v` of the common axis lie (u, v < the total) and
-// returns the total; the whole block calls it, `sh` holds 34 int64 and `out`
-// two PagedStarts in shared memory.  The threads share the requests in runs.
-// A value at or behind the total leaves its PagedStart unwritten.
-template <int U, int E, int kThreads, typename F>
-__device__ __forceinline__ int64_t paged_locate(const PagedArgs& a, int64_t* sh, PagedStart* out, F units) {
+// Finds where the first unit of block c lies and returns the shares; the whole
+// block calls it, `sh` holds 32 int64 and `out` a PagedStart in shared memory
+// (not written where c has no first unit).  The threads share the requests in runs.
+template <int U, int E, int kThreads>
+__device__ __forceinline__ PagedShare paged_locate(const PagedArgs& a, int64_t* sh, PagedStart* out, int c) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int run = (a.n_reqs + kThreads - 1) / kThreads;
   const int r0 = min(tid * run, a.n_reqs), r1 = min(r0 + run, a.n_reqs);
@@ -30,9 +29,9 @@ __device__ __forceinline__ int64_t paged_locate(const PagedArgs& a, int64_t* sh,
     if (w < warp) before += sh[w];
     total += sh[w];
   }
-  for (int k = 0; k < 2; ++k) {
-    const int64_t u = units(total, k);
-    if (u < before || u >= before + mine || u >= total) continue;
+  const PagedShare share(total, a.grid);
+  const int64_t u = share.first(c);
+  if (u >= before && u < before + mine) {
     int64_t base = before;
     for (int r = r0; r < r1; ++r) {
       const PagedReq q = paged_req(a, r);
@@ -41,13 +40,13 @@ __device__ __forceinline__ int64_t paged_locate(const PagedArgs& a, int64_t* sh,
         base += per * a.Hkv;
         continue;
       }
-      const int h = int((u - base) / per);
+      const int h = int(paged_div(u - base, per));
       int64_t rest = u - base - h * per;
       const int nt = paged_tiles(a, q);
       for (int t = 0; t < nt; ++t) {
         const int cost = paged_tile<U>(a, q, t).n + E;
         if (rest < cost) {
-          out[k] = PagedStart{r, h, t, int32_t(rest)};
+          *out = PagedStart{r, h, t, int32_t(rest)};
           break;
         }
         rest -= cost;
@@ -56,7 +55,7 @@ __device__ __forceinline__ int64_t paged_locate(const PagedArgs& a, int64_t* sh,
     }
   }
   __syncthreads();
-  return total;
+  return share;
 }
 
 // The merge kernel may start early; it waits for its predecessor here.

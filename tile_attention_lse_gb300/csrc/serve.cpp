@@ -98,9 +98,10 @@ template <int U, int E, typename F>
 void walk_all(const PagedArgs& a, F f) {
   int64_t total = 0;
   for (int r = 0; r < a.n_reqs; ++r) total += paged_req_units<U, E>(a, paged_req(a, r)) * a.Hkv;
+  const PagedShare share(total, a.grid);
   PagedStart at{0, 0, 0, 0};
   for (int c = 0; c < a.grid; ++c) {
-    const int64_t u0 = paged_first_unit(total, c, a.grid), u1 = paged_first_unit(total, c + 1, a.grid);
+    const int64_t u0 = share.first(c), u1 = share.first(c + 1);
     if (u1 <= u0) continue;
     // where u0 lies: the walk of the block before ended there; step over what
     // has no tile
@@ -323,7 +324,7 @@ cp_status cp_paged_attn_fwd(const cp_paged_desc* desc, int32_t n_reqs, int64_t r
   if (st != CP_OK) return st;
   if (n_reqs < 0 || rows < 0 || max_blocks < 1) return CP_ERR_INVALID_ARG;
   const cp_kv_cache& c = desc->kv;
-  if (rows * (desc->heads_q / c.heads_kv) >= (int64_t(1) << 31) ||
+  if (rows * (desc->heads_q / c.heads_kv) >= (int64_t(1) << 31) - 1024 ||
       int64_t(max_blocks) * c.page_size > (int64_t(1) << 30))
     return CP_ERR_UNSUPPORTED;
   if (n_reqs == 0 || rows == 0) return CP_OK;
