@@ -403,7 +403,7 @@ class PagedKV:
             raise ValueError("k_cache and v_cache share their type and device, head_dim contiguous")
         self.k_cache, self.v_cache = k_cache, v_cache
         self.n_pages, self.page_size, self.heads_kv, self.head_dim = k_cache.shape
-        self.dtype, self.device = k_cache.dtype, k_cache.device
+        self.dtype, self.device, self._index = k_cache.dtype, k_cache.device, k_cache.get_device()
         s = k_cache.stride()
         self._desc = CpKvCache(k_cache.data_ptr(), v_cache.data_ptr(), *k_cache.shape, s[0], s[1], s[2],
                                _dtype_code(k_cache.dtype))
@@ -434,19 +434,27 @@ class PagedProblem:
         self._ref = ctypes.byref(self._desc)
 
 
-def _rows(x: torch.Tensor, what: str, shape, dtype, device):
-    """Row stride (elements) of a [rows, heads, head_dim] tensor whose rows are contiguous."""
-    if x.shape[1:] != shape or x.dim() != 3 or x.dtype != dtype or x.device != device:
-        raise ValueError(f"{what} is a [rows, {shape[0]}, {shape[1]}] {dtype} tensor on {device}")
+# A call's checks and marshalling cost more host time than its launch (a few
+# microseconds, which a decode step of small calls feels), so they compare
+# singletons and device indices and look the raw stream up directly.
+_I32, _F32 = torch.int32, torch.float32
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _rows(x: torch.Tensor, what: str, heads: int, d: int, dtype, device: int):
+    """Row stride (elements) of a [rows, heads, d] tensor whose rows are contiguous."""
+    shape = x.shape
+    if len(shape) != 3 or shape[1] != heads or shape[2] != d or x.dtype is not dtype or x.get_device() != device:
+        raise ValueError(f"{what} is a [rows, {heads}, {d}] {dtype} tensor on cuda:{device}")
     s = x.stride()
-    if s[2] != 1 or (s[1] != shape[1] and shape[0] > 1):
+    if s[2] != 1 or (s[1] != d and heads > 1):
         raise ValueError(f"{what}: the heads of a row are contiguous")
-    return s[0] if x.shape[0] > 1 else shape[0] * shape[1]
+    return s[0] if shape[0] > 1 else heads * d
 
 
-def _ints(x: torch.Tensor, what: str, shape, device):
-    if x.dtype != torch.int32 or tuple(x.shape) != shape or not x.is_contiguous() or x.device != device:
-        raise ValueError(f"{what} is a contiguous {list(shape)} int32 tensor on {device}")
+def _ints(x: torch.Tensor, what: str, shape, device: int):
+    if x.dtype is not _I32 or x.shape != shape or x.get_device() != device or not x.is_contiguous():
+        raise ValueError(f"{what} is a contiguous {list(shape)} int32 tensor on cuda:{device}")
     return x.data_ptr()
 
 
@@ -454,16 +462,29 @@ def _new(out, what, shape, dtype, device):
     """The caller's output tensor (contiguous, of that shape and type), or a new one."""
     if out is None:
         return torch.empty(shape, dtype=dtype, device=device)
-    if tuple(out.shape) != tuple(shape) or out.dtype != dtype or out.device != device or not out.is_contiguous():
+    if out.shape != shape or out.dtype is not dtype or out.device != device or not out.is_contiguous():
         raise ValueError(f"{what} is a contiguous {list(shape)} {dtype} tensor on {device}")
     return out
 
 
-def _stream_of(device):
+def _stream_of(device: int) -> int:
     """The current stream of the device that holds the tensors (it has to be the current device)."""
-    if device.type != "cuda" or device.index != torch.cuda.current_device():
-        raise ValueError(f"the tensors are on {device}: make it the current CUDA device")
-    return torch.cuda.current_stream().cuda_stream
+    if device < 0 or device != torch.cuda.current_device():
+        raise ValueError("the tensors are not on the current CUDA device")
+    return _raw_stream(device)
+
+
+def _tables(block_table, free_pages, n_free, **per_request):
+    """Sizes, device index and pointers of a call on the request tables."""
+    if block_table.dim() != 2:
+        raise ValueError("block_table is [n_reqs, max_blocks]")
+    n, width = block_table.shape
+    dev = block_table.get_device()
+    pool = free_pages.numel()
+    args = [_ints(x, name, (n,), dev) for name, x in per_request.items()]
+    args += [_ints(free_pages, "free_pages", (pool,), dev), _ints(n_free, "n_free", (1,), dev),
+             _ints(block_table, "block_table", (n, width), dev)]
+    return n, width, pool, args, _stream_of(dev)
 
 
 def kv_extend(page_size: int, block_table, lens, add, free_pages, n_free, max_rows: int):
@@ -471,40 +492,27 @@ def kv_extend(page_size: int, block_table, lens, add, free_pages, n_free, max_ro
 
     block_table [n_reqs, max_blocks] changes in place; returns (lens, cu_new,
     slots, pos, n_free) as new tensors."""
-    if block_table.dim() != 2:
-        raise ValueError("block_table is [n_reqs, max_blocks]")
-    n, width = block_table.shape
-    dev = block_table.device
-    pool = free_pages.numel()
-    args = [_ints(lens, "lens", (n,), dev), _ints(add, "add", (n,), dev), _ints(free_pages, "free_pages", (pool,), dev),
-            _ints(n_free, "n_free", (1,), dev), _ints(block_table, "block_table", (n, width), dev)]
-    s = _stream_of(dev)
-    out = torch.empty(2 * n + 2 + 2 * max_rows, dtype=torch.int32, device=dev)
-    lens_out, cu, n_free_out, slots, pos = out.split((n, n + 1, 1, max_rows, max_rows))
-    base = out.data_ptr()
-    _check(lib().cp_kv_extend(n, width, page_size, max_rows, pool, *args, base, base + 4 * n, base + 4 * (2 * n + 2),
-                              base + 4 * (2 * n + 2 + max_rows), base + 4 * (2 * n + 1), s), "cp_kv_extend")
+    n, width, pool, args, s = _tables(block_table, free_pages, n_free, lens=lens, add=add)
+    out = torch.empty(2 * n + 2 + 2 * max_rows, dtype=_I32, device=block_table.device)
+    at = out.data_ptr()
+    rows_at = at + 4 * (2 * n + 2)
+    _check(lib().cp_kv_extend(n, width, page_size, max_rows, pool, *args, at, at + 4 * n, rows_at,
+                              rows_at + 4 * max_rows, rows_at - 4, s), "cp_kv_extend")
+    lens_out, cu, n_free_out, slots, pos = torch.split_with_sizes(out, (n, n + 1, 1, max_rows, max_rows))
     return lens_out, cu, slots, pos, n_free_out
 
 
 def kv_release(page_size: int, block_table, lens, done, free_pages, n_free):
     """Gives the pages of the requests with done != 0 back (cp_kv_release);
     block_table and free_pages change in place; returns (lens, n_free)."""
-    if block_table.dim() != 2:
-        raise ValueError("block_table is [n_reqs, max_blocks]")
-    n, width = block_table.shape
-    dev = block_table.device
-    pool = free_pages.numel()
-    args = [_ints(lens, "lens", (n,), dev), _ints(done, "done", (n,), dev), _ints(free_pages, "free_pages", (pool,), dev),
-            _ints(n_free, "n_free", (1,), dev), _ints(block_table, "block_table", (n, width), dev)]
-    s = _stream_of(dev)
+    n, width, pool, args, s = _tables(block_table, free_pages, n_free, lens=lens, done=done)
     lens_out, n_free_out = torch.empty_like(lens), torch.empty_like(n_free)
     _check(lib().cp_kv_release(n, width, page_size, pool, *args, lens_out.data_ptr(), n_free_out.data_ptr(), s),
            "cp_kv_release")
     return lens_out, n_free_out
 
 
-def _positions(rope: Rope, pos: torch.Tensor, rows: int, device):
+def _positions(rope: Rope, pos: torch.Tensor, rows: int, device: int):
     axes = len(rope.sections)
     return _ints(pos, "pos", (rows,) if axes == 1 and pos.dim() == 1 else (axes, rows), device)
 
@@ -512,21 +520,22 @@ def _positions(rope: Rope, pos: torch.Tensor, rows: int, device):
 def rope_axes(rope: Rope, pos, q, k=None, inverse: bool = False, q_out=None, k_out=None):
     """Rotates q [rows, heads, head_dim] (and k) by pos [axes, rows] (cp_rope_axes);
     inverse: the transpose, which is the gradient."""
-    dev, dt = q.device, q.dtype
     if q.dim() != 3 or (k is not None and k.dim() != 3):
         raise ValueError("q and k are [rows, heads, head_dim]")
+    dev, dt = q.get_device(), q.dtype
     rows, hq, d = q.shape
-    qs = _rows(q, "q", (hq, d), dt, dev)
-    hk, ks = (0, 0) if k is None else (k.shape[1], _rows(k, "k", (k.shape[1], d), dt, dev))
-    if k is not None and k.shape[0] != rows:
-        raise ValueError("q and k have the same rows")
+    qs, hk, ks, kp, ko = _rows(q, "q", hq, d, dt, dev), 0, 0, None, None
     p, s = _positions(rope, pos, rows, dev), _stream_of(dev)
-    q_out = _new(q_out, "q_out", (rows, hq, d), dt, dev)
+    q_out = _new(q_out, "q_out", q.shape, dt, q.device)
     if k is not None:
-        k_out = _new(k_out, "k_out", (rows, hk, d), dt, dev)
-    _check(lib().cp_rope_axes(rope._ref, p, rows, d, _dtype_code(dt), hq, q.data_ptr(), qs, q_out.data_ptr(), hk,
-                              None if k is None else k.data_ptr(), ks, None if k is None else k_out.data_ptr(),
-                              int(inverse), s), "cp_rope_axes")
+        hk = k.shape[1]
+        ks = _rows(k, "k", hk, d, dt, dev)
+        if k.shape[0] != rows:
+            raise ValueError("q and k have the same rows")
+        k_out = _new(k_out, "k_out", k.shape, dt, k.device)
+        kp, ko = k.data_ptr(), k_out.data_ptr()
+    _check(lib().cp_rope_axes(rope._ref, p, rows, d, _dtype_code(dt), hq, q.data_ptr(), qs, q_out.data_ptr(), hk, kp, ks,
+                              ko, int(inverse), s), "cp_rope_axes")
     return q_out if k is None else (q_out, k_out)
 
 
@@ -534,25 +543,26 @@ def kv_append(kv: PagedKV, slots, k, v, rope: Rope | None = None, pos=None, q=No
     """Writes k and v [rows, heads_kv, head_dim] into the slots of the cache
     (cp_kv_append); with rope, k is rotated by pos on the way and q into the
     returned q_out."""
-    dev, dt, shape = kv.device, kv.dtype, (kv.heads_kv, kv.head_dim)
+    dev, dt, heads, d = kv._index, kv.dtype, kv.heads_kv, kv.head_dim
     rows = k.shape[0]
-    ks, vs = _rows(k, "k", shape, dt, dev), _rows(v, "v", shape, dt, dev)
+    ks, vs = _rows(k, "k", heads, d, dt, dev), _rows(v, "v", heads, d, dt, dev)
     if v.shape[0] != rows:
         raise ValueError("k and v have the same rows")
     if (rope is None) != (pos is None) or (q is not None and rope is None):
         raise ValueError("rope, pos and q: positions come with a rotation, q is rotated")
-    hq, qs = 0, 0
+    hq, qs, qp, qo, r, p = 0, 0, None, None, None, None
+    if rope is not None:
+        r, p = rope._ref, _positions(rope, pos, rows, dev)
+    at, s = _ints(slots, "slots", (rows,), dev), _stream_of(dev)
     if q is not None:
         if q.dim() != 3 or q.shape[0] != rows:
             raise ValueError("q is [rows, heads_q, head_dim]")
         hq = q.shape[1]
-        qs = _rows(q, "q", (hq, kv.head_dim), dt, dev)
-        q_out = _new(q_out, "q_out", (rows, hq, kv.head_dim), dt, dev)
-    p = None if rope is None else _positions(rope, pos, rows, dev)
-    s = _stream_of(dev)
-    _check(lib().cp_kv_append(kv._ref, _ints(slots, "slots", (rows,), dev), rows, k.data_ptr(), ks, v.data_ptr(), vs,
-                              None if rope is None else rope._ref, p, hq, None if q is None else q.data_ptr(), qs,
-                              None if q is None else q_out.data_ptr(), s), "cp_kv_append")
+        qs = _rows(q, "q", hq, d, dt, dev)
+        q_out = _new(q_out, "q_out", q.shape, dt, q.device)
+        qp, qo = q.data_ptr(), q_out.data_ptr()
+    _check(lib().cp_kv_append(kv._ref, at, rows, k.data_ptr(), ks, v.data_ptr(), vs, r, p, hq, qp, qs, qo, s),
+           "cp_kv_append")
     return None if q is None else q_out
 
 
@@ -589,21 +599,24 @@ def paged_attn_fwd(p: PagedProblem, q, block_table, cu_new, kv_lens, ws: torch.T
     """Attention of the new tokens q [rows, heads_q, head_dim] over the pages of
     their requests (cp_paged_attn_fwd) -> (o, lse).  Rows behind the last
     request's are left as they were (unset in a new o and lse)."""
-    kv = p.kv
-    dev = kv.device
-    qs = _rows(q, "q", (p.heads_q, kv.head_dim), kv.dtype, dev)
+    kv, heads = p.kv, p.heads_q
+    dev, d = kv._index, kv.head_dim
+    qs = _rows(q, "q", heads, d, kv.dtype, dev)
     if block_table.dim() != 2:
         raise ValueError("block_table is [n_reqs, max_blocks]")
     n, width = block_table.shape
-    tables = (_ints(block_table, "block_table", (n, width), dev), _ints(cu_new, "cu_new", (n + 1,), dev),
-              _ints(kv_lens, "kv_lens", (n,), dev))
+    table, cu, lens = (_ints(block_table, "block_table", (n, width), dev), _ints(cu_new, "cu_new", (n + 1,), dev),
+                       _ints(kv_lens, "kv_lens", (n,), dev))
     s = _stream_of(dev)
-    ws = paged_workspace(p) if ws is None else ws
+    if ws is None:
+        ws = paged_workspace(p)
+    elif ws.get_device() != dev or not ws.is_contiguous():
+        raise ValueError(f"ws is a contiguous tensor on cuda:{dev}")
     rows = q.shape[0]
-    out = _new(out, "out", (rows, p.heads_q, kv.head_dim), kv.dtype, dev)
-    lse = _new(lse, "lse", (rows, p.heads_q), torch.float32, dev)
-    _check(lib().cp_paged_attn_fwd(p._ref, n, rows, width, q.data_ptr(), qs, *tables, out.data_ptr(), lse.data_ptr(),
-                                   ws.data_ptr(), ws.nbytes, s), "cp_paged_attn_fwd")
+    out = _new(out, "out", q.shape, kv.dtype, kv.device)
+    lse = _new(lse, "lse", (rows, heads), _F32, kv.device)
+    _check(lib().cp_paged_attn_fwd(p._ref, n, rows, width, q.data_ptr(), qs, table, cu, lens, out.data_ptr(),
+                                   lse.data_ptr(), ws.data_ptr(), ws.nbytes, s), "cp_paged_attn_fwd")
     return out, lse
 
 

@@ -13,7 +13,7 @@
 //   producer  walks the block's share, up to four pieces ahead, and loads it: Q
 //             by 16-byte copies, K and V by TMA, a box per page and 128 bytes
 //             of the head, into a ring of stages of 32 KB (head_dim 64: 16 KB);
-//   workers   four take each stage, the other four the next; a worker has its own
+//   workers   take the stages in turn (bf16: four of them each, float32: one); a worker has its own
 //             slice of a stage's keys and its own running maximum, sum and O, so
 //             no barrier stands between them; at the end of a piece it leaves its state
 //             in shared memory and goes on with the next one;
@@ -29,8 +29,7 @@
 //   precision), its row sum is taken in float32 before that.  The legacy
 //   tensor path is chosen here because these tiles have too few rows to be
 //   bound by it.
-// float32: FFMA throughout.  Four lanes own a key (a quarter of the head each)
-//   in the first product, a lane 4 columns of the head in the second.
+// float32: FFMA throughout, for the arithmetic's sake.
 #include <cuda_bf16.h>
 
 #include <atomic>
@@ -141,8 +140,8 @@ struct SliceOut {
 template <int D, int R>
 struct SliceBf16 {
   using T = __nv_bfloat16;
-  static constexpr int kWarps = 8, kKeys = 16, kStages = D == 128 ? 4 : 8;
-  static constexpr int kStageKeys = 4 * kKeys;
+  static constexpr int kWarps = 8, kPerStage = 4, kKeys = 16, kStages = D == 128 ? 4 : 8;  // kPerStage: workers of a stage
+  static constexpr int kStageKeys = kPerStage * kKeys;
   static constexpr int MT = R / 16, NT = D / 8;
   static constexpr int kAcc = MT * NT * 4, kRows = MT * 2;  // accumulators and rows of a thread
   static constexpr int kQBytes = R * D * 2;
@@ -351,17 +350,20 @@ struct SliceBf16 {
 };
 
 // --------------------------------------------------------- float32: FFMA ---
+// A worker has a stage of 32 keys to itself.  First product: a lane owns a key
+// and all R rows of Q come by broadcast, so nothing is summed across lanes and every
+// exponential is formed once; P changes hands through shared memory, and in the second product a lane
+// owns 4 columns (head_dim 64: of half of the keys).
 template <int D, int R>
 struct SliceF32 {
   using T = float;
-  static constexpr int kWarps = 8, kKeys = 8, kStages = D == 128 ? 4 : 8;
-  static constexpr int kStageKeys = 4 * kKeys;
+  static constexpr int kWarps = 8, kPerStage = 1, kKeys = 32, kStages = D == 128 ? 4 : 8;
+  static constexpr int kStageKeys = kKeys;
   static constexpr int kAcc = 4 * R;
-  static constexpr int kQStride = (D + 16) * 4;  // each quarter of a row sits 16 bytes on: other banks
-  static constexpr int kQBytes = R * kQStride;
-  static constexpr int kScratch = kKeys * R * 4;  // P of a worker's slice
+  static constexpr int kQBytes = R * D * 4;
+  static constexpr int kScratch = kKeys * R * 4;        // P of a worker's slice
   static constexpr int kState = kAcc / 4 * 32 + R / 2;  // float4s of a worker's state; m and l are the same in every lane
-  static constexpr int kPieces = D == 128 ? 2 : 4;      // pieces that the scheduler is ahead (their Q fills the rest of shared memory)
+  static constexpr int kPieces = D == 128 ? 2 : 4;      // pieces that the producer is ahead (their Q fills the rest of shared memory)
   float acc[kAcc];
   float m[R], l[R];
   int32_t pos0, row0, kv;
@@ -369,7 +371,11 @@ struct SliceF32 {
   static __device__ __forceinline__ uint32_t at(int r, int c) {
     return uint32_t((c >> 3) * (kStageKeys * 128) + r * 128 + (((c ^ r) & 7) << 4));
   }
-  static __device__ __forceinline__ uint32_t q_at(int r, int c) { return uint32_t(r * kQStride + ((c + c / (D / 16)) << 4)); }
+  static __device__ __forceinline__ uint32_t q_at(int r, int c) { return uint32_t(r * D * 4 + (c << 4)); }
+  // P of rows r .. r + 3 for a key, swizzled so that 8 lanes' keys fall on different banks
+  static __device__ __forceinline__ float4* p_at(float* sp, int key, int r) {
+    return reinterpret_cast<float4*>(sp + key * R) + (R == 16 ? (r / 4) ^ ((key >> 1) & 3) : r / 4);
+  }
   static __device__ __forceinline__ float4 lds4(uint32_t addr) {
     float4 v;
     asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
@@ -394,39 +400,48 @@ struct SliceF32 {
 
   __device__ __forceinline__ void slice(const PagedArgs& a, uint32_t sq, uint32_t sk, uint32_t sv, int srow, float* sp,
                                         int key, bool full, int klo, int khi, int lane) {
-    const int kx = lane & 7, quarter = lane >> 3;
+    constexpr int RB = R < 8 ? R : 8;  // rows whose Q is in registers at once
     float s[R];
 #pragma unroll
     for (int r = 0; r < R; ++r) s[r] = 0.f;
+#pragma unroll 2
+    for (int c = 0; c < D / 4; ++c) {
+      const float4 k = lds4(sk + at(srow + lane, c));
 #pragma unroll
-    for (int c0 = 0; c0 < D / 16; ++c0) {
-      const int c = quarter * (D / 16) + c0;
-      const float4 k = lds4(sk + at(srow + kx, c));
+      for (int r0 = 0; r0 < R; r0 += RB) {
+        float4 q[RB];
 #pragma unroll
-      for (int r = 0; r < R; ++r) {
-        const float4 q = lds4(sq + uint32_t(r * kQStride + ((c + quarter) << 4)));
-        s[r] = fmaf(q.x, k.x, s[r]);
-        s[r] = fmaf(q.y, k.y, s[r]);
-        s[r] = fmaf(q.z, k.z, s[r]);
-        s[r] = fmaf(q.w, k.w, s[r]);
+        for (int r = 0; r < RB; ++r) q[r] = lds4(sq + q_at(r0 + r, c));
+#pragma unroll
+        for (int r = 0; r < RB; ++r) s[r0 + r] = fmaf(q[r].x, k.x, s[r0 + r]);
+#pragma unroll
+        for (int r = 0; r < RB; ++r) s[r0 + r] = fmaf(q[r].y, k.y, s[r0 + r]);
+#pragma unroll
+        for (int r = 0; r < RB; ++r) s[r0 + r] = fmaf(q[r].z, k.z, s[r0 + r]);
+#pragma unroll
+        for (int r = 0; r < RB; ++r) s[r0 + r] = fmaf(q[r].w, k.w, s[r0 + r]);
       }
     }
-    const int j = key + kx;
-    bool grow = false;
-    float up[R];
+    const int j = key + lane;
+    if (!full) {
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-      s[r] += __shfl_xor_sync(0xffffffffu, s[r], 8);
-      s[r] += __shfl_xor_sync(0xffffffffu, s[r], 16);
-      if (!full) {
+      for (int r = 0; r < R; ++r) {
         const int pos = pos0 + (row0 + r) / a.G;
         const bool see = j < kv && (!a.causal || j <= pos) && (a.window == 0 || pos - j < a.window);
         s[r] = see ? s[r] : -INFINITY;
       }
-      float v = s[r];
+    }
+    float up[R];
 #pragma unroll
-      for (int o = 1; o < 8; o <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
-      up[r] = v * a.scale_log2;
+    for (int r = 0; r < R; ++r) up[r] = s[r];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+      for (int r = 0; r < R; ++r) up[r] = fmaxf(up[r], __shfl_xor_sync(0xffffffffu, up[r], o));
+    bool grow = false;
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      up[r] *= a.scale_log2;
       grow |= up[r] > m[r] + 8.f;
     }
     if (grow) {  // the same in every lane
@@ -444,25 +459,21 @@ struct SliceF32 {
     for (int r = 0; r < R; ++r) {
       const float base = m[r] == -INFINITY ? 0.f : m[r];
       s[r] = exp2f(fmaf(s[r], a.scale_log2, -base));
-      l[r] += s[r];  // four lanes of a key hold the same
+      l[r] += s[r];
     }
-    // the four lanes of a key store a quarter of its rows each
 #pragma unroll
-    for (int r = 0; r < R; r += 4)
-      if ((r / 4) % 4 == quarter || R == 4)
-        *reinterpret_cast<float4*>(sp + kx * R + r) = make_float4(s[r], s[r + 1], s[r + 2], s[r + 3]);
+    for (int r = 0; r < R; r += 4) *p_at(sp, lane, r) = make_float4(s[r], s[r + 1], s[r + 2], s[r + 3]);
     __syncwarp();
-    // head_dim 128: 32 lanes x 4 columns; 64: 16 lanes x 4 columns, each half of the warp half of the keys
     constexpr int kn = D == 128 ? kKeys : kKeys / 2;
-    const int c = D == 128 ? lane : lane & 15;
-#pragma unroll
+    const int c = D == 128 ? lane : lane & 15, x0 = D == 128 ? 0 : (lane >> 4) * kn;
+#pragma unroll 4
     for (int i = 0; i < kn; ++i) {
-      const int x = D == 128 ? i : (lane >> 4) * kn + i;
+      const int x = x0 + i;
       float4 v = lds4(sv + at(srow + x, c));
       if (!full && (key + x < klo || key + x >= khi)) v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int r = 0; r < R; r += 4) {
-        const float4 p = *reinterpret_cast<const float4*>(sp + x * R + r);
+        const float4 p = *p_at(sp, x, r);
         const float pr[4] = {p.x, p.y, p.z, p.w};
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
@@ -478,10 +489,7 @@ struct SliceF32 {
 
   __device__ __forceinline__ void end() {
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-#pragma unroll
-      for (int o = 1; o < 8; o <<= 1) l[r] += __shfl_xor_sync(0xffffffffu, l[r], o);
-    }
+    for (int r = 0; r < R; ++r) l[r] = warp_sum(l[r]);
     if (D == 64) {
 #pragma unroll
       for (int i = 0; i < kAcc; ++i) acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], 16);
@@ -583,7 +591,6 @@ __global__ void __launch_bounds__(SliceLayout<S, D, R>::kThreads, 1)
   constexpr int V = 16 / int(sizeof(T));           // elements of a Q copy
   constexpr int CH = D / V;                        // Q copies of a row
   constexpr int CB = D * int(sizeof(T)) / 128;     // 128-byte columns of a row
-  static_assert(NS % 2 == 0, "a worker's stages keep their slots");
   extern __shared__ __align__(1024) uint8_t smem[];
   __shared__ int64_t s_scan[32];
   __shared__ PagedStart s_start;
@@ -615,7 +622,7 @@ __global__ void __launch_bounds__(SliceLayout<S, D, R>::kThreads, 1)
     for (int i = 0; i < 3 * kPieces; ++i) tc::mbar_init(tc::smem_u32(s_bar + i), i / kPieces == 1 ? 32 : 1);
     for (int i = 0; i < NS; ++i) {
       tc::mbar_init(bar_full(i), 1);
-      tc::mbar_init(bar_empty(i), W / 2);
+      tc::mbar_init(bar_empty(i), S::kPerStage);
     }
     tc::mbar_init(bar_state, W);
     s_abort = 0;
@@ -713,7 +720,7 @@ __global__ void __launch_bounds__(SliceLayout<S, D, R>::kThreads, 1)
 
   // -------------------------------------------------------------- worker --
   float* scratch = reinterpret_cast<float*>(smem + L::kOffP + warp * S::kScratch);
-  const int srow = (warp & 3) * kKeys;
+  const int srow = (warp % S::kPerStage) * kKeys;
   uint32_t g = 0;
   bool ok = true;
   S st;
@@ -727,8 +734,11 @@ __global__ void __launch_bounds__(SliceLayout<S, D, R>::kThreads, 1)
     const int n = p.n, lo = p.lo, hi = p.hi, full_lo = p.full_lo, full_hi = p.full_hi;
     int key = p.key0 + srow;
     for (int t = 0; t < n; ++t, ++g, key += SK) {
-      if (int(g & 1) != (warp >> 2)) continue;  // the other four workers' stage
-      ok = wait(bar_full(g), (g / NS) & 1);
+      if (int(g % (W / S::kPerStage)) != warp / S::kPerStage) continue;  // other workers' stage
+      // a phase can be told from the one two before it only once the one between is complete,
+      // which another worker's turn may have waited for
+      if (W / S::kPerStage > NS && g >= uint32_t(NS)) ok = wait(bar_full(g - NS), (g / NS - 1) & 1);
+      ok = ok && wait(bar_full(g), (g / NS) & 1);
       if (!ok) break;
       const uint32_t sk = sbase + L::kOffRing + (g % NS) * L::kStageBytes;
       if (key < hi && key + kKeys > lo)

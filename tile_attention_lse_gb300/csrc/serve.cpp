@@ -3,6 +3,7 @@
 // validation and launches on the caller's stream; nothing here allocates.
 #include <cmath>
 #include <cstdint>
+#include <cstring>
 
 #include "internal.h"
 #include "paged.h"
@@ -38,9 +39,32 @@ cp_status check_cache(const cp_kv_cache* c) {
 
 // Axis and exponent of every pair, and its turns per position as a 64-bit
 // binary fraction (whole turns fall away: positions are whole numbers).
+// The table of the last rotation is kept (by its contents): 64 powers cost
+// as much host time as the launch.
+cp_status make_turns(const cp_rope* r, int32_t head_dim, RopeTurns* t);
+
 cp_status fill_turns(const cp_rope* r, int32_t head_dim, RopeTurns* t) {
+  static thread_local cp_rope last = {};
+  static thread_local int32_t last_dim = 0;
+  static thread_local RopeTurns kept;
   *t = RopeTurns{};
   if (!r) return CP_OK;
+  const bool same = last_dim == head_dim && last.n_axes == r->n_axes && last.base == r->base &&
+                    last.interleaved == r->interleaved && last.restart == r->restart &&
+                    last.adjacent == r->adjacent && std::memcmp(last.section, r->section, sizeof(r->section)) == 0;
+  if (!same) {
+    last_dim = 0;
+    const cp_status st = make_turns(r, head_dim, &kept);
+    if (st != CP_OK) return st;
+    last = *r;
+    last_dim = head_dim;
+  }
+  *t = kept;
+  return CP_OK;
+}
+
+cp_status make_turns(const cp_rope* r, int32_t head_dim, RopeTurns* t) {
+  *t = RopeTurns{};
   if (r->n_axes < 1 || r->n_axes > 4 || !(r->base > 0.f) || !std::isfinite(r->base)) return CP_ERR_INVALID_ARG;
   int32_t pairs = 0, left[4] = {}, seen[4] = {};
   for (int i = 0; i < r->n_axes; ++i) {
