@@ -498,7 +498,7 @@ def kv_extend(page_size: int, block_table, lens, add, free_pages, n_free, max_ro
     rows_at = at + 4 * (2 * n + 2)
     _check(lib().cp_kv_extend(n, width, page_size, max_rows, pool, *args, at, at + 4 * n, rows_at,
                               rows_at + 4 * max_rows, rows_at - 4, s), "cp_kv_extend")
-    lens_out, cu, n_free_out, slots, pos = torch.split_with_sizes(out, (n, n + 1, 1, max_rows, max_rows))
+    lens_out, cu, n_free_out, slots, pos = torch.unsafe_split_with_sizes(out, (n, n + 1, 1, max_rows, max_rows))
     return lens_out, cu, slots, pos, n_free_out
 
 

@@ -17,7 +17,7 @@
 //             slice of a stage's keys and its own running maximum, sum and O, so
 //             no barrier stands between them; at the end of a piece it leaves its state
 //             in shared memory and goes on with the next one;
-//   joiner    joins the workers' states of a piece and writes it out meanwhile.
+//   joiners   join the workers' states of a piece and write it out meanwhile.
 // Pages that no row sees are loaded from outside the map: zeros, without
 // touching memory.  Keys outside a tile's range that share a page with others
 // are masked out of S, and their V is masked to zero before the second product (0 times
@@ -72,6 +72,8 @@ __device__ __forceinline__ void mma16816(float* c, const uint32_t* a, uint32_t b
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+
+constexpr int kJoiners = 3;  // with the producer they make the 12 warps that 168 registers allow
 
 // What the rows of a tile need to know of a piece, in shared memory.
 struct PieceInfo {
@@ -295,7 +297,8 @@ struct SliceBf16 {
   // Joins the workers' states at `st` (float4s [worker][kAcc / 4 + kRows / 2][lane])
   // and writes them out.  Loops stay loops: one warp runs this once per
   // piece, and unrolled it waited for its own instructions (4 to 9 us a piece, 1 us so).
-  static __device__ __forceinline__ void join(const PagedArgs& a, const PieceInfo& p, const float4* st, int lane) {
+  static __device__ __forceinline__ void join(const PagedArgs& a, const PieceInfo& p, const float4* st, int part,
+                                              int lane) {
 #pragma unroll 1
     for (int i = 0; i < MT; ++i) {  // this lane's rows 8 * 2 i + lane / 4 and 8 further
       const SliceOut<T, D, R> out0(a, p, (lane >> 2) + 16 * i), out1(a, p, (lane >> 2) + 16 * i + 8);
@@ -314,13 +317,13 @@ struct SliceBf16 {
         l0 = fmaf(x[w].z, c0[w], l0);
         l1 = fmaf(x[w].w, c1[w], l1);
       }
-      if ((lane & 3) == 0) {
+      if (part == 0 && (lane & 3) == 0) {
         out0.put_lse(l0 > 0.f ? t0 + tc::lg2(l0) : -INFINITY);
         out1.put_lse(l1 > 0.f ? t1 + tc::lg2(l1) : -INFINITY);
       }
       const float v0 = l0 > 0.f ? 1.f / l0 : 0.f, v1 = l1 > 0.f ? 1.f / l1 : 0.f;
 #pragma unroll 2
-      for (int n = 0; n < NT; ++n) {
+      for (int n = part; n < NT; n += kJoiners) {
         float o0[2] = {}, o1[2] = {};
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
@@ -496,49 +499,37 @@ struct SliceF32 {
     }
   }
 
-  static __device__ __forceinline__ void join(const PagedArgs& a, const PieceInfo& p, const float4* st, int lane) {
+  static __device__ __forceinline__ void join(const PagedArgs& a, const PieceInfo& p, const float4* st, int part,
+                                              int lane) {
+    constexpr int kAt = D == 128 ? 1 : 2;  // rows at once: a row's columns take 32 lanes or 16
 #pragma unroll 1
-    for (int i = 0; i < R / 2; ++i) {  // rows 2 i, 2 i + 1
-      const SliceOut<T, D, R> out0(a, p, 2 * i), out1(a, p, 2 * i + 1);
-      float4 x[kWarps];
-      float t0 = -INFINITY, t1 = -INFINITY, l0 = 0.f, l1 = 0.f;
+    for (int i = part * kAt; i < R; i += kJoiners * kAt) {
+      const int r = D == 128 ? i : i + (lane >> 4), c = D == 128 ? lane : lane & 15;
+      const SliceOut<T, D, R> out(a, p, r);
+      float2 x[kWarps];  // m and l
+      float top = -INFINITY, sum = 0.f;
+      const float* ml = reinterpret_cast<const float*>(st + kAcc / 4 * 32) + (r >> 1) * 4 + (r & 1);
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
-        x[w] = st[w * kState + kAcc / 4 * 32 + i];
-        t0 = fmaxf(t0, x[w].x);
-        t1 = fmaxf(t1, x[w].y);
+        x[w] = make_float2(ml[w * kState * 4], ml[w * kState * 4 + 2]);
+        top = fmaxf(top, x[w].x);
       }
-      float o0[4] = {}, o1[4] = {};
+      float o[4] = {};
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
-        const float c0 = x[w].x == -INFINITY ? 0.f : exp2f(x[w].x - t0);
-        const float c1 = x[w].y == -INFINITY ? 0.f : exp2f(x[w].y - t1);
-        l0 = fmaf(x[w].z, c0, l0);
-        l1 = fmaf(x[w].w, c1, l1);
-        const float4 y = st[w * kState + (2 * i) * 32 + lane], z = st[w * kState + (2 * i + 1) * 32 + lane];
-        o0[0] = fmaf(y.x, c0, o0[0]);
-        o0[1] = fmaf(y.y, c0, o0[1]);
-        o0[2] = fmaf(y.z, c0, o0[2]);
-        o0[3] = fmaf(y.w, c0, o0[3]);
-        o1[0] = fmaf(z.x, c1, o1[0]);
-        o1[1] = fmaf(z.y, c1, o1[1]);
-        o1[2] = fmaf(z.z, c1, o1[2]);
-        o1[3] = fmaf(z.w, c1, o1[3]);
+        const float f = x[w].x == -INFINITY ? 0.f : exp2f(x[w].x - top);
+        sum = fmaf(x[w].y, f, sum);
+        const float4 y = st[w * kState + r * 32 + c];
+        o[0] = fmaf(y.x, f, o[0]);
+        o[1] = fmaf(y.y, f, o[1]);
+        o[2] = fmaf(y.z, f, o[2]);
+        o[3] = fmaf(y.w, f, o[3]);
       }
-      const float v0 = l0 > 0.f ? 1.f / l0 : 0.f, v1 = l1 > 0.f ? 1.f / l1 : 0.f;
+      const float inv = sum > 0.f ? 1.f / sum : 0.f;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        o0[e] *= v0;
-        o1[e] *= v1;
-      }
-      if (4 * lane < D) {
-        out0.template put<4>(4 * lane, o0);
-        out1.template put<4>(4 * lane, o1);
-      }
-      if (lane == 0) {
-        out0.put_lse(l0 > 0.f ? t0 + log2f(l0) : -INFINITY);
-        out1.put_lse(l1 > 0.f ? t1 + log2f(l1) : -INFINITY);
-      }
+      for (int e = 0; e < 4; ++e) o[e] *= inv;
+      out.template put<4>(4 * c, o);
+      if (c == 0) out.put_lse(sum > 0.f ? top + log2f(sum) : -INFINITY);
     }
   }
   __device__ __forceinline__ void leave(float4* st, int warp, int lane) const {
@@ -562,7 +553,7 @@ struct SliceLayout {
   static constexpr int kQBytes = (S::kQBytes + 127) & ~127;
   static constexpr int kOffP = kOffQ + S::kPieces * kQBytes;
   static constexpr int kBytes = kOffP + S::kWarps * S::kScratch;
-  static constexpr int kThreads = (S::kWarps + 2) * 32;
+  static constexpr int kThreads = (S::kWarps + kJoiners + 1) * 32;
   static_assert(kBytes + 2048 <= 232448, "shared memory of one block");
 };
 
@@ -619,7 +610,7 @@ __global__ void __launch_bounds__(SliceLayout<S, D, R>::kThreads, 1)
 
   grid_launch_dependents();
   if (tid == 0) {
-    for (int i = 0; i < 3 * kPieces; ++i) tc::mbar_init(tc::smem_u32(s_bar + i), i / kPieces == 1 ? 32 : 1);
+    for (int i = 0; i < 3 * kPieces; ++i) tc::mbar_init(tc::smem_u32(s_bar + i), i / kPieces == 1 ? 32 : (i / kPieces == 2 ? kJoiners : 1));
     for (int i = 0; i < NS; ++i) {
       tc::mbar_init(bar_full(i), 1);
       tc::mbar_init(bar_empty(i), S::kPerStage);
@@ -634,28 +625,43 @@ __global__ void __launch_bounds__(SliceLayout<S, D, R>::kThreads, 1)
   const int64_t u0 = share.first(blockIdx.x), u1 = share.first(blockIdx.x + 1);
   if (u1 <= u0) return;
 
-  if (warp == W + 1) {
+  if (warp == W + kJoiners) {
     // ---------------------------------------------------------- producer --
     PagedWalk<kSliceUnit, kSliceExtra> walk;
     walk.start(a, s_start, u1 - u0, blockIdx.x);
-    const int bs = sp.box_shift, box = 1 << bs;
+    const int bs = sp.box_shift, box = 1 << bs, nb = SK >> bs;  // keys of a box, boxes of a stage's keys
+    const int sub = (lane & 15) / CB, col = (lane & 15) % CB;   // this lane's box: K on lanes 0 .. 15, V on 16 .. 31
+    const bool mine = sub < nb;
+    struct Next {
+      PieceInfo i;
+      int32_t r;
+    };
+    auto come = [&]() {
+      Next x;
+      x.i.valid = 0;
+      x.i.nrows = x.i.n = 0;
+      x.i.lo = x.i.hi = x.i.key0 = 0;
+      x.r = 0;
+      PagedPiece p;
+      if (walk.next(a, p)) {
+        x.i = piece_info<SK>(a, p);
+        x.r = p.r;
+      }
+      return x;
+    };
+    // Pages of 32 boxes from box f of a piece on, one per lane (n_pages where
+    // no row sees a key of it): asked for a window, or a piece, ahead of their use.
+    auto seen = [&](const PieceInfo& i, int key) { return key < i.hi && key + box > i.lo; };
+    auto window = [&](const Next& x, int f) -> int32_t {
+      const int key = x.i.key0 + ((f + lane) << bs);
+      return seen(x.i, key) ? a.table[int64_t(x.r) * a.max_blocks + (key >> a.page_shift)] : a.n_pages;
+    };
     uint32_t g = 0;
     bool ok = true;
+    Next at = come();
+    int32_t pages = window(at, 0);
     for (int k = 0; ok; ++k) {
-      PagedPiece p;
-      PieceInfo i;
-      i.valid = 0;
-      i.nrows = 0;
-      if (walk.next(a, p)) i = piece_info<SK>(a, p);
-      // page of the box that lane l < 8 (16 for K, V) loads in the stage of key0: n_pages where no row sees a key of it
-      auto seen = [&](int key) { return key < i.hi && key + box > i.lo; };
-      const int sub = (lane & 15) / CB, col = (lane & 15) % CB;  // this lane's box: K on lanes 0 .. 15, V on 16 .. 31
-      const bool mine = (sub << bs) < SK;
-      auto page = [&](int key0) -> int32_t {
-        const int key = key0 + (sub << bs);
-        return mine && seen(key) ? a.table[int64_t(p.r) * a.max_blocks + (key >> a.page_shift)] : a.n_pages;
-      };
-      int32_t pg = i.valid && i.n > 0 ? page(i.key0) : a.n_pages;
+      const PieceInfo& i = at.i;
       if (k >= kPieces && !wait(bar_joined(k), phase(k) ^ 1)) break;
       if (lane == 0) {
         s_piece[k % kPieces] = i;
@@ -669,29 +675,42 @@ __global__ void __launch_bounds__(SliceLayout<S, D, R>::kThreads, 1)
         cp_async16(sbase + L::kOffQ + (k % kPieces) * L::kQBytes + S::q_at(r, c), static_cast<const T*>(a.q) + off, in);
       }
       asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar_q(k)) : "memory");
-      for (int t = 0; t < i.n; ++t, ++g) {
-        const int key0 = i.key0 + t * SK;
-        const int32_t now = pg;
-        if (t + 1 < i.n) pg = page(key0 + SK);
-        ok = wait(bar_empty(g), ((g / NS) & 1) ^ 1);
-        if (!ok) break;
-        if (lane == 0) tc::mbar_arrive_expect_tx(bar_full(g), L::kStageBytes);
-        __syncwarp();
-        if (mine) {
-          const int key = key0 + (sub << bs);
-          int32_t at = now;
-          if (uint32_t(at) >= uint32_t(a.n_pages)) {
-            if (seen(key) && a.err) atomicCAS(a.err, 0, kErrBadPage);
-            at = a.n_pages;
+      int32_t more = i.n * nb > 32 ? window(at, 32) : a.n_pages;
+      Next ahead;
+      int32_t ahead_pages = 0;
+      for (int t = 0; t < i.n || t == 0; ++t) {
+        if (t < i.n) {
+          const int f = t * nb;
+          if (f > 0 && (f & 31) == 0) {
+            pages = more;
+            if (i.n * nb > f + 32) more = window(at, f + 32);
           }
-          const int token = key & ((1 << a.page_shift) - 1);
-          const uint32_t dst = sbase + L::kOffRing + (g % NS) * L::kStageBytes +
-                               (lane < 16 ? 0 : L::kStageBytes / 2) + col * (SK * 128) + ((sub << bs) * 128);
-          const CUtensorMap* map = lane < 16 ? &sp.tmk : &sp.tmv;
-          tma_load_4d(dst, map, bar_full(g), col * (128 / int(sizeof(T))), sp.head_inner ? i.h : token,
-                      sp.head_inner ? token : i.h, at);
+          ok = wait(bar_empty(g), ((g / NS) & 1) ^ 1);
+          if (!ok) break;
+          if (lane == 0) tc::mbar_arrive_expect_tx(bar_full(g), L::kStageBytes);
+          int32_t page = __shfl_sync(0xffffffffu, pages, (f + sub) & 31);
+          if (mine) {
+            const int key = i.key0 + t * SK + (sub << bs);
+            if (uint32_t(page) >= uint32_t(a.n_pages)) {
+              if (seen(i, key) && a.err) atomicCAS(a.err, 0, kErrBadPage);
+              page = a.n_pages;
+            }
+            const int token = key & ((1 << a.page_shift) - 1);
+            const uint32_t dst = sbase + L::kOffRing + (g % NS) * L::kStageBytes +
+                                 (lane < 16 ? 0 : L::kStageBytes / 2) + col * (SK * 128) + ((sub << bs) * 128);
+            const CUtensorMap* map = lane < 16 ? &sp.tmk : &sp.tmv;
+            tma_load_4d(dst, map, bar_full(g), col * (128 / int(sizeof(T))), sp.head_inner ? i.h : token,
+                        sp.head_inner ? token : i.h, page);
+          }
+          ++g;
+        }
+        if (t == 0) {  // the next piece, and its first pages, behind this one's first stage
+          ahead = come();
+          ahead_pages = window(ahead, 0);
         }
       }
+      at = ahead;
+      pages = ahead_pages;
     }
     // Every copy has landed before the block ends (the workers wait for theirs
     // unless a wait gave up).
@@ -704,14 +723,14 @@ __global__ void __launch_bounds__(SliceLayout<S, D, R>::kThreads, 1)
   }
 
   float4* states = reinterpret_cast<float4*>(smem + L::kOffState);
-  if (warp == W) {
+  if (warp >= W) {
     // ------------------------------------------------------------ joiner --
     for (int k = 0;; ++k) {
       if (!wait(bar_piece(k), phase(k))) break;
       const PieceInfo& p = s_piece[k % kPieces];
       if (!p.valid) break;
       if (!wait(bar_state, uint32_t(k) & 1u)) break;
-      S::join(a, p, states, lane);
+      S::join(a, p, states, warp - W, lane);
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(bar_joined(k));
     }
@@ -795,26 +814,43 @@ __global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const __grid
   for (int i = warp; i < kMergeRows; i += kMergeThreads / 32) {
     const int r = blockIdx.y * kMergeRows + i;
     if (r >= t.nrows) break;
-    float top = -INFINITY;
+    // the first pieces' O is asked for together with their weights
+    constexpr int kEager = 4;
+    float x[kEager][N];
+#pragma unroll
+    for (int j = 0; j < kEager; ++j)
+      if (j < n) load_vec<float, N>(a.part_o + (slot(j) * a.R + r) * D + N * lane, x[j]);
     const float first = lane < n ? a.part_l[slot(lane) * a.R + r] : -INFINITY;  // the whole of it, up to 32 pieces
-    top = first;
+    float top = first;
     for (int e = 32 + lane; e < n; e += 32) top = fmaxf(top, a.part_l[slot(e) * a.R + r]);
     top = warp_max(top);
     float acc[N] = {};
     float sum = 0.f;
-    if (top != -INFINITY) {
+    if (top != -INFINITY) {  // an empty state's O is 0
       for (int e0 = 0; e0 < n; e0 += 32) {
         const float l = e0 == 0 ? first : (e0 + lane < n ? a.part_l[slot(e0 + lane) * a.R + r] : -INFINITY);
         const float w = exp2f(l - top);
         const int m = min(32, n - e0);
+        int j0 = 0;
+        if (e0 == 0) {
+          j0 = min(kEager, m);
+#pragma unroll
+          for (int j = 0; j < kEager; ++j) {
+            if (j >= n) break;
+            const float we = __shfl_sync(0xffffffffu, w, j);
+            sum += we;
+#pragma unroll
+            for (int v = 0; v < N; ++v) acc[v] = fmaf(we, x[j][v], acc[v]);
+          }
+        }
 #pragma unroll 8
-        for (int j = 0; j < m; ++j) {
+        for (int j = j0; j < m; ++j) {
           const float we = __shfl_sync(0xffffffffu, w, j);
-          float x[N];
-          load_vec<float, N>(a.part_o + (slot(e0 + j) * a.R + r) * D + N * lane, x);  // an empty state's O is 0
+          float y[N];
+          load_vec<float, N>(a.part_o + (slot(e0 + j) * a.R + r) * D + N * lane, y);
           sum += we;
 #pragma unroll
-          for (int v = 0; v < N; ++v) acc[v] = fmaf(we, x[v], acc[v]);
+          for (int v = 0; v < N; ++v) acc[v] = fmaf(we, y[v], acc[v]);
         }
       }
     }
