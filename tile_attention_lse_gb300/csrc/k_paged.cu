@@ -144,6 +144,7 @@ struct SliceBf16 {
   using T = __nv_bfloat16;
   static constexpr int kWarps = 8, kPerStage = 4, kKeys = 16, kStages = D == 128 ? 4 : 8;  // kPerStage: workers of a stage
   static constexpr int kStageKeys = kPerStage * kKeys;
+  static __device__ __forceinline__ int first_key(int warp) { return (warp % kPerStage) * kKeys; }  // a worker's slice of a stage
   static constexpr int MT = R / 16, NT = D / 8;
   static constexpr int kAcc = MT * NT * 4, kRows = MT * 2;  // accumulators and rows of a thread
   static constexpr int kQBytes = R * D * 2;
@@ -162,7 +163,7 @@ struct SliceBf16 {
     return uint32_t((c >> 3) * (kStageKeys * 128) + r * 128 + (((c ^ r) & 7) << 4));
   }
 
-  __device__ __forceinline__ void begin(const PagedArgs& a, const PieceInfo& p, uint32_t sq, int lane) {
+  __device__ __forceinline__ void begin(const PagedArgs& a, const PieceInfo& p, uint32_t sq, int, int lane) {
 #pragma unroll
     for (int i = 0; i < kAcc; ++i) acc[i] = 0.f;
 #pragma unroll
@@ -353,23 +354,26 @@ struct SliceBf16 {
 };
 
 // --------------------------------------------------------- float32: FFMA ---
-// A worker has a stage of 32 keys to itself.  First product: a lane owns a key
-// and all R rows of Q come by broadcast, so nothing is summed across lanes and every
+// A stage of 32 keys is one worker's, or two workers' with half of the tile's
+// rows each.  First product: a lane owns a key
+// and the rows of Q come by broadcast, so nothing is summed across lanes and every
 // exponential is formed once; P changes hands through shared memory, and in the second product a lane
 // owns 4 columns (head_dim 64: of half of the keys).
 template <int D, int R>
 struct SliceF32 {
   using T = float;
-  static constexpr int kWarps = 8, kPerStage = 1, kKeys = 32, kStages = D == 128 ? 4 : 8;
+  static constexpr int RW = R < 8 ? R : 8;  // rows of a worker
+  static constexpr int kWarps = R < 8 ? 4 : 8, kPerStage = R / RW, kKeys = 32, kStages = D == 128 ? 4 : 8;
   static constexpr int kStageKeys = kKeys;
-  static constexpr int kAcc = 4 * R;
+  static __device__ __forceinline__ int first_key(int) { return 0; }
+  static constexpr int kAcc = 4 * RW;
   static constexpr int kQBytes = R * D * 4;
-  static constexpr int kScratch = kKeys * R * 4;        // P of a worker's slice
-  static constexpr int kState = kAcc / 4 * 32 + R / 2;  // float4s of a worker's state; m and l are the same in every lane
-  static constexpr int kPieces = D == 128 ? 2 : 4;      // pieces that the producer is ahead (their Q fills the rest of shared memory)
-  float acc[kAcc];
-  float m[R], l[R];
-  int32_t pos0, row0, kv;
+  static constexpr int kScratch = kKeys * RW * 4;  // P of a worker's slice
+  static constexpr int kState = RW * 32 + RW / 2;  // float4s of a worker's state; m and l are the same in every lane
+  static constexpr int kPieces = 4;                // pieces that the producer is ahead
+  uint64_t acc[kAcc / 2];  // [row pair][column] of (row, row + 1): packed float32 pairs, two FMAs an instruction
+  float m[RW], l[RW];
+  int32_t pos0, row0, kv, first;  // first: this worker's first row of the tile
 
   static __device__ __forceinline__ uint32_t at(int r, int c) {
     return uint32_t((c >> 3) * (kStageKeys * 128) + r * 128 + (((c ^ r) & 7) << 4));
@@ -377,114 +381,119 @@ struct SliceF32 {
   static __device__ __forceinline__ uint32_t q_at(int r, int c) { return uint32_t(r * D * 4 + (c << 4)); }
   // P of rows r .. r + 3 for a key, swizzled so that 8 lanes' keys fall on different banks
   static __device__ __forceinline__ float4* p_at(float* sp, int key, int r) {
-    return reinterpret_cast<float4*>(sp + key * R) + (R == 16 ? (r / 4) ^ ((key >> 1) & 3) : r / 4);
+    return reinterpret_cast<float4*>(sp + key * RW) + (RW == 8 ? (r / 4) ^ ((key >> 2) & 1) : r / 4);
   }
-  static __device__ __forceinline__ float4 lds4(uint32_t addr) {
-    float4 v;
-    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
-                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-                 : "r"(addr)
-                 : "memory");
-    return v;
+  static __device__ __forceinline__ void lds2(uint32_t addr, uint64_t& lo, uint64_t& hi) {
+    asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(lo), "=l"(hi) : "r"(addr) : "memory");
   }
 
-  __device__ __forceinline__ void begin(const PagedArgs&, const PieceInfo& p, uint32_t, int) {
+  __device__ __forceinline__ void begin(const PagedArgs&, const PieceInfo& p, uint32_t, int warp, int) {
 #pragma unroll
-    for (int i = 0; i < kAcc; ++i) acc[i] = 0.f;
+    for (int i = 0; i < kAcc / 2; ++i) acc[i] = 0;
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
+    for (int r = 0; r < RW; ++r) {
       m[r] = -INFINITY;
       l[r] = 0.f;
     }
     pos0 = p.pos0;
-    row0 = p.row0;
+    first = (warp % kPerStage) * RW;
+    row0 = p.row0 + first;
     kv = p.kv;
   }
 
   __device__ __forceinline__ void slice(const PagedArgs& a, uint32_t sq, uint32_t sk, uint32_t sv, int srow, float* sp,
                                         int key, bool full, int klo, int khi, int lane) {
-    constexpr int RB = R < 8 ? R : 8;  // rows whose Q is in registers at once
-    float s[R];
+    uint64_t s2[RW];                   // sums over even and odd elements of the head
 #pragma unroll
-    for (int r = 0; r < R; ++r) s[r] = 0.f;
+    for (int r = 0; r < RW; ++r) s2[r] = 0;
 #pragma unroll 2
     for (int c = 0; c < D / 4; ++c) {
-      const float4 k = lds4(sk + at(srow + lane, c));
+      uint64_t k0, k1;
+      lds2(sk + at(srow + lane, c), k0, k1);
+      uint64_t q0[RW], q1[RW];
 #pragma unroll
-      for (int r0 = 0; r0 < R; r0 += RB) {
-        float4 q[RB];
+      for (int r = 0; r < RW; ++r) lds2(sq + q_at(first + r, c), q0[r], q1[r]);
 #pragma unroll
-        for (int r = 0; r < RB; ++r) q[r] = lds4(sq + q_at(r0 + r, c));
+      for (int r = 0; r < RW; ++r) s2[r] = tc::ffma2(q0[r], k0, s2[r]);
 #pragma unroll
-        for (int r = 0; r < RB; ++r) s[r0 + r] = fmaf(q[r].x, k.x, s[r0 + r]);
+      for (int r = 0; r < RW; ++r) s2[r] = tc::ffma2(q1[r], k1, s2[r]);
+    }
+    float s[RW];
 #pragma unroll
-        for (int r = 0; r < RB; ++r) s[r0 + r] = fmaf(q[r].y, k.y, s[r0 + r]);
-#pragma unroll
-        for (int r = 0; r < RB; ++r) s[r0 + r] = fmaf(q[r].z, k.z, s[r0 + r]);
-#pragma unroll
-        for (int r = 0; r < RB; ++r) s[r0 + r] = fmaf(q[r].w, k.w, s[r0 + r]);
-      }
+    for (int r = 0; r < RW; ++r) {
+      float x, y;
+      tc::f32x2_split(s2[r], x, y);
+      s[r] = x + y;
     }
     const int j = key + lane;
     if (!full) {
 #pragma unroll
-      for (int r = 0; r < R; ++r) {
+      for (int r = 0; r < RW; ++r) {
         const int pos = pos0 + (row0 + r) / a.G;
         const bool see = j < kv && (!a.causal || j <= pos) && (a.window == 0 || pos - j < a.window);
         s[r] = see ? s[r] : -INFINITY;
       }
     }
-    float up[R];
+    float up[RW];
 #pragma unroll
-    for (int r = 0; r < R; ++r) up[r] = s[r];
+    for (int r = 0; r < RW; ++r) up[r] = s[r];
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1)
 #pragma unroll
-      for (int r = 0; r < R; ++r) up[r] = fmaxf(up[r], __shfl_xor_sync(0xffffffffu, up[r], o));
+      for (int r = 0; r < RW; ++r) up[r] = fmaxf(up[r], __shfl_xor_sync(0xffffffffu, up[r], o));
     bool grow = false;
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
+    for (int r = 0; r < RW; ++r) {
       up[r] *= a.scale_log2;
       grow |= up[r] > m[r] + 8.f;
     }
     if (grow) {  // the same in every lane
 #pragma unroll
-      for (int r = 0; r < R; ++r) {
-        const float t = fmaxf(m[r], up[r]);
-        const float c = m[r] == -INFINITY ? 0.f : exp2f(m[r] - t);
-        m[r] = t;
-        l[r] *= c;
+      for (int r = 0; r < RW; r += 2) {
+        float c[2];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) acc[4 * r + e] *= c;
+        for (int w = 0; w < 2; ++w) {
+          const float t = fmaxf(m[r + w], up[r + w]);
+          c[w] = m[r + w] == -INFINITY ? 0.f : exp2f(m[r + w] - t);
+          m[r + w] = t;
+          l[r + w] *= c[w];
+        }
+        const uint64_t c2 = tc::f32x2(c[0], c[1]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[2 * r + e] = tc::fmul2(acc[2 * r + e], c2);
       }
     }
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
+    for (int r = 0; r < RW; ++r) {
       const float base = m[r] == -INFINITY ? 0.f : m[r];
       s[r] = exp2f(fmaf(s[r], a.scale_log2, -base));
       l[r] += s[r];
     }
 #pragma unroll
-    for (int r = 0; r < R; r += 4) *p_at(sp, lane, r) = make_float4(s[r], s[r + 1], s[r + 2], s[r + 3]);
+    for (int r = 0; r < RW; r += 4) *p_at(sp, lane, r) = make_float4(s[r], s[r + 1], s[r + 2], s[r + 3]);
     __syncwarp();
     constexpr int kn = D == 128 ? kKeys : kKeys / 2;
     const int c = D == 128 ? lane : lane & 15, x0 = D == 128 ? 0 : (lane >> 4) * kn;
 #pragma unroll 4
     for (int i = 0; i < kn; ++i) {
       const int x = x0 + i;
-      float4 v = lds4(sv + at(srow + x, c));
-      if (!full && (key + x < klo || key + x >= khi)) v = make_float4(0.f, 0.f, 0.f, 0.f);
+      uint64_t v0, v1;
+      lds2(sv + at(srow + x, c), v0, v1);
+      if (!full && (key + x < klo || key + x >= khi)) v0 = v1 = 0;
+      float v[4];
+      tc::f32x2_split(v0, v[0], v[1]);
+      tc::f32x2_split(v1, v[2], v[3]);
+      uint64_t vv[4];
 #pragma unroll
-      for (int r = 0; r < R; r += 4) {
-        const float4 p = *p_at(sp, x, r);
-        const float pr[4] = {p.x, p.y, p.z, p.w};
+      for (int e = 0; e < 4; ++e) vv[e] = tc::f32x2(v[e], v[e]);
 #pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          float* o = acc + 4 * (r + t);
-          o[0] = fmaf(pr[t], v.x, o[0]);
-          o[1] = fmaf(pr[t], v.y, o[1]);
-          o[2] = fmaf(pr[t], v.z, o[2]);
-          o[3] = fmaf(pr[t], v.w, o[3]);
+      for (int r = 0; r < RW; r += 4) {
+        uint64_t p0, p1;  // rows r, r + 1 and r + 2, r + 3
+        lds2(tc::smem_u32(p_at(sp, x, r)), p0, p1);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          acc[2 * r + e] = tc::ffma2(p0, vv[e], acc[2 * r + e]);
+          acc[2 * r + 4 + e] = tc::ffma2(p1, vv[e], acc[2 * r + 4 + e]);
         }
       }
     }
@@ -492,10 +501,10 @@ struct SliceF32 {
 
   __device__ __forceinline__ void end() {
 #pragma unroll
-    for (int r = 0; r < R; ++r) l[r] = warp_sum(l[r]);
+    for (int r = 0; r < RW; ++r) l[r] = warp_sum(l[r]);
     if (D == 64) {
 #pragma unroll
-      for (int i = 0; i < kAcc; ++i) acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], 16);
+      for (int i = 0; i < kAcc / 2; ++i) acc[i] = tc::fadd2(acc[i], __shfl_xor_sync(0xffffffffu, acc[i], 16));
     }
   }
 
@@ -506,20 +515,23 @@ struct SliceF32 {
     for (int i = part * kAt; i < R; i += kJoiners * kAt) {
       const int r = D == 128 ? i : i + (lane >> 4), c = D == 128 ? lane : lane & 15;
       const SliceOut<T, D, R> out(a, p, r);
-      float2 x[kWarps];  // m and l
+      constexpr int W = kWarps / kPerStage;  // workers that hold the row: every kPerStage-th
+      const int rw = r % RW;
+      const float4* base = st + (r / RW) * kState;
+      float2 x[W];  // m and l
       float top = -INFINITY, sum = 0.f;
-      const float* ml = reinterpret_cast<const float*>(st + kAcc / 4 * 32) + (r >> 1) * 4 + (r & 1);
+      const float* ml = reinterpret_cast<const float*>(base + RW * 32) + (rw >> 1) * 4 + (rw & 1);
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        x[w] = make_float2(ml[w * kState * 4], ml[w * kState * 4 + 2]);
+      for (int w = 0; w < W; ++w) {
+        x[w] = make_float2(ml[w * kPerStage * kState * 4], ml[w * kPerStage * kState * 4 + 2]);
         top = fmaxf(top, x[w].x);
       }
       float o[4] = {};
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
+      for (int w = 0; w < W; ++w) {
         const float f = x[w].x == -INFINITY ? 0.f : exp2f(x[w].x - top);
         sum = fmaf(x[w].y, f, sum);
-        const float4 y = st[w * kState + r * 32 + c];
+        const float4 y = base[w * kPerStage * kState + rw * 32 + c];
         o[0] = fmaf(y.x, f, o[0]);
         o[1] = fmaf(y.y, f, o[1]);
         o[2] = fmaf(y.z, f, o[2]);
@@ -535,10 +547,16 @@ struct SliceF32 {
   __device__ __forceinline__ void leave(float4* st, int warp, int lane) const {
     float4* x = st + warp * kState + lane;
 #pragma unroll
-    for (int i = 0; i < kAcc / 4; ++i) x[i * 32] = make_float4(acc[4 * i], acc[4 * i + 1], acc[4 * i + 2], acc[4 * i + 3]);
+    for (int r = 0; r < RW; r += 2) {
+      float u[4], w[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) tc::f32x2_split(acc[2 * r + e], u[e], w[e]);
+      x[r * 32] = make_float4(u[0], u[1], u[2], u[3]);
+      x[(r + 1) * 32] = make_float4(w[0], w[1], w[2], w[3]);
+    }
     if (lane == 0) {
 #pragma unroll
-      for (int i = 0; i < R / 2; ++i) x[kAcc / 4 * 32 + i] = make_float4(m[2 * i], m[2 * i + 1], l[2 * i], l[2 * i + 1]);
+      for (int i = 0; i < RW / 2; ++i) x[RW * 32 + i] = make_float4(m[2 * i], m[2 * i + 1], l[2 * i], l[2 * i + 1]);
     }
   }
 };
@@ -562,6 +580,7 @@ struct SliceParams {
   PagedArgs a;
   int32_t box_shift;     // log2 keys of a box
   int32_t head_inner;    // the head dimension comes before the token dimension
+  int32_t after_pair;
 };
 
 __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int c0, int c1, int c2,
@@ -582,6 +601,9 @@ __global__ void __launch_bounds__(SliceLayout<S, D, R>::kThreads, 1)
   constexpr int V = 16 / int(sizeof(T));           // elements of a Q copy
   constexpr int CH = D / V;                        // Q copies of a row
   constexpr int CB = D * int(sizeof(T)) / 128;     // 128-byte columns of a row
+  // a slot of the ring is always the same workers', who wait for its phases in
+  // order (a phase's parity tells it only from the next one)
+  static_assert(NS % (W / S::kPerStage) == 0, "a worker's stages keep their slots");
   extern __shared__ __align__(1024) uint8_t smem[];
   __shared__ int64_t s_scan[32];
   __shared__ PagedStart s_start;
@@ -623,7 +645,10 @@ __global__ void __launch_bounds__(SliceLayout<S, D, R>::kThreads, 1)
   }
   const PagedShare share = paged_locate<kSliceUnit, kSliceExtra, L::kThreads>(a, s_scan, &s_start, blockIdx.x);
   const int64_t u0 = share.first(blockIdx.x), u1 = share.first(blockIdx.x + 1);
-  if (u1 <= u0) return;
+  if (u1 <= u0) {
+    if (sp.after_pair) grid_wait();
+    return;
+  }
 
   if (warp == W + kJoiners) {
     // ---------------------------------------------------------- producer --
@@ -719,6 +744,7 @@ __global__ void __launch_bounds__(SliceLayout<S, D, R>::kThreads, 1)
       for (uint32_t s = g > uint32_t(NS) ? g - NS : 0; s < g; ++s) tc::mbar_wait(bar_full(s), (s / NS) & 1, &never, nullptr);
     }
     cp_async_wait<0>();
+    if (sp.after_pair) grid_wait();  // this launch is complete only when the one before it is
     return;
   }
 
@@ -739,7 +765,7 @@ __global__ void __launch_bounds__(SliceLayout<S, D, R>::kThreads, 1)
 
   // -------------------------------------------------------------- worker --
   float* scratch = reinterpret_cast<float*>(smem + L::kOffP + warp * S::kScratch);
-  const int srow = (warp % S::kPerStage) * kKeys;
+  const int srow = S::first_key(warp);
   uint32_t g = 0;
   bool ok = true;
   S st;
@@ -749,15 +775,12 @@ __global__ void __launch_bounds__(SliceLayout<S, D, R>::kThreads, 1)
     if (!p.valid) break;
     if (!wait(bar_q(k), phase(k))) break;
     const uint32_t sq = sbase + L::kOffQ + (k % kPieces) * L::kQBytes;
-    st.begin(a, p, sq, lane);
+    st.begin(a, p, sq, warp, lane);
     const int n = p.n, lo = p.lo, hi = p.hi, full_lo = p.full_lo, full_hi = p.full_hi;
     int key = p.key0 + srow;
     for (int t = 0; t < n; ++t, ++g, key += SK) {
       if (int(g % (W / S::kPerStage)) != warp / S::kPerStage) continue;  // other workers' stage
-      // a phase can be told from the one two before it only once the one between is complete,
-      // which another worker's turn may have waited for
-      if (W / S::kPerStage > NS && g >= uint32_t(NS)) ok = wait(bar_full(g - NS), (g / NS - 1) & 1);
-      ok = ok && wait(bar_full(g), (g / NS) & 1);
+      ok = wait(bar_full(g), (g / NS) & 1);
       if (!ok) break;
       const uint32_t sk = sbase + L::kOffRing + (g % NS) * L::kStageBytes;
       if (key < hi && key + kKeys > lo)
@@ -776,6 +799,24 @@ __global__ void __launch_bounds__(SliceLayout<S, D, R>::kThreads, 1)
   }
 }
 
+// Launch that may start while the launch before it on the stream still runs
+// (it waits for that one itself: grid_wait).
+template <typename P>
+cp_status launch_early(void (*kern)(P), dim3 grid, dim3 block, int smem, bool early, cudaStream_t s, const P& p) {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = size_t(smem);
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = early ? 1 : 0;
+  if (cudaLaunchKernelEx(&cfg, kern, p) != cudaSuccess) return CP_ERR_CUDA;
+  return cuda_status(cudaGetLastError());
+}
+
 // ---------------------------------------------------------------- merge ---
 // One tile that starts in block c and goes on behind it: its partial states
 // are the blocks' from c on.  O = sum_e w_e O_e / sum_e w_e, w_e = 2^(L_e - max L),
@@ -783,10 +824,7 @@ __global__ void __launch_bounds__(SliceLayout<S, D, R>::kThreads, 1)
 constexpr int kMergeThreads = 128, kMergeRows = 16;
 
 template <typename T, int D, int U, int E>
-__global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const __grid_constant__ PagedArgs a) {
-  __shared__ int64_t s_scan[32];
-  __shared__ PagedStart s_start;
-  const int c = blockIdx.x;
+__device__ __forceinline__ void merge_block(const PagedArgs& a, int c, int64_t* s_scan, PagedStart& s_start) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const PagedShare share = paged_locate<U, E, kMergeThreads>(a, s_scan, &s_start, c + 1);
   const int64_t u0 = share.first(c), u1 = share.first(c + 1);
@@ -864,8 +902,23 @@ __global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const __grid
   }
 }
 
+struct MergeParams {
+  PagedArgs pair, slice;
+};
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const __grid_constant__ MergeParams p) {
+  __shared__ int64_t s_scan[32];
+  __shared__ PagedStart s_start;
+  const int c = blockIdx.x;
+  if constexpr (D == 128 && sizeof(T) == 2) {
+    if (c < p.pair.grid) return merge_block<T, D, kPairUnit, kPairExtra>(p.pair, c, s_scan, s_start);
+  }
+  merge_block<T, D, kSliceUnit, kSliceExtra>(p.slice, c - p.pair.grid, s_scan, s_start);
+}
+
 template <typename S, int D, int R>
-cp_status run_slice(const PagedArgs& a, cudaStream_t s) {
+cp_status run_slice(const PagedArgs& a, bool after_pair, cudaStream_t s) {
   using L = SliceLayout<S, D, R>;
   auto* kern = paged_slice_kernel<S, D, R>;
   static std::atomic<bool> ready[64] = {};  // per device (an idempotent first set-up)
@@ -883,54 +936,45 @@ cp_status run_slice(const PagedArgs& a, cudaStream_t s) {
   p.a = a;
   p.box_shift = 0;
   while ((1 << p.box_shift) < box) ++p.box_shift;
-  kern<<<unsigned(a.grid), L::kThreads, L::kBytes, s>>>(p);
-  return cuda_status(cudaGetLastError());
+  p.after_pair = after_pair;
+  return launch_early(kern, dim3(unsigned(a.grid)), dim3(L::kThreads), L::kBytes, after_pair, s, p);
 }
 
-template <typename T, int D, int U, int E>
-cp_status run_merge(const PagedArgs& a, cudaStream_t s) {
-  cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.gridDim = dim3(unsigned(a.grid), unsigned((a.R + kMergeRows - 1) / kMergeRows));
-  cfg.blockDim = dim3(kMergeThreads);
-  cfg.stream = s;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, paged_merge_kernel<T, D, U, E>, a) != cudaSuccess) return CP_ERR_CUDA;
-  return cuda_status(cudaGetLastError());
+template <typename T, int D>
+cp_status run_merge(const PagedArgs& pair, const PagedArgs& slice, cudaStream_t s) {
+  const int rows = pair.grid > 0 ? pair.R : slice.R;  // the pair's tiles have more rows
+  return launch_early(paged_merge_kernel<T, D>, dim3(unsigned(pair.grid + slice.grid), unsigned((rows + kMergeRows - 1) / kMergeRows)),
+                      dim3(kMergeThreads), 0, true, s, MergeParams{pair, slice});
 }
 
 }  // namespace
 
 int paged_slice_grid() { return num_sms(); }
 
-cp_status launch_paged_slice(const PagedArgs& a, PagedKernel k, cudaStream_t s) {
+cp_status launch_paged_slice(const PagedArgs& a, PagedKernel k, bool after_pair, cudaStream_t s) {
   if (a.dtype == CP_BF16) {
     if (k == kPagedSlice16)
-      return a.d == 128 ? run_slice<SliceBf16<128, 16>, 128, 16>(a, s) : run_slice<SliceBf16<64, 16>, 64, 16>(a, s);
+      return a.d == 128 ? run_slice<SliceBf16<128, 16>, 128, 16>(a, after_pair, s)
+                        : run_slice<SliceBf16<64, 16>, 64, 16>(a, after_pair, s);
     if (k == kPagedSlice32)
-      return a.d == 64 ? run_slice<SliceBf16<64, 32>, 64, 32>(a, s) : CP_ERR_UNSUPPORTED;
+      return a.d == 64 ? run_slice<SliceBf16<64, 32>, 64, 32>(a, after_pair, s) : CP_ERR_UNSUPPORTED;
     return CP_ERR_UNSUPPORTED;
   }
   if (k == kPagedSlice4)
-    return a.d == 128 ? run_slice<SliceF32<128, 4>, 128, 4>(a, s) : run_slice<SliceF32<64, 4>, 64, 4>(a, s);
+    return a.d == 128 ? run_slice<SliceF32<128, 4>, 128, 4>(a, after_pair, s)
+                      : run_slice<SliceF32<64, 4>, 64, 4>(a, after_pair, s);
   if (k == kPagedSlice16)
-    return a.d == 128 ? run_slice<SliceF32<128, 16>, 128, 16>(a, s) : run_slice<SliceF32<64, 16>, 64, 16>(a, s);
+    return a.d == 128 ? run_slice<SliceF32<128, 16>, 128, 16>(a, after_pair, s)
+                      : run_slice<SliceF32<64, 16>, 64, 16>(a, after_pair, s);
   return CP_ERR_UNSUPPORTED;
 }
 
-cp_status launch_paged_merge(const PagedArgs& a, PagedKernel k, cudaStream_t s) {
-  if (k == kPagedPair) {
-    if (a.d != 128 || a.dtype != CP_BF16) return CP_ERR_UNSUPPORTED;
-    return run_merge<__nv_bfloat16, 128, kPairUnit, kPairExtra>(a, s);
-  }
+cp_status launch_paged_merge(const PagedArgs& pair, const PagedArgs& slice, cudaStream_t s) {
+  const PagedArgs& a = pair.grid > 0 ? pair : slice;
+  if (pair.grid > 0 && (a.d != 128 || a.dtype != CP_BF16)) return CP_ERR_UNSUPPORTED;
   if (a.dtype == CP_BF16)
-    return a.d == 128 ? run_merge<__nv_bfloat16, 128, kSliceUnit, kSliceExtra>(a, s)
-                      : run_merge<__nv_bfloat16, 64, kSliceUnit, kSliceExtra>(a, s);
-  return a.d == 128 ? run_merge<float, 128, kSliceUnit, kSliceExtra>(a, s)
-                    : run_merge<float, 64, kSliceUnit, kSliceExtra>(a, s);
+    return a.d == 128 ? run_merge<__nv_bfloat16, 128>(pair, slice, s) : run_merge<__nv_bfloat16, 64>(pair, slice, s);
+  return a.d == 128 ? run_merge<float, 128>(pair, slice, s) : run_merge<float, 64>(pair, slice, s);
 }
 
 }  // namespace cpattn

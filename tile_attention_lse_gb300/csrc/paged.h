@@ -38,6 +38,7 @@ struct PagedArgs {
   int32_t max_keys;  // max_blocks * page_size
   int32_t H, Hkv, G, d;
   int32_t R;  // packed rows of a tile
+  int32_t row_min, row_max;  // requests of fewer or more packed rows are another launch's
   int32_t causal, window;
   float scale_log2;  // softmax scale * log2(e)
   cp_dtype dtype;
@@ -64,6 +65,7 @@ CPATTN_HD PagedReq paged_req(const PagedArgs& a, int r) {
   PagedReq q;
   q.q0 = clamp_i32(a.cu[r], 0, int32_t(a.rows));
   q.nq = clamp_i32(a.cu[r + 1], q.q0, int32_t(a.rows)) - q.q0;
+  if (q.nq * a.G < a.row_min || q.nq * a.G > a.row_max) q.nq = 0;
   q.kv = clamp_i32(a.lens[r], 0, a.max_keys);
   return q;
 }
@@ -204,8 +206,11 @@ inline int paged_rows(PagedKernel k, int G) {
   return 16;
 }
 
-cp_status launch_paged_slice(const PagedArgs& a, PagedKernel k, cudaStream_t s);
-cp_status launch_paged_merge(const PagedArgs& a, PagedKernel k, cudaStream_t s);
+// after_pair: behind a pair launch on the same stream, whose blocks' last
+// moments it may overlap (and which is complete when it is).
+cp_status launch_paged_slice(const PagedArgs& a, PagedKernel k, bool after_pair, cudaStream_t s);
+// Joins the cut tiles of a pair launch, a slice launch or both (grid 0: none).
+cp_status launch_paged_merge(const PagedArgs& pair, const PagedArgs& slice, cudaStream_t s);
 int paged_slice_grid();
 cp_status launch_paged_pair(const PagedArgs& a, cudaStream_t s);
 // Pairs of SMs that can run at once (sets the kernel up on the first call).

@@ -93,19 +93,33 @@ cp_status make_turns(const cp_rope* r, int32_t head_dim, RopeTurns* t) {
   return CP_OK;
 }
 
-// The kernel of a call, by its types and by the packed rows of a request
-// (max_new * G).
-PagedKernel pick_kernel(const cp_paged_desc& d) {
+// The launches of a call, by its types and by the packed rows of a request
+// (max_new * G at most).  bf16 with head_dim 128: requests of up to 16 rows
+// run on the slice kernel (bound by their keys' bytes), those of more on the
+// pair kernel (bound by the products); where both may come, both are
+// launched, each for its own requests (measured on 20 single tokens and 4 chunks of
+// up to 509 over 6000 cached tokens: 250 us with all of them on the pair kernel).  A single
+// request of unknown length runs on the pair kernel whatever it brings.
+struct PagedPlan {
+  PagedKernel slice = kPagedSlice16;
+  bool use_slice = true, use_pair = false;
+};
+PagedPlan pick_kernels(const cp_paged_desc& d, int32_t n_reqs) {
   const int64_t G = d.heads_q / d.kv.heads_kv;
   const int64_t rows = d.max_new > 0 ? G * d.max_new : INT64_MAX;
-  if (d.kv.dtype == CP_F32) return rows <= 4 ? kPagedSlice4 : kPagedSlice16;
-  if (rows <= 16) return kPagedSlice16;
-  if (d.kv.head_dim == 64) return kPagedSlice32;
-  return G <= kPairRows ? kPagedPair : kPagedSlice16;
+  PagedPlan p;
+  if (d.kv.dtype == CP_F32) {
+    p.slice = rows <= 4 ? kPagedSlice4 : kPagedSlice16;
+  } else if (rows > 16) {
+    if (d.kv.head_dim == 64) {
+      p.slice = kPagedSlice32;
+    } else if (G <= kPairRows) {
+      p.use_pair = true;
+      p.use_slice = n_reqs > 1 && G <= 16;
+    }
+  }
+  return p;
 }
-
-// Blocks (pairs of blocks) that a launch has at most.
-int paged_grid(PagedKernel k) { return k == kPagedPair ? paged_slice_grid() / 2 : paged_slice_grid(); }
 
 cp_status check_paged(const cp_paged_desc* d) {
   if (!d) return CP_ERR_INVALID_ARG;
@@ -152,8 +166,45 @@ void walk_all(const PagedArgs& a, F f) {
   }
 }
 
-size_t part_floats(const cp_paged_desc& d, PagedKernel k) {
-  return size_t(2) * paged_grid(k) * paged_rows(k, d.heads_q / d.kv.heads_kv);
+// Partial states: two per block, the pair launch's in front of the slice launch's.
+int pair_blocks(const PagedPlan& p) { return p.use_pair ? paged_slice_grid() / 2 : 0; }
+int64_t pair_states(const cp_paged_desc& d, const PagedPlan& p) {
+  return int64_t(2) * pair_blocks(p) * paged_rows(kPagedPair, d.heads_q / d.kv.heads_kv);
+}
+int64_t slice_states(const cp_paged_desc& d, const PagedPlan& p) {
+  return p.use_slice ? int64_t(2) * paged_slice_grid() * paged_rows(p.slice, d.heads_q / d.kv.heads_kv) : 0;
+}
+
+// What both launches of a call share.
+PagedArgs paged_args(const cp_paged_desc& d, int32_t n_reqs, int64_t rows, int32_t max_blocks, const int32_t* cu,
+                     const int32_t* lens) {
+  PagedArgs a{};
+  a.cu = cu;
+  a.lens = lens;
+  a.n_reqs = n_reqs;
+  a.rows = rows;
+  a.max_blocks = max_blocks;
+  a.max_keys = max_blocks * d.kv.page_size;
+  a.H = d.heads_q;
+  a.Hkv = d.kv.heads_kv;
+  a.G = a.H / a.Hkv;
+  a.d = d.kv.head_dim;
+  a.dtype = d.kv.dtype;
+  a.causal = d.causal != 0;
+  a.window = d.window;
+  a.row_max = INT32_MAX;
+  return a;
+}
+void split_args(const PagedPlan& p, const PagedArgs& a, PagedArgs* pair, PagedArgs* slice) {
+  *pair = *slice = a;
+  pair->R = paged_rows(kPagedPair, p.use_pair ? a.G : 1);
+  slice->R = paged_rows(p.slice, a.G);
+  pair->grid = pair_blocks(p);
+  slice->grid = p.use_slice ? paged_slice_grid() : 0;
+  if (p.use_pair && p.use_slice) {
+    pair->row_min = 17;
+    slice->row_max = 16;
+  }
 }
 
 }  // namespace
@@ -300,7 +351,8 @@ cp_status cp_validate_paged_desc(const cp_paged_desc* desc) { return check_paged
 
 size_t cp_paged_attn_workspace_bytes(const cp_paged_desc* desc) {
   if (check_paged(desc) != CP_OK) return 0;
-  return part_floats(*desc, pick_kernel(*desc)) * (size_t(desc->kv.head_dim) + 1) * 4;
+  const PagedPlan p = pick_kernels(*desc, 2);  // the most that any number of requests takes
+  return size_t(pair_states(*desc, p) + slice_states(*desc, p)) * (size_t(desc->kv.head_dim) + 1) * 4;
 }
 
 cp_status cp_paged_schedule(const cp_paged_desc* desc, int32_t n_reqs, int64_t rows, int32_t max_blocks,
@@ -309,34 +361,23 @@ cp_status cp_paged_schedule(const cp_paged_desc* desc, int32_t n_reqs, int64_t r
   const cp_status st = check_paged(desc);
   if (st != CP_OK) return st;
   if (n_reqs < 1 || rows < 0 || max_blocks < 1 || !cu_new || !kv_lens) return CP_ERR_INVALID_ARG;
-  const PagedKernel kern = pick_kernel(*desc);
-  PagedArgs a{};
-  a.cu = cu_new;
-  a.lens = kv_lens;
-  a.n_reqs = n_reqs;
-  a.rows = rows;
-  a.max_blocks = max_blocks;
-  a.max_keys = max_blocks * desc->kv.page_size;
-  a.Hkv = desc->kv.heads_kv;
-  a.H = desc->heads_q;
-  a.G = a.H / a.Hkv;
-  a.R = paged_rows(kern, a.G);
-  a.causal = desc->causal != 0;
-  a.window = desc->window;
-  a.grid = paged_grid(kern);
-  if (grid) *grid = a.grid;
+  const PagedPlan plan = pick_kernels(*desc, n_reqs);
+  PagedArgs pair, slice;
+  split_args(plan, paged_args(*desc, n_reqs, rows, max_blocks, cu_new, kv_lens), &pair, &slice);
+  if (grid) *grid = pair.grid + slice.grid;
   int64_t count = 0;
+  int first = 0;
   auto f = [&](int c, const PagedPiece& p, int32_t k0, int32_t k1) {
     if (pieces) {
-      const int32_t row[8] = {c, p.r, p.h, p.tile.row0, p.tile.nrows, k0, k1, p.slot};
+      const int32_t row[8] = {first + c, p.r,  p.h, p.tile.row0, p.tile.nrows,
+                              k0,        k1, p.slot < 0 ? -1 : 2 * first + p.slot};
       for (int i = 0; i < 8; ++i) pieces[8 * count + i] = row[i];
     }
     ++count;
   };
-  if (kern == kPagedPair)
-    walk_all<kPairUnit, kPairExtra>(a, f);
-  else
-    walk_all<kSliceUnit, kSliceExtra>(a, f);
+  if (plan.use_pair) walk_all<kPairUnit, kPairExtra>(pair, f);
+  first = pair.grid;
+  if (plan.use_slice) walk_all<kSliceUnit, kSliceExtra>(slice, f);
   if (n) *n = count;
   return CP_OK;
 }
@@ -355,9 +396,10 @@ cp_status cp_paged_attn_fwd(const cp_paged_desc* desc, int32_t n_reqs, int64_t r
   if (!q || !block_table || !cu_new || !kv_lens || !o || !lse || !ws || !aligned(ws, 256)) return CP_ERR_INVALID_ARG;
   if (q_stride < int64_t(desc->heads_q) * c.head_dim) return CP_ERR_INVALID_ARG;
   if (!aligned(q, 16) || !aligned(o, 16) || !row_aligned(q_stride, c.dtype)) return CP_ERR_ALIGNMENT;
-  const PagedKernel kern = pick_kernel(*desc);
   if (ws_bytes < cp_paged_attn_workspace_bytes(desc)) return CP_ERR_WORKSPACE;
-  PagedArgs a{};
+  if (!tc_available()) return CP_ERR_UNSUPPORTED;
+  const PagedPlan plan = pick_kernels(*desc, n_reqs);
+  PagedArgs a = paged_args(*desc, n_reqs, rows, max_blocks, cu_new, kv_lens);
   a.q = q;
   a.q_stride = q_stride;
   a.k = c.k;
@@ -366,42 +408,36 @@ cp_status cp_paged_attn_fwd(const cp_paged_desc* desc, int32_t n_reqs, int64_t r
   a.token_stride = c.token_stride;
   a.head_stride = c.head_stride;
   a.table = block_table;
-  a.cu = cu_new;
-  a.lens = kv_lens;
   a.o = o;
   a.lse = lse;
-  a.part_o = static_cast<float*>(ws);
-  a.part_l = a.part_o + part_floats(*desc, kern) * c.head_dim;
-  a.n_reqs = n_reqs;
-  a.max_blocks = max_blocks;
   a.n_pages = c.n_pages;
   a.page_shift = log2_of(c.page_size);
-  a.rows = rows;
-  a.max_keys = max_blocks * c.page_size;
-  a.H = desc->heads_q;
-  a.Hkv = c.heads_kv;
-  a.G = a.H / a.Hkv;
-  a.d = c.head_dim;
-  a.R = paged_rows(kern, a.G);
-  a.causal = desc->causal != 0;
-  a.window = desc->window;
   const float scale = desc->softmax_scale > 0.f ? desc->softmax_scale : 1.f / std::sqrt(float(c.head_dim));
   a.scale_log2 = scale * 1.4426950408889634f;
-  a.dtype = c.dtype;
-  a.grid = paged_grid(kern);
   a.err = device_error_ptr();
-  if (kern == kPagedPair) {
-    const cp_status r = tc_available() ? paged_pair_grid(&a.grid) : CP_ERR_UNSUPPORTED;
+  PagedArgs pair, slice;
+  split_args(plan, a, &pair, &slice);
+  const int64_t states = pair_states(*desc, plan) + slice_states(*desc, plan);
+  pair.part_o = static_cast<float*>(ws);
+  pair.part_l = pair.part_o + states * c.head_dim;
+  slice.part_o = pair.part_o + pair_states(*desc, plan) * c.head_dim;
+  slice.part_l = pair.part_l + pair_states(*desc, plan);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cp_status r = CP_OK;
+  if (plan.use_pair) {
+    r = paged_pair_grid(&pair.grid);
+    if (r != CP_OK) return r;
+    ProfScope ps(CP_K_PAGED, s);
+    r = launch_paged_pair(pair, s);
     if (r != CP_OK) return r;
   }
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  {
+  if (plan.use_slice) {
     ProfScope ps(CP_K_PAGED, s);
-    const cp_status r = kern == kPagedPair ? launch_paged_pair(a, s) : launch_paged_slice(a, kern, s);
+    r = launch_paged_slice(slice, plan.slice, plan.use_pair, s);
     if (r != CP_OK) return r;
   }
   ProfScope ps(CP_K_PAGED_MERGE, s);
-  return launch_paged_merge(a, kern, s);
+  return launch_paged_merge(pair, slice, s);
 }
 
 }  // extern "C"
