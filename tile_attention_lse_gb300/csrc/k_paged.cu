@@ -10,9 +10,11 @@
 // What bounds it: a single token per request reads 4 d bytes (bf16) of K and V
 // per key and kv-head and does 8 d G flops on them, so HBM is the bound; the
 // kernel's job is to keep enough loads in flight on every SM.  Warps have parts:
-//   producer  walks the block's share, up to four pieces ahead, and loads it: Q
-//             by 16-byte copies, K and V by TMA, a box per page and 128 bytes
-//             of the head, into a ring of stages of 32 KB (head_dim 64: 16 KB);
+//   producers walk the block's share, up to four pieces ahead, and load it, one
+//             K (and Q by 16-byte copies), one V: by TMA, a box per page and 128
+//             bytes of the head, into a ring of stages of 32 KB (head_dim 64:
+//             16 KB).  A box costs its issuer about 55 ns whatever it
+//             holds, 2 KB at pages of 16: two issuers share them;
 //   workers   take the stages in turn (bf16: four of them each, float32: one); a worker has its own
 //             slice of a stage's keys and its own running maximum, sum and O, so
 //             no barrier stands between them; at the end of a piece it leaves its state
@@ -73,7 +75,7 @@ __device__ __forceinline__ void mma16816(float* c, const uint32_t* a, uint32_t b
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-constexpr int kJoiners = 3;  // with the producer they make the 12 warps that 168 registers allow
+constexpr int kJoiners = 2;  // with the producers they make the 12 warps that 168 registers allow
 
 // What the rows of a tile need to know of a piece, in shared memory.
 struct PieceInfo {
@@ -571,7 +573,7 @@ struct SliceLayout {
   static constexpr int kQBytes = (S::kQBytes + 127) & ~127;
   static constexpr int kOffP = kOffQ + S::kPieces * kQBytes;
   static constexpr int kBytes = kOffP + S::kWarps * S::kScratch;
-  static constexpr int kThreads = (S::kWarps + kJoiners + 1) * 32;
+  static constexpr int kThreads = (S::kWarps + kJoiners + 2) * 32;
   static_assert(kBytes + 2048 <= 232448, "shared memory of one block");
 };
 
@@ -634,7 +636,7 @@ __global__ void __launch_bounds__(SliceLayout<S, D, R>::kThreads, 1)
   if (tid == 0) {
     for (int i = 0; i < 3 * kPieces; ++i) tc::mbar_init(tc::smem_u32(s_bar + i), i / kPieces == 1 ? 32 : (i / kPieces == 2 ? kJoiners : 1));
     for (int i = 0; i < NS; ++i) {
-      tc::mbar_init(bar_full(i), 1);
+      tc::mbar_init(bar_full(i), 2);  // both producers
       tc::mbar_init(bar_empty(i), S::kPerStage);
     }
     tc::mbar_init(bar_state, W);
@@ -650,13 +652,15 @@ __global__ void __launch_bounds__(SliceLayout<S, D, R>::kThreads, 1)
     return;
   }
 
-  if (warp == W + kJoiners) {
+  if (warp >= W + kJoiners) {
     // ---------------------------------------------------------- producer --
     PagedWalk<kSliceUnit, kSliceExtra> walk;
     walk.start(a, s_start, u1 - u0, blockIdx.x);
     const int bs = sp.box_shift, box = 1 << bs, nb = SK >> bs;  // keys of a box, boxes of a stage's keys
-    const int sub = (lane & 15) / CB, col = (lane & 15) % CB;   // this lane's box: K on lanes 0 .. 15, V on 16 .. 31
+    const bool of_k = warp == W + kJoiners;
+    const int sub = lane / CB, col = lane % CB;  // this lane's box
     const bool mine = sub < nb;
+    const CUtensorMap* map = of_k ? &sp.tmk : &sp.tmv;
     struct Next {
       PieceInfo i;
       int32_t r;
@@ -687,19 +691,21 @@ __global__ void __launch_bounds__(SliceLayout<S, D, R>::kThreads, 1)
     int32_t pages = window(at, 0);
     for (int k = 0; ok; ++k) {
       const PieceInfo& i = at.i;
-      if (k >= kPieces && !wait(bar_joined(k), phase(k) ^ 1)) break;
-      if (lane == 0) {
-        s_piece[k % kPieces] = i;
-        tc::mbar_arrive(bar_piece(k));
+      if (of_k) {
+        if (k >= kPieces && !wait(bar_joined(k), phase(k) ^ 1)) break;
+        if (lane == 0) {
+          s_piece[k % kPieces] = i;
+          tc::mbar_arrive(bar_piece(k));
+        }
       }
       if (!i.valid) break;
-      for (int e = lane; e < R * CH; e += 32) {  // Q, zeros behind the tile's rows
+      for (int e = of_k ? lane : R * CH; e < R * CH; e += 32) {  // Q, zeros behind the tile's rows
         const int r = e / CH, c = e % CH, row = i.row0 + r;
         const bool in = r < i.nrows;
         const int64_t off = in ? int64_t(i.q0 + row / a.G) * a.q_stride + int64_t(i.h * a.G + row % a.G) * D + c * V : 0;
         cp_async16(sbase + L::kOffQ + (k % kPieces) * L::kQBytes + S::q_at(r, c), static_cast<const T*>(a.q) + off, in);
       }
-      asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar_q(k)) : "memory");
+      if (of_k) asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar_q(k)) : "memory");
       int32_t more = i.n * nb > 32 ? window(at, 32) : a.n_pages;
       Next ahead;
       int32_t ahead_pages = 0;
@@ -712,7 +718,7 @@ __global__ void __launch_bounds__(SliceLayout<S, D, R>::kThreads, 1)
           }
           ok = wait(bar_empty(g), ((g / NS) & 1) ^ 1);
           if (!ok) break;
-          if (lane == 0) tc::mbar_arrive_expect_tx(bar_full(g), L::kStageBytes);
+          if (lane == 0) tc::mbar_arrive_expect_tx(bar_full(g), L::kStageBytes / 2);
           int32_t page = __shfl_sync(0xffffffffu, pages, (f + sub) & 31);
           if (mine) {
             const int key = i.key0 + t * SK + (sub << bs);
@@ -722,8 +728,7 @@ __global__ void __launch_bounds__(SliceLayout<S, D, R>::kThreads, 1)
             }
             const int token = key & ((1 << a.page_shift) - 1);
             const uint32_t dst = sbase + L::kOffRing + (g % NS) * L::kStageBytes +
-                                 (lane < 16 ? 0 : L::kStageBytes / 2) + col * (SK * 128) + ((sub << bs) * 128);
-            const CUtensorMap* map = lane < 16 ? &sp.tmk : &sp.tmv;
+                                 (of_k ? 0 : L::kStageBytes / 2) + col * (SK * 128) + ((sub << bs) * 128);
             tma_load_4d(dst, map, bar_full(g), col * (128 / int(sizeof(T))), sp.head_inner ? i.h : token,
                         sp.head_inner ? token : i.h, page);
           }
@@ -820,11 +825,14 @@ cp_status launch_early(void (*kern)(P), dim3 grid, dim3 block, int smem, bool ea
 // ---------------------------------------------------------------- merge ---
 // One tile that starts in block c and goes on behind it: its partial states
 // are the blocks' from c on.  O = sum_e w_e O_e / sum_e w_e, w_e = 2^(L_e - max L),
-// L in log2 units, a warp per row; what bounds it is the launch (about 2 us).
-constexpr int kMergeThreads = 128, kMergeRows = 16;
+// L in log2 units.  16 lanes per row, so a warp has two rows' loads under way;
+// the first pieces' O is asked for together with their weights.  What bounds
+// it is its launch and three dependent loads (2 us): it starts while the attention
+// still runs and finds its tile meanwhile.
+constexpr int kMergeThreads = 128, kMergeRows = 32;
 
 template <typename T, int D, int U, int E>
-__device__ __forceinline__ void merge_block(const PagedArgs& a, int c, int64_t* s_scan, PagedStart& s_start) {
+__device__ __forceinline__ void merge_block(const PagedArgs& a, int c, int part, int64_t* s_scan, PagedStart& s_start) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const PagedShare share = paged_locate<U, E, kMergeThreads>(a, s_scan, &s_start, c + 1);
   const int64_t u0 = share.first(c), u1 = share.first(c + 1);
@@ -848,47 +856,48 @@ __device__ __forceinline__ void merge_block(const PagedArgs& a, int c, int64_t* 
   if (!work) return;
   const int n = last - c + 1;
   auto slot = [&](int e) { return int64_t(e == 0 ? slot0 : 2 * (c + e)); };
-  constexpr int N = D / 32;
-  for (int i = warp; i < kMergeRows; i += kMergeThreads / 32) {
-    const int r = blockIdx.y * kMergeRows + i;
+  constexpr int N = D / 16, kEager = 2;
+  const int half = lane >> 4, sl = lane & 15;
+  const uint32_t lanes = 0xffffu << (16 * half);
+  for (int i = 2 * warp + half; i < kMergeRows; i += kMergeThreads / 16) {
+    const int r = part * kMergeRows + i;
     if (r >= t.nrows) break;
-    // the first pieces' O is asked for together with their weights
-    constexpr int kEager = 4;
+    auto load = [&](int e, float* x) {
+      const float* src = a.part_o + (slot(e) * a.R + r) * D + 4 * sl;
+#pragma unroll
+      for (int v = 0; v < N; v += 4) load_vec<float, 4>(src + 16 * v, x + v);
+    };
     float x[kEager][N];
 #pragma unroll
-    for (int j = 0; j < kEager; ++j)
-      if (j < n) load_vec<float, N>(a.part_o + (slot(j) * a.R + r) * D + N * lane, x[j]);
-    const float first = lane < n ? a.part_l[slot(lane) * a.R + r] : -INFINITY;  // the whole of it, up to 32 pieces
+    for (int j = 0; j < kEager; ++j) load(j, x[j]);  // n >= 2
+    const float first = sl < n ? a.part_l[slot(sl) * a.R + r] : -INFINITY;
     float top = first;
-    for (int e = 32 + lane; e < n; e += 32) top = fmaxf(top, a.part_l[slot(e) * a.R + r]);
-    top = warp_max(top);
+    for (int e = 16 + sl; e < n; e += 16) top = fmaxf(top, a.part_l[slot(e) * a.R + r]);
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(lanes, top, o, 16));
     float acc[N] = {};
     float sum = 0.f;
     if (top != -INFINITY) {  // an empty state's O is 0
-      for (int e0 = 0; e0 < n; e0 += 32) {
-        const float l = e0 == 0 ? first : (e0 + lane < n ? a.part_l[slot(e0 + lane) * a.R + r] : -INFINITY);
+      auto add = [&](float we, const float* y) {
+        sum += we;
+#pragma unroll
+        for (int v = 0; v < N; ++v) acc[v] = fmaf(we, y[v], acc[v]);
+      };
+      for (int e0 = 0; e0 < n; e0 += 16) {
+        const float l = e0 == 0 ? first : (e0 + sl < n ? a.part_l[slot(e0 + sl) * a.R + r] : -INFINITY);
         const float w = exp2f(l - top);
-        const int m = min(32, n - e0);
+        const int m = min(16, n - e0);
         int j0 = 0;
         if (e0 == 0) {
-          j0 = min(kEager, m);
+          j0 = kEager;
 #pragma unroll
-          for (int j = 0; j < kEager; ++j) {
-            if (j >= n) break;
-            const float we = __shfl_sync(0xffffffffu, w, j);
-            sum += we;
-#pragma unroll
-            for (int v = 0; v < N; ++v) acc[v] = fmaf(we, x[j][v], acc[v]);
-          }
+          for (int j = 0; j < kEager; ++j) add(__shfl_sync(lanes, w, j, 16), x[j]);
         }
-#pragma unroll 8
+#pragma unroll 4
         for (int j = j0; j < m; ++j) {
-          const float we = __shfl_sync(0xffffffffu, w, j);
           float y[N];
-          load_vec<float, N>(a.part_o + (slot(e0 + j) * a.R + r) * D + N * lane, y);
-          sum += we;
-#pragma unroll
-          for (int v = 0; v < N; ++v) acc[v] = fmaf(we, y[v], acc[v]);
+          load(e0 + j, y);
+          add(__shfl_sync(lanes, w, j, 16), y);
         }
       }
     }
@@ -897,24 +906,28 @@ __device__ __forceinline__ void merge_block(const PagedArgs& a, int c, int64_t* 
     for (int v = 0; v < N; ++v) acc[v] *= inv;
     const int row = t.row0 + r;
     const int64_t out = int64_t(q.q0 + row / a.G) * a.H + st.h * a.G + row % a.G;
-    store_vec<T, N>(static_cast<T*>(a.o) + out * D + N * lane, acc);
-    if (lane == 0) a.lse[out] = sum > 0.f ? (top + log2f(sum)) * 0.69314718055994531f : -INFINITY;
+#pragma unroll
+    for (int v = 0; v < N; v += 4) store_vec<T, 4>(static_cast<T*>(a.o) + out * D + 4 * sl + 16 * v, acc + v);
+    if (sl == 0) a.lse[out] = sum > 0.f ? (top + log2f(sum)) * 0.69314718055994531f : -INFINITY;
   }
 }
 
 struct MergeParams {
   PagedArgs pair, slice;
+  int32_t pair_parts;  // blocks of kMergeRows rows of a pair's tile
 };
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const __grid_constant__ MergeParams p) {
   __shared__ int64_t s_scan[32];
   __shared__ PagedStart s_start;
-  const int c = blockIdx.x;
+  const int n_pair = p.pair.grid * p.pair_parts;
   if constexpr (D == 128 && sizeof(T) == 2) {
-    if (c < p.pair.grid) return merge_block<T, D, kPairUnit, kPairExtra>(p.pair, c, s_scan, s_start);
+    if (int(blockIdx.x) < n_pair)
+      return merge_block<T, D, kPairUnit, kPairExtra>(p.pair, blockIdx.x / p.pair_parts, blockIdx.x % p.pair_parts,
+                                                      s_scan, s_start);
   }
-  merge_block<T, D, kSliceUnit, kSliceExtra>(p.slice, c - p.pair.grid, s_scan, s_start);
+  merge_block<T, D, kSliceUnit, kSliceExtra>(p.slice, blockIdx.x - n_pair, 0, s_scan, s_start);
 }
 
 template <typename S, int D, int R>
@@ -942,9 +955,10 @@ cp_status run_slice(const PagedArgs& a, bool after_pair, cudaStream_t s) {
 
 template <typename T, int D>
 cp_status run_merge(const PagedArgs& pair, const PagedArgs& slice, cudaStream_t s) {
-  const int rows = pair.grid > 0 ? pair.R : slice.R;  // the pair's tiles have more rows
-  return launch_early(paged_merge_kernel<T, D>, dim3(unsigned(pair.grid + slice.grid), unsigned((rows + kMergeRows - 1) / kMergeRows)),
-                      dim3(kMergeThreads), 0, true, s, MergeParams{pair, slice});
+  static_assert(kMergeRows >= 32, "a slice's tile is one block's");
+  const int parts = (pair.R + kMergeRows - 1) / kMergeRows;
+  return launch_early(paged_merge_kernel<T, D>, dim3(unsigned(pair.grid * parts + slice.grid)), dim3(kMergeThreads), 0,
+                      true, s, MergeParams{pair, slice, parts});
 }
 
 }  // namespace

@@ -13,14 +13,15 @@
 //    share every load of K and V; a CTA's tile is 128 / G whole tokens.
 //  - Pages: the producer warp's lanes issue one box per page and 64 columns
 //    (at most 64 keys of a page); lane l looks up the page of the l-th 8 keys of
-//    a tile two tiles ahead, so no load waits for the table.  A page
+//    a tile ahead of its use.  A page
 //    that no row sees is given the page number n_pages: outside the map, read
 //    as zeros without touching memory.
 //  - The tile that holds a request's last key inside a page (or a window's
 //    first): P is 0 there, but 0 times whatever the page holds may be NaN.
-//    V of such a tile is copied by the producer's lanes with plain
+//    V of such a tile is copied by its producer's lanes with plain
 //    asynchronous copies that zero-fill the keys outside, a tile or two per
-//    piece; all others come by TMA.
+//    piece; all others come by TMA.  V has a producer of its own: its plain copies
+//    hold up no K, and a box costs its issuer about 55 ns (pages of 16: 16 boxes a tile).
 //  - Work is the common axis of paged.h: a pair runs an equal share of
 //    all key tiles, and a tile that is cut leaves float32 partial states.
 #include <cuda_bf16.h>
@@ -180,12 +181,12 @@ __global__ void __launch_bounds__(kThreads, 1) paged_pair_kernel(const __grid_co
   if (warp < 4) {
     tc::setmaxnreg_dec<kSmallRegs>();
   }
-  if (warp == 0) {
-    // ---------------------------------------------------------- producer --
+  if (warp == 0 || warp == 3) {
+    // ------------------------------------ producers: Q and K, and V --
+    const bool of_k = warp == 0;
     if (lane == 0) {
-      tc::prefetch_tmap(&p.tmq);
-      tc::prefetch_tmap(&p.tmk);
-      tc::prefetch_tmap(&p.tmv);
+      if (of_k) tc::prefetch_tmap(&p.tmq);
+      tc::prefetch_tmap(of_k ? &p.tmk : &p.tmv);
     }
     uint32_t qi = 0, kg = 0, vg = 0, odd_parity = 0;
     bool ok = true;
@@ -267,31 +268,27 @@ __global__ void __launch_bounds__(kThreads, 1) paged_pair_kernel(const __grid_co
       ++vg;
       return true;
     };
-    // pages in flight: value tile, key tile (one ahead), the tile after it
     while (ok && w.next(a, pc)) {
       const int n = pc.ub - pc.ua, t0 = pc.tile.b0 + pc.ua;
       if (n == 0) continue;
-      int32_t pg_k = pages(t0), pg_n = n > 1 ? pages(t0 + 1) : a.n_pages;
-      const uint32_t qb = qi % kQBufs;
-      ok = __all_sync(0xffffffffu, wt(B_QEMPTY0 + qb, ((qi / kQBufs) & 1) ^ 1));
-      if (!ok) break;
-      if (lane == 0) {
-        if (even) tc::mbar_arrive_expect_tx(bar(B_QFULL0 + qb), 4u * 128u * uint32_t(half_rows));
-        const int tok = pc.q.q0 + (pc.tile.row0 + int(rank) * half_rows) / a.G, h = pc.h * a.G;
-        tc::tma_load_3d_pair(sQ + qb * kQBytes, &p.tmq, bar_even(B_QFULL0 + qb), 0, h, tok);
-        tc::tma_load_3d_pair(sQ + qb * kQBytes + kQHalf, &p.tmq, bar_even(B_QFULL0 + qb), 64, h, tok);
+      int32_t pg = pages(t0);
+      if (of_k) {
+        const uint32_t qb = qi % kQBufs;
+        ok = __all_sync(0xffffffffu, wt(B_QEMPTY0 + qb, ((qi / kQBufs) & 1) ^ 1));
+        if (!ok) break;
+        if (lane == 0) {
+          if (even) tc::mbar_arrive_expect_tx(bar(B_QFULL0 + qb), 4u * 128u * uint32_t(half_rows));
+          const int tok = pc.q.q0 + (pc.tile.row0 + int(rank) * half_rows) / a.G, h = pc.h * a.G;
+          tc::tma_load_3d_pair(sQ + qb * kQBytes, &p.tmq, bar_even(B_QFULL0 + qb), 0, h, tok);
+          tc::tma_load_3d_pair(sQ + qb * kQBytes + kQHalf, &p.tmq, bar_even(B_QFULL0 + qb), 64, h, tok);
+        }
+        ++qi;
       }
-      ++qi;
-      pg_k = checked(t0, pg_k);
-      ok = load_k(t0, pg_k);
-      for (int t = 1; t < n && ok; ++t) {
-        const int32_t pg_v = pg_k;
-        pg_k = checked(t0 + t, pg_n);
-        if (t + 1 < n) pg_n = pages(t0 + t + 1);
-        ok = load_k(t0 + t, pg_k);
-        if (ok) ok = load_v(t0 + t - 1, pg_v);
+      for (int t = 0; t < n && ok; ++t) {
+        const int32_t now = checked(t0 + t, pg);
+        if (t + 1 < n) pg = pages(t0 + t + 1);  // a tile ahead of its use
+        ok = of_k ? load_k(t0 + t, now) : load_v(t0 + t, now);
       }
-      if (ok) ok = load_v(t0 + n - 1, pg_k);
     }
     // Drain: every copy this CTA started has landed before the block exits
     // (the even CTA waits for the phases it armed, which count the odd CTA's

@@ -5,16 +5,46 @@
 
 namespace cpattn {
 
+// Tiles that a thread sums by itself; a request of more is summed by its whole warp.
+constexpr int kOwnTiles = 4;
+
 // Finds where the first unit of block c lies and returns the shares; the whole
 // block calls it, `sh` holds 32 int64 and `out` a PagedStart in shared memory
-// (not written where c has no first unit).  The threads share the requests in runs.
+// (not written where c has no first unit).  The threads share the requests in
+// runs; the loops are warp-uniform so that lanes can help one another.
 template <int U, int E, int kThreads>
 __device__ __forceinline__ PagedShare paged_locate(const PagedArgs& a, int64_t* sh, PagedStart* out, int c) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int run = (a.n_reqs + kThreads - 1) / kThreads;
-  const int r0 = min(tid * run, a.n_reqs), r1 = min(r0 + run, a.n_reqs);
-  int64_t mine = 0;
-  for (int r = r0; r < r1; ++r) mine += paged_req_units<U, E>(a, paged_req(a, r)) * a.Hkv;
+  const int r0 = tid * run;
+  // units of one kv-head of this lane's i-th request
+  auto units = [&](int i, PagedReq& q, int& nt) -> int64_t {
+    q = PagedReq{0, 0, 0};
+    if (r0 + i < a.n_reqs) q = paged_req(a, r0 + i);
+    nt = paged_tiles(a, q);
+    int64_t s = 0;
+    if (nt <= kOwnTiles)
+      for (int t = 0; t < nt; ++t) s += paged_tile<U>(a, q, t).n + E;
+    for (uint32_t big = __ballot_sync(0xffffffffu, nt > kOwnTiles); big; big &= big - 1) {
+      const int from = __ffs(big) - 1;
+      const PagedReq x{__shfl_sync(0xffffffffu, q.q0, from), __shfl_sync(0xffffffffu, q.nq, from),
+                       __shfl_sync(0xffffffffu, q.kv, from)};
+      const int n = __shfl_sync(0xffffffffu, nt, from);
+      int64_t part = 0;
+      for (int t = lane; t < n; t += 32) part += paged_tile<U>(a, x, t).n + E;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) part += __shfl_xor_sync(0xffffffffu, part, o);
+      if (lane == from) s = part;
+    }
+    return s;
+  };
+  PagedReq q{};
+  int nt = 0;
+  int64_t mine = 0, last = 0;
+  for (int i = 0; i < run; ++i) {
+    last = units(i, q, nt);
+    mine += last * a.Hkv;
+  }
   int64_t x = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -31,27 +61,44 @@ __device__ __forceinline__ PagedShare paged_locate(const PagedArgs& a, int64_t* 
   }
   const PagedShare share(total, a.grid);
   const int64_t u = share.first(c);
-  if (u >= before && u < before + mine) {
+  const uint32_t who = __ballot_sync(0xffffffffu, u >= before && u < before + mine);
+  if (who) {  // this warp holds it: its lane's requests, then the tiles of the one
+    const int from = __ffs(who) - 1;
     int64_t base = before;
-    for (int r = r0; r < r1; ++r) {
-      const PagedReq q = paged_req(a, r);
-      const int64_t per = paged_req_units<U, E>(a, q);
-      if (u >= base + per * a.Hkv) {
-        base += per * a.Hkv;
-        continue;
+    bool found = false;
+    int r = 0;
+    for (int i = 0; i < run; ++i) {
+      if (run > 1) last = units(i, q, nt);
+      const bool here = lane == from && !found && u < base + last * a.Hkv;
+      if (__any_sync(0xffffffffu, here)) {
+        r = i;
+        found = true;
+        break;
       }
-      const int h = int(paged_div(u - base, per));
-      int64_t rest = u - base - h * per;
-      const int nt = paged_tiles(a, q);
-      for (int t = 0; t < nt; ++t) {
-        const int cost = paged_tile<U>(a, q, t).n + E;
-        if (rest < cost) {
-          *out = PagedStart{r, h, t, int32_t(rest)};
-          break;
-        }
-        rest -= cost;
+      base += last * a.Hkv;
+    }
+    base = __shfl_sync(0xffffffffu, base, from);
+    const int64_t per = __shfl_sync(0xffffffffu, last, from);
+    const PagedReq y{__shfl_sync(0xffffffffu, q.q0, from), __shfl_sync(0xffffffffu, q.nq, from),
+                     __shfl_sync(0xffffffffu, q.kv, from)};
+    const int n = __shfl_sync(0xffffffffu, nt, from);
+    const int h = int(paged_div(u - base, per));
+    int64_t rest = u - base - h * per;
+    for (int t0 = 0; t0 < n; t0 += 32) {  // 32 tiles at a time
+      const int cost = t0 + lane < n ? paged_tile<U>(a, y, t0 + lane).n + E : 0;
+      int64_t upto = cost;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t z = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += z;
       }
-      break;
+      const uint32_t in = __ballot_sync(0xffffffffu, rest < upto);
+      if (in) {
+        if (lane == __ffs(in) - 1)
+          *out = PagedStart{(warp * 32 + from) * run + r, h, t0 + lane, int32_t(rest - (upto - cost))};
+        break;
+      }
+      rest -= __shfl_sync(0xffffffffu, upto, 31);
     }
   }
   __syncthreads();
