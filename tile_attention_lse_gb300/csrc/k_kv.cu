@@ -7,7 +7,7 @@
 //   repeats the scan (a few hundred requests: one step of 1024 threads) and
 //   fills its own rows, so one launch does without a second pass over the
 //   results; what bounds it is the chain of dependent loads, about 4 us.
-// head_rows_kernel: a warp takes one row and a few of its heads.  The turn
+// head_rows_kernel: a warp takes one row and a few heads of one tensor.  The turn
 //   of pair i at position n is n * turn[i] mod 1, exact in 64-bit integers
 //   (turn is base^-e / 2 pi as a binary fraction, so the product wraps at whole
 //   turns: no float64 and no range reduction), rounded once to float32 half
@@ -62,15 +62,13 @@ __device__ __forceinline__ void block_scan2(int64_t& x, int64_t& y, int64_t* sh)
   }
 }
 
-constexpr int kRowsPerTabBlock = 4096;
-
 __global__ void __launch_bounds__(kTabThreads) kv_extend_kernel(KvTables a) {
   extern __shared__ int32_t sm[];  // [n_reqs] first row, [n_reqs] free pages taken before
   int32_t* s_cu = sm;
   int32_t* s_before = sm + a.n_reqs;
   __shared__ int64_t sh[64];
   __shared__ int s_stop;
-  __shared__ int32_t s_rows;
+  __shared__ int32_t s_rows, s_taken;
   const int tid = threadIdx.x;
   const int32_t p = a.page_size;
   const int64_t n_free = min(int64_t(max(*a.n_free, 0)), int64_t(a.pool));
@@ -106,45 +104,45 @@ __global__ void __launch_bounds__(kTabThreads) kv_extend_kernel(KvTables a) {
   __syncthreads();
   const int stop = s_stop;
   if (tid == 0) {
-    s_rows = 0;
-    if (stop > 0) s_rows = s_cu[stop - 1] + a.add[stop - 1];
+    s_rows = s_taken = 0;
+    if (stop > 0) {
+      const int64_t len = a.lens[stop - 1], n = a.add[stop - 1];
+      s_rows = s_cu[stop - 1] + int32_t(n);
+      s_taken = s_before[stop - 1] + int32_t((len + n + p - 1) / p - (len + p - 1) / p);
+    }
   }
   __syncthreads();
-  const int32_t rows = s_rows;
-  // tables, lengths and row offsets: block b takes every gridDim.x-th request
-  for (int r = blockIdx.x * kTabThreads + tid; r < a.n_reqs; r += gridDim.x * kTabThreads) {
+  const int32_t rows = s_rows, taken = s_taken;
+  // the last granted request whose entry of `from` is at most x (requests that
+  // add nothing share theirs with the next)
+  auto find = [&](const int32_t* from, int64_t x) {
+    int lo = 0, hi = stop - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (from[mid] <= x) lo = mid; else hi = mid - 1;
+    }
+    return lo;
+  };
+  const int32_t stride = gridDim.x * kTabThreads, first = blockIdx.x * kTabThreads + tid;
+  for (int r = first; r < a.n_reqs; r += stride) {
     const bool ok = r < stop;
-    const int32_t len = a.lens[r], add = ok ? a.add[r] : 0;
-    a.lens_out[r] = len + add;
+    a.lens_out[r] = a.lens[r] + (ok ? a.add[r] : 0);
     a.cu[r] = ok ? s_cu[r] : rows;
-    if (add > 0) {
-      const int32_t have = int32_t((int64_t(len) + p - 1) / p);
-      const int32_t end = int32_t((int64_t(len) + add + p - 1) / p);
-      for (int32_t j = have; j < end; ++j)
-        a.table[int64_t(r) * a.max_blocks + j] = a.free_pages[n_free - 1 - (s_before[r] + j - have)];
-    }
   }
-  if (blockIdx.x == 0 && tid == 0) {
+  for (int64_t i = first; i < taken; i += stride) {  // page i of those taken
+    const int r = find(s_before, i);
+    const int32_t have = int32_t((int64_t(a.lens[r]) + p - 1) / p);
+    a.table[int64_t(r) * a.max_blocks + have + i - s_before[r]] = a.free_pages[n_free - 1 - i];
+  }
+  if (first == 0) {
     a.cu[a.n_reqs] = rows;
-    int64_t taken = 0;
-    if (stop > 0) {
-      const int64_t len = a.lens[stop - 1];
-      taken = s_before[stop - 1] + (len + a.add[stop - 1] + p - 1) / p - (len + p - 1) / p;
-    }
     *a.n_free_out = int32_t(n_free - taken);
   }
   // rows: slot and position; -1 and 0 behind the last
-  const int64_t t1 = min(a.max_rows, int64_t(blockIdx.x + 1) * kRowsPerTabBlock);
-  for (int64_t t = int64_t(blockIdx.x) * kRowsPerTabBlock + tid; t < t1; t += kTabThreads) {
+  for (int64_t t = first; t < a.max_rows; t += stride) {
     int32_t slot = -1, pos = 0;
     if (t < rows) {
-      // the last granted request that starts at or before t (requests that
-      // add nothing start where the next does)
-      int lo = 0, hi = stop - 1;
-      while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (s_cu[mid] <= t) lo = mid; else hi = mid - 1;
-      }
+      const int lo = find(s_cu, t);
       const int32_t len = a.lens[lo];
       pos = len + int32_t(t - s_cu[lo]);
       const int32_t have = int32_t((int64_t(len) + p - 1) / p), b = pos / p;
@@ -201,25 +199,51 @@ __device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float
 __device__ __forceinline__ void from_f(float x, float& y) { y = x; }
 __device__ __forceinline__ void from_f(float x, __nv_bfloat16& y) { y = __float2bfloat16_rn(x); }
 
+// Sine and cosine of `turn` / 2^32 turns.  bfloat16 takes the hardware's (off
+// by 2^-21 at most for angles within a half turn either way, 2^-13 of the
+// output's own rounding), float32 the accurate ones.
+template <typename T>
+__device__ __forceinline__ void turn_sincos(int32_t turn, float* s, float* c) {
+  if constexpr (sizeof(T) == 2)
+    __sincosf(float(turn) * 1.4629180792671596e-9f, s, c);  // * 2 pi / 2^32
+  else
+    sincospif(float(turn) * 4.656612873077393e-10f, s, c);  // * 2^-31: half turns
+}
+
+// Tasks of a row: its q heads, k heads and v heads, `per` at a time.
+struct RowTasks {
+  int32_t per, of_q, of_k, all;
+};
+
+constexpr int kRowBlocks = 4;  // resident blocks of 256 threads: 64 registers
+
 template <typename T, int D, bool kAdjacent>
-__global__ void __launch_bounds__(256) head_rows_kernel(const __grid_constant__ HeadRows a, int32_t heads_per_task,
-                                                        int32_t tasks_per_row, int64_t tasks) {
+__global__ void __launch_bounds__(256, kRowBlocks) head_rows_kernel(const __grid_constant__ HeadRows a, RowTasks rt, int64_t tasks) {
   constexpr int V = 16 / int(sizeof(T));  // elements of one load
   constexpr int LPH = D / 2 / V;          // lanes of a head: each holds two vectors
   constexpr int HPI = 32 / LPH;           // heads of one step of a warp
   const int lane = threadIdx.x & 31;
   const int c = lane % LPH, sub = lane / LPH;
   const int pairs = a.turns.pairs;
-  const bool turns = c * V < pairs;
-  // this lane's vectors: its pairs' two halves, or two vectors side by side
-  const int off0 = (kAdjacent || !turns) ? 2 * c * V : c * V;
-  const int off1 = (kAdjacent || !turns) ? off0 + V : pairs + c * V;
-  const int heads = a.heads_q + a.heads_k + a.heads_v;
+  // this lane's pairs' turns and positions (by lane from constant memory: once)
+  uint64_t turn[D / 64];
+  const int32_t* pos[D / 64];
+#pragma unroll
+  for (int j = 0; j < D / 64; ++j) {
+    const int i = min(lane + 32 * j, 63);
+    turn[j] = a.turns.turn[i];
+    pos[j] = lane + 32 * j < pairs ? a.pos + int64_t(a.turns.axis[i]) * a.rows : nullptr;
+  }
   const int64_t stride = (int64_t(gridDim.x) * blockDim.x) >> 5;
+  // a row's tasks differ in length: where a warp would always meet the same
+  // kind, it moves on by one each time (its row's tasks are all in this step then)
+  const int turn_by = stride % rt.all == 0 ? 1 : 0;
+  int skew = 0;
   for (int64_t task = (int64_t(blockIdx.x) * blockDim.x + threadIdx.x) >> 5; task < tasks; task += stride) {
-    const int64_t row = task / tasks_per_row;
-    const int h0 = int(task - row * tasks_per_row) * heads_per_task;
-    const int h1 = min(heads, h0 + heads_per_task);
+    const int64_t row = tasks >> 31 ? task / rt.all : int64_t(uint32_t(task) / uint32_t(rt.all));
+    int part = int(task - row * rt.all) + skew;
+    if (part >= rt.all) part -= rt.all;
+    skew = skew + turn_by == rt.all ? 0 : skew + turn_by;
     int64_t cache_off = 0;
     if (a.slots) {
       const int32_t slot = a.slots[row];
@@ -227,17 +251,54 @@ __global__ void __launch_bounds__(256) head_rows_kernel(const __grid_constant__ 
       if (slot < 0 || page >= a.n_pages) continue;
       cache_off = page * a.page_stride + int64_t(slot & ((1 << a.page_shift) - 1)) * a.token_stride;
     }
+    // the task's heads of one tensor
+    const T* src;
+    T* dst;
+    int64_t step = D;  // elements between heads of dst
+    int heads;
+    const bool of_v = part >= rt.of_q + rt.of_k;
+    if (part < rt.of_q) {
+      heads = a.heads_q;
+      src = static_cast<const T*>(a.q) + row * a.q_stride;
+      dst = static_cast<T*>(a.q_out) + row * a.heads_q * D;
+    } else if (!of_v) {
+      part -= rt.of_q;
+      heads = a.heads_k;
+      src = static_cast<const T*>(a.k) + row * a.k_stride;
+      dst = static_cast<T*>(a.k_out) + (a.slots ? cache_off : row * a.heads_k * D);
+      if (a.slots) step = a.head_stride;
+    } else {
+      part -= rt.of_q + rt.of_k;
+      heads = a.heads_v;
+      src = static_cast<const T*>(a.v) + row * a.v_stride;
+      dst = static_cast<T*>(a.v_out) + cache_off;
+      step = a.head_stride;
+    }
+    const bool rotate = !of_v && c * V < pairs;
+    // this lane's vectors: its pairs' two halves, or two vectors side by side
+    const int off0 = kAdjacent || !rotate ? 2 * c * V : c * V;
+    const int off1 = kAdjacent || !rotate ? off0 + V : pairs + c * V;
+    const int h1 = min(heads, (part + 1) * rt.per);
+    int h = part * rt.per + sub;
+    // the loads of a step of heads are under way while the angles are formed,
+    // and then while the step before it is turned
+    Vec16<T> n0, n1;
+    auto load = [&](int at) {
+      if (at < h1) {
+        n0.u = *reinterpret_cast<const uint4*>(src + at * D + off0);
+        n1.u = *reinterpret_cast<const uint4*>(src + at * D + off1);
+      }
+    };
+    load(h);
     float cs[V], sn[V];
-    if (pairs > 0 && h0 < a.heads_q + a.heads_k) {
+    if (!of_v && pairs > 0) {
       float c2[D / 64], s2[D / 64];
 #pragma unroll
       for (int j = 0; j < D / 64; ++j) {
-        const int i = lane + 32 * j;
         float s_ = 0.f, c_ = 1.f;
-        if (i < pairs) {
-          const int64_t n = a.pos[int64_t(a.turns.axis[i]) * a.rows + row];
-          const uint64_t t = uint64_t(n) * a.turns.turn[i];
-          sincospif(float(int32_t(uint32_t(t >> 32))) * 4.656612873077393e-10f, &s_, &c_);  // * 2^-31: half turns
+        if (pos[j]) {
+          const int64_t n = pos[j][row];
+          turn_sincos<T>(int32_t(uint32_t((uint64_t(n) * turn[j]) >> 32)), &s_, &c_);
         }
         c2[j] = c_;
         s2[j] = a.turns.inverse ? -s_ : s_;
@@ -257,66 +318,49 @@ __global__ void __launch_bounds__(256) head_rows_kernel(const __grid_constant__ 
         sn[j] = y;
       }
     }
-    for (int h = h0 + sub; h < h1; h += HPI) {
-      const T* src;
-      T* dst;
-      bool rotate = turns;
-      if (h < a.heads_q) {
-        src = static_cast<const T*>(a.q) + row * a.q_stride + int64_t(h) * D;
-        dst = static_cast<T*>(a.q_out) + (row * a.heads_q + h) * D;
-      } else if (h < a.heads_q + a.heads_k) {
-        const int g = h - a.heads_q;
-        src = static_cast<const T*>(a.k) + row * a.k_stride + int64_t(g) * D;
-        dst = static_cast<T*>(a.k_out) + (a.slots ? cache_off + g * a.head_stride : (row * a.heads_k + g) * D);
-      } else {
-        const int g = h - a.heads_q - a.heads_k;
-        src = static_cast<const T*>(a.v) + row * a.v_stride + int64_t(g) * D;
-        dst = static_cast<T*>(a.v_out) + cache_off + g * a.head_stride;
-        rotate = false;
-      }
-      const int o0 = rotate ? off0 : 2 * c * V;
-      const int o1 = rotate ? off1 : 2 * c * V + V;
-      Vec16<T> x0, x1;
-      x0.u = *reinterpret_cast<const uint4*>(src + o0);
-      x1.u = *reinterpret_cast<const uint4*>(src + o1);
+    for (; h < h1; h += HPI) {
+      Vec16<T> x0 = n0, x1 = n1;
+      load(h + HPI);
       if (rotate) {
         if (kAdjacent) {
 #pragma unroll
           for (int j = 0; j < V; ++j) {  // pair j: elements 2 j, 2 j + 1 of the lane's 2 V
             Vec16<T>& x = 2 * j < V ? x0 : x1;
             const int e = (2 * j) % V;
-            const float u = to_f(x.e[e]), w = to_f(x.e[e + 1]);
-            from_f(u * cs[j] - w * sn[j], x.e[e]);
-            from_f(w * cs[j] + u * sn[j], x.e[e + 1]);
+            const float y = to_f(x.e[e]), w = to_f(x.e[e + 1]);
+            from_f(y * cs[j] - w * sn[j], x.e[e]);
+            from_f(w * cs[j] + y * sn[j], x.e[e + 1]);
           }
         } else {
 #pragma unroll
           for (int j = 0; j < V; ++j) {
-            const float u = to_f(x0.e[j]), w = to_f(x1.e[j]);
-            from_f(u * cs[j] - w * sn[j], x0.e[j]);
-            from_f(w * cs[j] + u * sn[j], x1.e[j]);
+            const float y = to_f(x0.e[j]), w = to_f(x1.e[j]);
+            from_f(y * cs[j] - w * sn[j], x0.e[j]);
+            from_f(w * cs[j] + y * sn[j], x1.e[j]);
           }
         }
       }
-      *reinterpret_cast<uint4*>(dst + o0) = x0.u;
-      *reinterpret_cast<uint4*>(dst + o1) = x1.u;
+      *reinterpret_cast<uint4*>(dst + h * step + off0) = x0.u;
+      *reinterpret_cast<uint4*>(dst + h * step + off1) = x1.u;
     }
   }
 }
 
 template <typename T, int D>
 cp_status head_rows(const HeadRows& a, cudaStream_t s) {
-  const int heads = a.heads_q + a.heads_k + a.heads_v;
-  // few rows: one step of heads per warp, so that the rows spread over the SMs;
-  // many rows: more heads share one set of sines and cosines
-  const int per = a.rows >= 4096 ? 16 : 8;
-  const int tasks_per_row = (heads + per - 1) / per;
-  const int64_t tasks = a.rows * tasks_per_row;
+  // few rows: one or two steps of heads per warp, so that the rows spread over
+  // the SMs; many rows: more heads share one set of sines and cosines
+  RowTasks rt;
+  rt.per = a.rows >= 4096 ? 16 : 8;
+  rt.of_q = (a.heads_q + rt.per - 1) / rt.per;
+  rt.of_k = (a.heads_k + rt.per - 1) / rt.per;
+  rt.all = rt.of_q + rt.of_k + (a.heads_v + rt.per - 1) / rt.per;
+  const int64_t tasks = a.rows * rt.all;
   int64_t blocks = (tasks + 7) / 8;
-  const int64_t cap = int64_t(num_sms()) * 8;
+  const int64_t cap = int64_t(num_sms()) * kRowBlocks;
   if (blocks > cap) blocks = cap;
   auto* kern = a.turns.adjacent ? head_rows_kernel<T, D, true> : head_rows_kernel<T, D, false>;
-  kern<<<unsigned(blocks), 256, 0, s>>>(a, per, tasks_per_row, tasks);
+  kern<<<unsigned(blocks), 256, 0, s>>>(a, rt, tasks);
   return cuda_status(cudaGetLastError());
 }
 
@@ -334,8 +378,10 @@ cp_status launch_kv_extend(const KvTables& a, cudaStream_t s) {
       cudaFuncSetAttribute(kv_extend_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxTableReqs * 8) !=
           cudaSuccess)
     return CP_ERR_CUDA;
-  const int64_t blocks = (a.max_rows + kRowsPerTabBlock - 1) / kRowsPerTabBlock;
-  kv_extend_kernel<<<unsigned(blocks > 0 ? blocks : 1), kTabThreads, smem, s>>>(a);
+  int64_t blocks = (a.max_rows + kTabThreads - 1) / kTabThreads;
+  const int64_t cap = int64_t(num_sms()) * 2;
+  blocks = blocks < 1 ? 1 : blocks > cap ? cap : blocks;
+  kv_extend_kernel<<<unsigned(blocks), kTabThreads, smem, s>>>(a);
   return cuda_status(cudaGetLastError());
 }
 
