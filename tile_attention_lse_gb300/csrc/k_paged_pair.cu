@@ -53,8 +53,8 @@ constexpr int kOffQ = 0;
 constexpr int kOffK = kOffQ + kQBufs * kQBytes;
 constexpr int kOffV = kOffK + kKStages * kKBytes;
 constexpr int kOffBar = kOffV + kVStages * kVBytes;
-constexpr int kOffX = kOffBar + 512;  // running max [2 tile parities][128], row-sum base and sum [2 warps][2][128]
-constexpr int kOffScan = kOffX + (2 * 128 + 2 * 2 * 128) * 4;
+constexpr int kOffX = kOffBar + 512;  // running max [2 tile parities][128], row-sum base and sum [2 piece parities][2 warps][2][128]
+constexpr int kOffScan = kOffX + (2 * 128 + 2 * 2 * 2 * 128) * 4;
 constexpr int kSmemBytes = kOffScan + 32 * 8 + int(sizeof(PagedStart));
 static_assert(kSmemBytes <= 232448, "shared memory budget of one CTA");
 
@@ -76,7 +76,8 @@ enum {
   B_OEMPTY,                         // even: both CTAs' epilogues have read O (16 warp arrivals)
   B_DRAIN,                          // both: every MMA of both issuers complete (2 arrivals)
   B_MREADY0,                        // + 2 quarter + parity: the running max after a tile of that parity
-  B_COUNT = B_MREADY0 + 8
+  B_JOIN0 = B_MREADY0 + 8,          // + quarter: its two warps' row sums of a piece are in shared memory (2 arrivals)
+  B_COUNT = B_JOIN0 + 4
 };
 static_assert(8 * B_COUNT + 8 <= 512, "barrier area");
 
@@ -160,6 +161,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_pair_kernel(const __grid_co
         cnt = 8;  // a tile's 4 softmax warps x 2 CTAs
       if (i == B_OEMPTY) cnt = 16;  // all 8 softmax warps x 2 CTAs
       if (i == B_DRAIN) cnt = 2;    // both issuers
+      if (i >= B_JOIN0) cnt = 2;
       tc::mbar_init(bar(i), cnt);
     }
     *abort_flag = 0;
@@ -400,11 +402,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_pair_kernel(const __grid_co
     const uint32_t lane_off = uint32_t(quarter * 32) << 16;
     const uint32_t tO = tmem + lane_off + kColO;
     float* mrow = reinterpret_cast<float*>(smem + kOffX);  // [tile parity][row]
-    float* xend = mrow + 2 * 128;                           // [warp half][base m, sum][row]
-    const uint32_t pair_bar = 1 + quarter;                  // the two warps of this lane quarter
+    float* xjoin = mrow + 2 * 128;                          // [piece parity][warp half][base m, sum][row]
     const float sl2 = a.scale_log2;
     const uint64_t sl2x2 = tc::f32x2(sl2, sl2);
-    uint32_t g = 0, items = 0;
+    uint32_t g = 0, items = 0, pieces = 0;
     bool ok = true;
     PagedPiece pc;
     while (ok && w.next(a, pc)) {
@@ -504,16 +505,17 @@ __global__ void __launch_bounds__(kThreads, 1) paged_pair_kernel(const __grid_co
       }
       if (!ok) break;
       // ------------------------------------------------------ epilogue --
-      if (n > 0) {
-        ok = __all_sync(0xffffffffu, wt(B_ODONE, items & 1));
-        if (!ok) break;
-        tc::fence_after_sync();
-      }
-      // the row's sum over both warps' tiles against the final max (the
-      // larger of the two bases: the max never decreases along the stream)
+      // What does not need O comes first: the last PV is still running.  The
+      // row's sum over both warps' tiles is taken against the final max (the
+      // larger of the two bases: the max never decreases along the stream).
+      float* xend = xjoin + (pieces & 1) * 512;
       xend[half * 256 + row] = m_own;
       xend[half * 256 + 128 + row] = l;
-      tc::named_bar(pair_bar, 64);
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(bar(B_JOIN0 + quarter));
+      ok = __all_sync(0xffffffffu, wt(B_JOIN0 + quarter, pieces & 1));
+      if (!ok) break;
+      ++pieces;
       const float m_o = xend[(half ^ 1) * 256 + row], l_o = xend[(half ^ 1) * 256 + 128 + row];
       const float m_fin = fmaxf(m_own, m_o);
       float l_all = 0.f;
@@ -521,58 +523,60 @@ __global__ void __launch_bounds__(kThreads, 1) paged_pair_kernel(const __grid_co
         if (m_own != -INFINITY) l_all += l * tc::ex2(m_own - m_fin);
         if (m_o != -INFINITY) l_all += l_o * tc::ex2(m_o - m_fin);
       }
-      tc::named_bar(pair_bar, 64);  // both have read before the next piece writes
+      const float inv = l_all > 0.f ? 1.f / l_all : 0.f;
       // A whole tile writes the final O (bf16, round to nearest even) and LSE;
       // a piece of one its partial state (O in float32, LSE in log2 units).
-      const int c0 = 64 * half;
       const bool direct = pc.slot < 0;
       const int trow = int(rank) * half_rows + row;
       const int packed = pc.tile.row0 + trow;
       const int64_t at = direct ? int64_t(pc.q.q0 + packed / a.G) * a.H + pc.h * a.G + packed % a.G
                                 : int64_t(pc.slot) * a.R + trow;
-      const float inv = l_all > 0.f ? 1.f / l_all : 0.f;
-      if (!idle) {
-#pragma unroll
-        for (int cc = 0; cc < 2; ++cc) {
-          uint32_t orr[32];
-          if (n > 0) {
-            tc::tmem_ld32(tO + c0 + cc * 32, orr);
-            tc::tmem_wait_ld();
-          } else {
-#pragma unroll
-            for (int j = 0; j < 32; ++j) orr[j] = 0u;
-          }
-          if (row_ok && direct) {
-            uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.o) + at * 128 + c0) + cc * 4;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const uint32_t* e = orr + 8 * j;
-              dst[j] = make_uint4(tc::pack_bf16x2(__uint_as_float(e[0]) * inv, __uint_as_float(e[1]) * inv),
-                                  tc::pack_bf16x2(__uint_as_float(e[2]) * inv, __uint_as_float(e[3]) * inv),
-                                  tc::pack_bf16x2(__uint_as_float(e[4]) * inv, __uint_as_float(e[5]) * inv),
-                                  tc::pack_bf16x2(__uint_as_float(e[6]) * inv, __uint_as_float(e[7]) * inv));
-            }
-          } else if (row_ok) {
-            float4* dst = reinterpret_cast<float4*>(a.part_o + at * 128 + c0) + cc * 8;
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-              dst[j] = make_float4(__uint_as_float(orr[4 * j]) * inv, __uint_as_float(orr[4 * j + 1]) * inv,
-                                   __uint_as_float(orr[4 * j + 2]) * inv, __uint_as_float(orr[4 * j + 3]) * inv);
-          }
-        }
-        if (row_ok && half == 0) {
-          const float l2 = l_all > 0.f ? m_fin + tc::lg2(l_all) : -INFINITY;
-          if (direct)
-            a.lse[at] = l2 * 0.69314718055994531f;
-          else
-            a.part_l[at] = l2;
-        }
+      if (row_ok && half == 0) {
+        const float l2 = l_all > 0.f ? m_fin + tc::lg2(l_all) : -INFINITY;
+        if (direct)
+          a.lse[at] = l2 * 0.69314718055994531f;
+        else
+          a.part_l[at] = l2;
       }
-      if (n > 0) {  // O may be overwritten by the next piece's first PV
-        tc::fence_before_sync();
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive_remote(bar_even(B_OEMPTY));
+      const int c0 = 64 * half;  // each warp writes 64 columns
+      if (n > 0) {
+        ok = __all_sync(0xffffffffu, wt(B_ODONE, items & 1));
+        if (!ok) break;
+        tc::fence_after_sync();
         ++items;
+      }
+#pragma unroll
+      for (int cc = 0; cc < 2; ++cc) {
+        uint32_t orr[32];
+        if (n > 0 && !idle) {
+          tc::tmem_ld32(tO + c0 + cc * 32, orr);
+          tc::tmem_wait_ld();
+        } else {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) orr[j] = 0u;
+        }
+        if (n > 0 && cc == 1) {  // O is in registers: the next piece's first PV may overwrite it
+          tc::fence_before_sync();
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive_remote(bar_even(B_OEMPTY));
+        }
+        if (row_ok && direct) {
+          uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.o) + at * 128 + c0) + cc * 4;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const uint32_t* e = orr + 8 * j;
+            dst[j] = make_uint4(tc::pack_bf16x2(__uint_as_float(e[0]) * inv, __uint_as_float(e[1]) * inv),
+                                tc::pack_bf16x2(__uint_as_float(e[2]) * inv, __uint_as_float(e[3]) * inv),
+                                tc::pack_bf16x2(__uint_as_float(e[4]) * inv, __uint_as_float(e[5]) * inv),
+                                tc::pack_bf16x2(__uint_as_float(e[6]) * inv, __uint_as_float(e[7]) * inv));
+          }
+        } else if (row_ok) {
+          float4* dst = reinterpret_cast<float4*>(a.part_o + at * 128 + c0) + cc * 8;
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            dst[j] = make_float4(__uint_as_float(orr[4 * j]) * inv, __uint_as_float(orr[4 * j + 1]) * inv,
+                                 __uint_as_float(orr[4 * j + 2]) * inv, __uint_as_float(orr[4 * j + 3]) * inv);
+        }
       }
     }
   }
