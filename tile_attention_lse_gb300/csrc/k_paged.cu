@@ -825,8 +825,7 @@ cp_status launch_early(void (*kern)(P), dim3 grid, dim3 block, int smem, bool ea
 // ---------------------------------------------------------------- merge ---
 // One tile that starts in block c and goes on behind it: its partial states
 // are the blocks' from c on.  O = sum_e w_e O_e / sum_e w_e, w_e = 2^(L_e - max L),
-// L in log2 units.  16 lanes per row, so a warp has two rows' loads under way;
-// the first pieces' O is asked for together with their weights.  What bounds
+// L in log2 units.  The first pieces' O is asked for together with their weights.  What bounds
 // it is its launch and three dependent loads (2 us): it starts while the attention
 // still runs and finds its tile meanwhile.
 constexpr int kMergeThreads = 128, kMergeRows = 32;
@@ -856,48 +855,56 @@ __device__ __forceinline__ void merge_block(const PagedArgs& a, int c, int part,
   if (!work) return;
   const int n = last - c + 1;
   auto slot = [&](int e) { return int64_t(e == 0 ? slot0 : 2 * (c + e)); };
-  constexpr int N = D / 16, kEager = 2;
-  const int half = lane >> 4, sl = lane & 15;
-  const uint32_t lanes = 0xffffu << (16 * half);
-  for (int i = 2 * warp + half; i < kMergeRows; i += kMergeThreads / 16) {
+  // A slice's partial O is [row][column], 16 lanes a row; a pair's is
+  // [4 columns][row] (float4), and 4 lanes with every fourth of them take a row, 8
+  // rows a warp side by side.
+  constexpr bool kPair = U == kPairUnit;
+  constexpr int kLanes = kPair ? 4 : 16, N = D / kLanes, kEager = kPair ? 1 : 2;
+  constexpr int kRowsAtOnce = 32 / kLanes;
+  const int which = kPair ? lane & 7 : lane >> 4, sl = kPair ? lane >> 3 : lane & 15;
+  const uint32_t lanes = kPair ? 0x01010101u << which : 0xffffu << (16 * which);  // a row's
+  auto load = [&](int e, int r, float* x) {
+#pragma unroll
+    for (int v = 0; v < N; v += 4) {
+      const int c4 = sl + kLanes * (v / 4);  // 4 columns
+      const int64_t at = kPair ? (slot(e) * (D / 4) + c4) * a.R + r : (slot(e) * a.R + r) * (D / 4) + c4;
+      load_vec<float, 4>(a.part_o + 4 * at, x + v);
+    }
+  };
+  for (int i = kRowsAtOnce * warp + which; i < kMergeRows; i += kMergeThreads / kLanes) {
     const int r = part * kMergeRows + i;
     if (r >= t.nrows) break;
-    auto load = [&](int e, float* x) {
-      const float* src = a.part_o + (slot(e) * a.R + r) * D + 4 * sl;
-#pragma unroll
-      for (int v = 0; v < N; v += 4) load_vec<float, 4>(src + 16 * v, x + v);
-    };
     float x[kEager][N];
 #pragma unroll
-    for (int j = 0; j < kEager; ++j) load(j, x[j]);  // n >= 2
-    const float first = sl < n ? a.part_l[slot(sl) * a.R + r] : -INFINITY;
+    for (int j = 0; j < kEager; ++j) load(j, r, x[j]);  // n >= 2
+    auto weigh = [&](int e0) { return e0 + sl < n ? a.part_l[slot(e0 + sl) * a.R + r] : -INFINITY; };
+    const float first = weigh(0);  // the whole of it, up to kLanes pieces
     float top = first;
-    for (int e = 16 + sl; e < n; e += 16) top = fmaxf(top, a.part_l[slot(e) * a.R + r]);
+    for (int e0 = kLanes; e0 < n; e0 += kLanes) top = fmaxf(top, weigh(e0));
 #pragma unroll
-    for (int o = 8; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(lanes, top, o, 16));
+    for (int o = kLanes / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(lanes, top, kPair ? 8 * o : o));
     float acc[N] = {};
     float sum = 0.f;
     if (top != -INFINITY) {  // an empty state's O is 0
-      auto add = [&](float we, const float* y) {
+      auto add = [&](float w, int j, const float* y) {
+        const float we = __shfl_sync(lanes, w, kPair ? which + 8 * j : 16 * which + j);
         sum += we;
 #pragma unroll
         for (int v = 0; v < N; ++v) acc[v] = fmaf(we, y[v], acc[v]);
       };
-      for (int e0 = 0; e0 < n; e0 += 16) {
-        const float l = e0 == 0 ? first : (e0 + sl < n ? a.part_l[slot(e0 + sl) * a.R + r] : -INFINITY);
-        const float w = exp2f(l - top);
-        const int m = min(16, n - e0);
-        int j0 = 0;
+      for (int e0 = 0; e0 < n; e0 += kLanes) {
+        const float w = exp2f((e0 == 0 ? first : weigh(e0)) - top);
+        const int m = min(kLanes, n - e0);
+        int j = 0;
         if (e0 == 0) {
-          j0 = kEager;
 #pragma unroll
-          for (int j = 0; j < kEager; ++j) add(__shfl_sync(lanes, w, j, 16), x[j]);
+          for (; j < kEager; ++j) add(w, j, x[j]);
         }
-#pragma unroll 4
-        for (int j = j0; j < m; ++j) {
+#pragma unroll 2
+        for (; j < m; ++j) {
           float y[N];
-          load(e0 + j, y);
-          add(__shfl_sync(lanes, w, j, 16), y);
+          load(e0 + j, r, y);
+          add(w, j, y);
         }
       }
     }
@@ -907,7 +914,8 @@ __device__ __forceinline__ void merge_block(const PagedArgs& a, int c, int part,
     const int row = t.row0 + r;
     const int64_t out = int64_t(q.q0 + row / a.G) * a.H + st.h * a.G + row % a.G;
 #pragma unroll
-    for (int v = 0; v < N; v += 4) store_vec<T, 4>(static_cast<T*>(a.o) + out * D + 4 * sl + 16 * v, acc + v);
+    for (int v = 0; v < N; v += 4)
+      store_vec<T, 4>(static_cast<T*>(a.o) + out * D + 4 * (sl + kLanes * (v / 4)), acc + v);
     if (sl == 0) a.lse[out] = sum > 0.f ? (top + log2f(sum)) * 0.69314718055994531f : -INFINITY;
   }
 }

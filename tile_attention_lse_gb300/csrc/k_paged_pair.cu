@@ -433,19 +433,34 @@ __global__ void __launch_bounds__(kThreads, 1) paged_pair_kernel(const __grid_co
         const uint32_t span = uint32_t(max(limit - lo0, 0));
         const uint32_t tS = tmem + lane_off + sb * 128;
         uint32_t sr[128];
-        if (!idle) {
+        float mx = -INFINITY;
+        if (full && !idle) {
           tc::tmem_ld32(tS, sr);
           tc::tmem_ld32(tS + 32, sr + 32);
           tc::tmem_ld32(tS + 64, sr + 64);
           tc::tmem_ld32(tS + 96, sr + 96);
           tc::tmem_wait_ld();
         }
-        // the scores are in registers: S_sb may take the next tile's scores
-        tc::fence_before_sync();
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive_remote(bar_even(B_SEMPTY0 + sb));
-        float mx = -INFINITY;
-        if (!idle) mx = (full ? row_max<false>(sr, 0, kTile) : row_max<true>(sr, lo0, span)) * sl2;
+        if (full || idle) {  // the scores are in registers: S_sb may take the next tile's scores
+          tc::fence_before_sync();
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive_remote(bar_even(B_SEMPTY0 + sb));
+          if (!idle) mx = row_max<false>(sr, 0, kTile) * sl2;
+        } else {
+          // A tile that the mask cuts is read 32 scores at a time, now and
+          // again for P, in loops: unrolled like the others its code
+          // came from memory once a launch, 4 to 11 us.
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            uint32_t s32[32];
+            tc::tmem_ld32(tS + 32 * c, s32);
+            tc::tmem_wait_ld();
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              mx = fmaxf(mx, uint32_t(32 * c + j - lo0) < span ? __uint_as_float(s32[j]) : -INFINITY);
+          }
+          mx *= sl2;
+        }
         // the running max after tile g - 1 (every tile but the stream's first
         // waits, so each barrier is waited once per phase; a piece's first tile
         // starts from -inf)
@@ -476,7 +491,28 @@ __global__ void __launch_bounds__(kThreads, 1) paged_pair_kernel(const __grid_co
         }
         if (!idle) {
           const uint32_t tP = tmem + lane_off + kColP + sb * 64;
-          l += full ? p_pass<false>(sr, 0, kTile, mu, sl2x2, tP) : p_pass<true>(sr, lo0, span, mu, sl2x2, tP);
+          if (full) {
+            l += p_pass<false>(sr, 0, kTile, mu, sl2x2, tP);
+          } else {
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+              uint32_t s32[32], pk[16];
+              tc::tmem_ld32(tS + 32 * c, s32);
+              tc::tmem_wait_ld();
+#pragma unroll
+              for (int j = 0; j < 32; j += 2) {
+                const int k = 32 * c + j - lo0;
+                const float p0 = uint32_t(k) < span ? tc::ex2(fmaf(__uint_as_float(s32[j]), sl2, -mu)) : 0.f;
+                const float p1 = uint32_t(k + 1) < span ? tc::ex2(fmaf(__uint_as_float(s32[j + 1]), sl2, -mu)) : 0.f;
+                l += p0 + p1;
+                pk[j / 2] = tc::pack_bf16x2(p0, p1);
+              }
+              tc::tmem_st16(tP + 16 * c, pk);
+            }
+            tc::fence_before_sync();
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive_remote(bar_even(B_SEMPTY0 + sb));
+          }
           if (t > 0 && __any_sync(0xffffffffu, grow)) {
             // O holds the sum up to tile g - 1 against m_in once the PV that
             // read P of tile g - 1 is complete (the next PV waits for this P).
@@ -560,22 +596,53 @@ __global__ void __launch_bounds__(kThreads, 1) paged_pair_kernel(const __grid_co
           __syncwarp();
           if (lane == 0) tc::mbar_arrive_remote(bar_even(B_OEMPTY));
         }
-        if (row_ok && direct) {
-          uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.o) + at * 128 + c0) + cc * 4;
+        if (idle) continue;
+        if (direct) {
+          uint4 v[4];  // 16-byte chunk j of this lane's row
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             const uint32_t* e = orr + 8 * j;
-            dst[j] = make_uint4(tc::pack_bf16x2(__uint_as_float(e[0]) * inv, __uint_as_float(e[1]) * inv),
-                                tc::pack_bf16x2(__uint_as_float(e[2]) * inv, __uint_as_float(e[3]) * inv),
-                                tc::pack_bf16x2(__uint_as_float(e[4]) * inv, __uint_as_float(e[5]) * inv),
-                                tc::pack_bf16x2(__uint_as_float(e[6]) * inv, __uint_as_float(e[7]) * inv));
+            v[j] = make_uint4(tc::pack_bf16x2(__uint_as_float(e[0]) * inv, __uint_as_float(e[1]) * inv),
+                              tc::pack_bf16x2(__uint_as_float(e[2]) * inv, __uint_as_float(e[3]) * inv),
+                              tc::pack_bf16x2(__uint_as_float(e[4]) * inv, __uint_as_float(e[5]) * inv),
+                              tc::pack_bf16x2(__uint_as_float(e[6]) * inv, __uint_as_float(e[7]) * inv));
+          }
+          // four lanes turn their rows' chunks about: chunk (lane & 3) of row j
+          // of the four, so that a store writes 64 bytes of a row
+#pragma unroll
+          for (int s = 1; s < 4; s <<= 1) {
+            const bool up = lane & s;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              if (j & s) continue;
+              const uint4 send = up ? v[j] : v[j | s];
+              uint4 got;
+              got.x = __shfl_xor_sync(0xffffffffu, send.x, s);
+              got.y = __shfl_xor_sync(0xffffffffu, send.y, s);
+              got.z = __shfl_xor_sync(0xffffffffu, send.z, s);
+              got.w = __shfl_xor_sync(0xffffffffu, send.w, s);
+              if (up)
+                v[j] = got;
+              else
+                v[j | s] = got;
+            }
+          }
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int64_t at_j = __shfl_sync(0xffffffffu, at, (lane & ~3) + j);
+            if (quarter * 32 + (lane & ~3) + j < rows_here)
+              *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.o) + at_j * 128 + c0 + cc * 32 + 8 * (lane & 3)) =
+                  v[j];
           }
         } else if (row_ok) {
-          float4* dst = reinterpret_cast<float4*>(a.part_o + at * 128 + c0) + cc * 8;
+          // partial O: [slot][4 columns][row] float4, the rows of a warp side by side
+          float4* dst = reinterpret_cast<float4*>(a.part_o) +
+                        (int64_t(pc.slot) * 32 + (c0 + cc * 32) / 4) * a.R + trow;
 #pragma unroll
           for (int j = 0; j < 8; ++j)
-            dst[j] = make_float4(__uint_as_float(orr[4 * j]) * inv, __uint_as_float(orr[4 * j + 1]) * inv,
-                                 __uint_as_float(orr[4 * j + 2]) * inv, __uint_as_float(orr[4 * j + 3]) * inv);
+            dst[int64_t(j) * a.R] =
+                make_float4(__uint_as_float(orr[4 * j]) * inv, __uint_as_float(orr[4 * j + 1]) * inv,
+                            __uint_as_float(orr[4 * j + 2]) * inv, __uint_as_float(orr[4 * j + 3]) * inv);
         }
       }
     }
