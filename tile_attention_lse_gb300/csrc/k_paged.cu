@@ -144,7 +144,9 @@ struct SliceOut {
 template <int D, int R>
 struct SliceBf16 {
   using T = __nv_bfloat16;
-  static constexpr int kWarps = 8, kPerStage = 4, kKeys = 16, kStages = D == 128 ? 4 : 8;  // kPerStage: workers of a stage
+  // 32 rows of 128 columns: the states of four workers are what shared memory holds
+  static constexpr int kWarps = D * R > 64 * 32 && R > 16 ? 4 : 8, kPerStage = 4, kKeys = 16;  // kPerStage: workers of a stage
+  static constexpr int kStages = D == 128 ? 4 : 8;
   static constexpr int kStageKeys = kPerStage * kKeys;
   static __device__ __forceinline__ int first_key(int warp) { return (warp % kPerStage) * kKeys; }  // a worker's slice of a stage
   static constexpr int MT = R / 16, NT = D / 8;
@@ -152,7 +154,7 @@ struct SliceBf16 {
   static constexpr int kQBytes = R * D * 2;
   static constexpr int kScratch = 0;
   static constexpr int kState = (kAcc / 4 + kRows / 2) * 32;  // float4s of a worker's state
-  static constexpr int kPieces = 4;  // pieces that the scheduler is ahead
+  static constexpr int kPieces = kWarps == 4 ? 3 : 4;  // pieces that the producers are ahead
   static constexpr bool kKeepQ = MT == 1;
   float acc[kAcc];
   float m[kRows], l[kRows];
@@ -930,7 +932,7 @@ __global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const __grid
   __shared__ int64_t s_scan[32];
   __shared__ PagedStart s_start;
   const int n_pair = p.pair.grid * p.pair_parts;
-  if constexpr (D == 128 && sizeof(T) == 2) {
+  if constexpr (sizeof(T) == 2) {
     if (int(blockIdx.x) < n_pair)
       return merge_block<T, D, kPairUnit, kPairExtra>(p.pair, blockIdx.x / p.pair_parts, blockIdx.x % p.pair_parts,
                                                       s_scan, s_start);
@@ -979,7 +981,8 @@ cp_status launch_paged_slice(const PagedArgs& a, PagedKernel k, bool after_pair,
       return a.d == 128 ? run_slice<SliceBf16<128, 16>, 128, 16>(a, after_pair, s)
                         : run_slice<SliceBf16<64, 16>, 64, 16>(a, after_pair, s);
     if (k == kPagedSlice32)
-      return a.d == 64 ? run_slice<SliceBf16<64, 32>, 64, 32>(a, after_pair, s) : CP_ERR_UNSUPPORTED;
+      return a.d == 128 ? run_slice<SliceBf16<128, 32>, 128, 32>(a, after_pair, s)
+                        : run_slice<SliceBf16<64, 32>, 64, 32>(a, after_pair, s);
     return CP_ERR_UNSUPPORTED;
   }
   if (k == kPagedSlice4)
@@ -993,7 +996,7 @@ cp_status launch_paged_slice(const PagedArgs& a, PagedKernel k, bool after_pair,
 
 cp_status launch_paged_merge(const PagedArgs& pair, const PagedArgs& slice, cudaStream_t s) {
   const PagedArgs& a = pair.grid > 0 ? pair : slice;
-  if (pair.grid > 0 && (a.d != 128 || a.dtype != CP_BF16)) return CP_ERR_UNSUPPORTED;
+  if (pair.grid > 0 && a.dtype != CP_BF16) return CP_ERR_UNSUPPORTED;
   if (a.dtype == CP_BF16)
     return a.d == 128 ? run_merge<__nv_bfloat16, 128>(pair, slice, s) : run_merge<__nv_bfloat16, 64>(pair, slice, s);
   return a.d == 128 ? run_merge<float, 128>(pair, slice, s) : run_merge<float, 64>(pair, slice, s);

@@ -1,4 +1,4 @@
-// Paged attention of many rows (bf16, head_dim 128) on pairs of SMs
+// Paged attention of many rows (bf16) on pairs of SMs
 // (cta_group::2, sm_103a): chunks of prompts over their pages.
 //
 // The mathematics is the slice kernel's (k_paged.cu): one pass over the visible
@@ -22,6 +22,10 @@
 //    asynchronous copies that zero-fill the keys outside, a tile or two per
 //    piece; all others come by TMA.  V has a producer of its own: its plain copies
 //    hold up no K, and a box costs its issuer about 55 ns (pages of 16: 16 boxes a tile).
+//  - head_dim 64: K has half the steps.  The second product keeps N = 128: the
+//    even CTA's half of V is all 64 columns, the odd one's is never written and
+//    its columns of O never read (the pair is bound by its softmax by then, and
+//    a half of 32 columns would need another swizzle).
 //  - Work is the common axis of paged.h: a pair runs an equal share of
 //    all key tiles, and a tile that is cut leaves float32 partial states.
 #include <cuda_bf16.h>
@@ -46,7 +50,7 @@ constexpr int kSmallRegs = 72, kSoftmaxRegs = 216;
 static_assert(128 * kSmallRegs + 256 * kSoftmaxRegs == kThreads * kLaunchRegs,
               "register split must add up to the launch total");
 constexpr uint32_t kQBytes = 128 * 128 * 2, kQHalf = kQBytes / 2;  // this CTA's Q tile, one 64-column box of it
-constexpr uint32_t kKBytes = 64 * 128 * 2;                         // its half of a key tile (64 keys)
+constexpr uint32_t kKBytes = 64 * 128 * 2;                         // its half of a key tile (64 keys), head_dim 128
 constexpr uint32_t kVBytes = 128 * 64 * 2;                         // its half of a value tile (64 columns)
 constexpr int kQBufs = 2, kKStages = 4, kVStages = 4, kSBufs = 2;
 constexpr int kOffQ = 0;
@@ -119,7 +123,7 @@ using Walk = PagedWalk<kPairUnit, kPairExtra>;
 
 // kShortWaits: the copy launched while cp_debug_set_wait_limit has set a
 // short wait budget; the default copy never reads the limit.
-template <bool kShortWaits>
+template <int D, bool kShortWaits>
 __global__ void __launch_bounds__(kThreads, 1) paged_pair_kernel(const __grid_constant__ Params p) {
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t sbase = tc::smem_u32(smem);
@@ -218,12 +222,12 @@ __global__ void __launch_bounds__(kThreads, 1) paged_pair_kernel(const __grid_co
     auto load_k = [&](int t, int32_t pg) -> bool {
       const uint32_t st = kg % kKStages;
       if (!__all_sync(0xffffffffu, wt(B_KEMPTY0 + st, ((kg / kKStages) & 1) ^ 1))) return false;
-      if (even && lane == 0) tc::mbar_arrive_expect_tx(bar(B_KFULL0 + st), 2 * kKBytes);
-      // box b: keys (b / 2) box .. of this CTA's 64, columns 64 (b & 1) ..
-      const int sub = lane >> 1, col = lane & 1;
+      if (even && lane == 0) tc::mbar_arrive_expect_tx(bar(B_KFULL0 + st), 2 * (64 * D * 2));
+      // this lane's box: of this CTA's 64 keys those from sub * box on, columns 64 col ..
+      const int sub = lane / (D / 64), col = lane % (D / 64);
       const int key = 64 * int(rank) + (sub << bs);
       const int32_t mine = __shfl_sync(0xffffffffu, pg, (key >> 3) & 31);
-      if (lane < (128 >> bs))
+      if (sub < (64 >> bs))
         load_box(sK + st * kKBytes + col * (kKBytes / 2) + ((sub << bs) * 128), &p.tmk, bar_even(B_KFULL0 + st),
                  64 * col, t * kPairUnit + key, mine);
       ++kg;
@@ -237,7 +241,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_pair_kernel(const __grid_co
       const bool cut = (lo > k0 && (lo & (box - 1))) ||
                        (hi < k0 + kPairUnit && (hi & (box - 1)) && ((hi | (box - 1)) + 1) > pc.q.kv);
       if (!cut) {
-        if (even && lane == 0) tc::mbar_arrive_expect_tx(bar(B_VFULL0 + st), 2 * kVBytes);
+        if (even && lane == 0) tc::mbar_arrive_expect_tx(bar(B_VFULL0 + st), D == 128 ? 2 * kVBytes : kVBytes);
         const int key = lane << bs;
         const int32_t mine = __shfl_sync(0xffffffffu, pg, (key >> 3) & 31);
         if (lane < (128 >> bs))
@@ -256,7 +260,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_pair_kernel(const __grid_co
         asm volatile("cp.async.wait_all;" ::: "memory");
         tc::fence_proxy_async_smem();
         __syncwarp();
-        if (!even) {
+        if (D == 64) {
+          if (lane == 0) tc::mbar_arrive(bar(B_VFULL0 + st));
+        } else if (!even) {
           if (lane == 0) arrive_cluster(bar_even(B_VODD0 + st));
         } else {
           bool r = tc::wait_bounded<kShortWaits, true>(bar(B_VODD0 + st), (odd_parity >> st) & 1, abort_flag, a.err,
@@ -270,6 +276,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_pair_kernel(const __grid_co
       ++vg;
       return true;
     };
+    if (D == 64 && !even && !of_k) ok = false;  // no half of V of its own
     while (ok && w.next(a, pc)) {
       const int n = pc.ub - pc.ua, t0 = pc.tile.b0 + pc.ua;
       if (n == 0) continue;
@@ -279,10 +286,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_pair_kernel(const __grid_co
         ok = __all_sync(0xffffffffu, wt(B_QEMPTY0 + qb, ((qi / kQBufs) & 1) ^ 1));
         if (!ok) break;
         if (lane == 0) {
-          if (even) tc::mbar_arrive_expect_tx(bar(B_QFULL0 + qb), 4u * 128u * uint32_t(half_rows));
+          if (even) tc::mbar_arrive_expect_tx(bar(B_QFULL0 + qb), (D / 32) * 128u * uint32_t(half_rows));
           const int tok = pc.q.q0 + (pc.tile.row0 + int(rank) * half_rows) / a.G, h = pc.h * a.G;
           tc::tma_load_3d_pair(sQ + qb * kQBytes, &p.tmq, bar_even(B_QFULL0 + qb), 0, h, tok);
-          tc::tma_load_3d_pair(sQ + qb * kQBytes + kQHalf, &p.tmq, bar_even(B_QFULL0 + qb), 64, h, tok);
+          if (D == 128) tc::tma_load_3d_pair(sQ + qb * kQBytes + kQHalf, &p.tmq, bar_even(B_QFULL0 + qb), 64, h, tok);
         }
         ++qi;
       }
@@ -342,7 +349,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_pair_kernel(const __grid_co
           tc::fence_after_sync();
           const uint64_t kd = tc::kmajor_desc(sK + st * kKBytes);
 #pragma unroll
-          for (int kk = 0; kk < 8; ++kk)
+          for (int kk = 0; kk < D / 16; ++kk)
             tc::mma_pair_ss(tmem + sb * 128, tc::kmajor_step(qd, kk), khalf_step(kd, kk), kIdescS, kk > 0 ? 1u : 0u);
           tc::mma_commit_pair(bar(B_SFULL0 + sb), kBothCtas);
           tc::mma_commit_pair(bar(B_KEMPTY0 + st), kBothCtas);
@@ -524,7 +531,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_pair_kernel(const __grid_co
             if (!ok) break;
             tc::fence_after_sync();
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
+            for (int c = 0; c < D / 32; ++c) {
               uint32_t orr[32];
               tc::tmem_ld32(tO + c * 32, orr);
               tc::tmem_wait_ld();
@@ -574,7 +581,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_pair_kernel(const __grid_co
         else
           a.part_l[at] = l2;
       }
-      const int c0 = 64 * half;  // each warp writes 64 columns
+      const int c0 = D / 2 * half;  // each warp writes half of the columns
       if (n > 0) {
         ok = __all_sync(0xffffffffu, wt(B_ODONE, items & 1));
         if (!ok) break;
@@ -582,7 +589,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_pair_kernel(const __grid_co
         ++items;
       }
 #pragma unroll
-      for (int cc = 0; cc < 2; ++cc) {
+      for (int cc = 0; cc < D / 64; ++cc) {
         uint32_t orr[32];
         if (n > 0 && !idle) {
           tc::tmem_ld32(tO + c0 + cc * 32, orr);
@@ -591,7 +598,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_pair_kernel(const __grid_co
 #pragma unroll
           for (int j = 0; j < 32; ++j) orr[j] = 0u;
         }
-        if (n > 0 && cc == 1) {  // O is in registers: the next piece's first PV may overwrite it
+        if (n > 0 && cc == D / 64 - 1) {  // O is in registers: the next piece's first PV may overwrite it
           tc::fence_before_sync();
           __syncwarp();
           if (lane == 0) tc::mbar_arrive_remote(bar_even(B_OEMPTY));
@@ -631,13 +638,13 @@ __global__ void __launch_bounds__(kThreads, 1) paged_pair_kernel(const __grid_co
           for (int j = 0; j < 4; ++j) {
             const int64_t at_j = __shfl_sync(0xffffffffu, at, (lane & ~3) + j);
             if (quarter * 32 + (lane & ~3) + j < rows_here)
-              *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.o) + at_j * 128 + c0 + cc * 32 + 8 * (lane & 3)) =
+              *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.o) + at_j * D + c0 + cc * 32 + 8 * (lane & 3)) =
                   v[j];
           }
         } else if (row_ok) {
           // partial O: [slot][4 columns][row] float4, the rows of a warp side by side
           float4* dst = reinterpret_cast<float4*>(a.part_o) +
-                        (int64_t(pc.slot) * 32 + (c0 + cc * 32) / 4) * a.R + trow;
+                        (int64_t(pc.slot) * (D / 4) + (c0 + cc * 32) / 4) * a.R + trow;
 #pragma unroll
           for (int j = 0; j < 8; ++j)
             dst[int64_t(j) * a.R] =
@@ -669,8 +676,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_pair_kernel(const __grid_co
 bool make_tmap_packed(CUtensorMap* map, const PagedArgs& a, int tokens) {
   auto enc = tmap_encoder();
   if (!enc) return false;
-  const cuuint64_t dims[3] = {128, cuuint64_t(a.H), cuuint64_t(a.rows)};
-  const cuuint64_t strides[2] = {256, cuuint64_t(a.q_stride) * 2};
+  const cuuint64_t dims[3] = {cuuint64_t(a.d), cuuint64_t(a.H), cuuint64_t(a.rows)};
+  const cuuint64_t strides[2] = {cuuint64_t(a.d) * 2, cuuint64_t(a.q_stride) * 2};
   const cuuint32_t b[3] = {64, cuuint32_t(a.G), cuuint32_t(tokens)};
   const cuuint32_t es[3] = {1, 1, 1};
   return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(a.q), dims, strides, b, es,
@@ -693,17 +700,24 @@ cudaLaunchConfig_t pair_config(cudaLaunchAttribute* attr, int pairs, cudaStream_
   return cfg;
 }
 
+using Kernel = void (*)(Params);
+Kernel pair_kernel(int d, bool short_waits) {
+  if (d == 128) return short_waits ? paged_pair_kernel<128, true> : paged_pair_kernel<128, false>;
+  return short_waits ? paged_pair_kernel<64, true> : paged_pair_kernel<64, false>;
+}
+
 }  // namespace
 
-cp_status paged_pair_grid(int32_t* pairs) {
+cp_status paged_pair_grid(int32_t d, int32_t* pairs) {
   const bool short_waits = wait_limit_cycles() < tc::kWaitCycles;
-  auto* kern = short_waits ? paged_pair_kernel<true> : paged_pair_kernel<false>;
+  const Kernel kern = pair_kernel(d, short_waits);
   // per copy and device, set up by the first launch (under a lock: host threads may race on it)
-  static std::atomic<int> max_pairs[2][64] = {};
+  static std::atomic<int> max_pairs[4][64] = {};
+  const int copy = (d == 128 ? 2 : 0) + short_waits;
   static std::mutex setup_mu;
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return CP_ERR_CUDA;
-  int n = max_pairs[short_waits][dev].load(std::memory_order_acquire);
+  int n = max_pairs[copy][dev].load(std::memory_order_acquire);
   if (n == 0) {
     std::lock_guard<std::mutex> lock(setup_mu);
     // The register hand-over inside the kernel assumes the launch count.
@@ -716,14 +730,14 @@ cp_status paged_pair_grid(int32_t* pairs) {
     const cudaLaunchConfig_t cfg = pair_config(attr, num_sms() / 2, nullptr);
     if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n < 1) return CP_ERR_UNSUPPORTED;
     if (n > num_sms() / 2) n = num_sms() / 2;
-    max_pairs[short_waits][dev].store(n, std::memory_order_release);
+    max_pairs[copy][dev].store(n, std::memory_order_release);
   }
   *pairs = n;
   return CP_OK;
 }
 
 cp_status launch_paged_pair(const PagedArgs& a, cudaStream_t s) {
-  if (a.dtype != CP_BF16 || a.d != 128 || a.G > kPairRows) return CP_ERR_UNSUPPORTED;
+  if (a.dtype != CP_BF16 || a.G > kPairRows) return CP_ERR_UNSUPPORTED;
   Params p;
   const int page = 1 << a.page_shift, box = page < 64 ? page : 64;
   if (!make_tmap_packed(&p.tmq, a, kPairRows / a.G) || !make_tmap_pages(&p.tmk, a.k, a, box) ||
@@ -736,7 +750,7 @@ cp_status launch_paged_pair(const PagedArgs& a, cudaStream_t s) {
   p.wait_limit = wait_limit_cycles();
   cudaLaunchAttribute attr[1];
   const cudaLaunchConfig_t cfg = pair_config(attr, a.grid, s);
-  auto* kern = p.wait_limit < tc::kWaitCycles ? paged_pair_kernel<true> : paged_pair_kernel<false>;
+  const Kernel kern = pair_kernel(a.d, p.wait_limit < tc::kWaitCycles);
   if (cudaLaunchKernelEx(&cfg, kern, p) != cudaSuccess) return CP_ERR_CUDA;
   return cuda_status(cudaGetLastError());
 }

@@ -214,7 +214,7 @@ cp_status launch_paged_merge(const PagedArgs& pair, const PagedArgs& slice, cuda
 int paged_slice_grid();
 cp_status launch_paged_pair(const PagedArgs& a, cudaStream_t s);
 // Pairs of SMs that can run at once (sets the kernel up on the first call).
-cp_status paged_pair_grid(int32_t* pairs);
+cp_status paged_pair_grid(int32_t d, int32_t* pairs);
 
 // Rotation of the pairs of a head (cp_rope): turns per position of every
 // pair as 64-bit binary fractions, and the pair's axis.

@@ -94,12 +94,14 @@ cp_status make_turns(const cp_rope* r, int32_t head_dim, RopeTurns* t) {
 }
 
 // The launches of a call, by its types and by the packed rows of a request
-// (max_new * G at most).  bf16 with head_dim 128: requests of up to 16 rows
-// run on the slice kernel (bound by their keys' bytes), those of more on the
-// pair kernel (bound by the products); where both may come, both are
-// launched, each for its own requests (measured on 20 single tokens and 4 chunks of
-// up to 509 over 6000 cached tokens: 250 us with all of them on the pair kernel).  A single
-// request of unknown length runs on the pair kernel whatever it brings.
+// (max_new * G at most).  bf16: requests of up to 16 rows run on the slice kernel
+// (bound by their keys' bytes), and so do up to 32 where none has more
+// (32 requests of 8 tokens over 4000 keys, 4 heads a group: 101 us, 131 on
+// the pair kernel); those of more on the pair kernel (bound by the products and the
+// softmax).  Where both may come, both are launched, each for its own
+// requests (20 single tokens and 4 chunks of up to 509 over 6000
+// cached tokens: 251 us with all of them on the pair kernel, 231 on both).  A
+// single request of unknown length runs on the pair kernel whatever it brings.
 struct PagedPlan {
   PagedKernel slice = kPagedSlice16;
   bool use_slice = true, use_pair = false;
@@ -110,13 +112,11 @@ PagedPlan pick_kernels(const cp_paged_desc& d, int32_t n_reqs) {
   PagedPlan p;
   if (d.kv.dtype == CP_F32) {
     p.slice = rows <= 4 ? kPagedSlice4 : kPagedSlice16;
+  } else if (rows > 32 && G <= kPairRows) {
+    p.use_pair = true;
+    p.use_slice = n_reqs > 1 && G <= 16;
   } else if (rows > 16) {
-    if (d.kv.head_dim == 64) {
-      p.slice = kPagedSlice32;
-    } else if (G <= kPairRows) {
-      p.use_pair = true;
-      p.use_slice = n_reqs > 1 && G <= 16;
-    }
+    p.slice = kPagedSlice32;
   }
   return p;
 }
@@ -425,7 +425,7 @@ cp_status cp_paged_attn_fwd(const cp_paged_desc* desc, int32_t n_reqs, int64_t r
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cp_status r = CP_OK;
   if (plan.use_pair) {
-    r = paged_pair_grid(&pair.grid);
+    r = paged_pair_grid(c.head_dim, &pair.grid);
     if (r != CP_OK) return r;
     ProfScope ps(CP_K_PAGED, s);
     r = launch_paged_pair(pair, s);
