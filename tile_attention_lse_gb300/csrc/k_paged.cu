@@ -410,7 +410,7 @@ struct SliceF32 {
     uint64_t s2[RW];                   // sums over even and odd elements of the head
 #pragma unroll
     for (int r = 0; r < RW; ++r) s2[r] = 0;
-#pragma unroll 2
+#pragma unroll 4
     for (int c = 0; c < D / 4; ++c) {
       uint64_t k0, k1;
       lds2(sk + at(srow + lane, c), k0, k1);

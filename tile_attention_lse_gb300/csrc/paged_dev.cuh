@@ -6,7 +6,7 @@
 namespace cpattn {
 
 // Tiles that a thread sums by itself; a request of more is summed by its whole warp.
-constexpr int kOwnTiles = 4;
+constexpr int kOwnTiles = 16;
 
 // Finds where the first unit of block c lies and returns the shares; the whole
 // block calls it, `sh` holds 32 int64 and `out` a PagedStart in shared memory
