@@ -415,172 +415,190 @@ __global__ void __launch_bounds__(kThreads, 1) paged_pair_kernel(const __grid_co
     uint32_t g = 0, items = 0, pieces = 0;
     bool ok = true;
     PagedPiece pc;
-    while (ok && w.next(a, pc)) {
-      const int n = pc.ub - pc.ua, t0 = pc.tile.b0 + pc.ua;
-      const int rows_here = min(max(pc.tile.nrows - int(rank) * half_rows, 0), half_rows);
-      const bool row_ok = row < rows_here;
-      const bool idle = quarter * 32 >= rows_here;  // no row of this warp
-      // rows behind the last are masked like it (their sums go nowhere)
-      const int prow = pc.tile.row0 + int(rank) * half_rows + min(row, max(rows_here - 1, 0));
-      const int qpos = pc.q.kv - pc.q.nq + prow / a.G;
-      const int vis_hi = a.causal ? min(pc.q.kv, qpos + 1) : pc.q.kv;
-      const int vis_lo = a.window > 0 ? max(qpos - a.window + 1, 0) : 0;
-      float m_own = -INFINITY, l = 0.f;  // this warp's row sum and the max it is taken against
-      for (int t = 0; t < n && ok; ++t, ++g) {
-        if (int(g & 1) != half) continue;  // the other warp's tile
-        const uint32_t sb = g % kSBufs;
-        ok = __all_sync(0xffffffffu, wt(B_SFULL0 + sb, (g / kSBufs) & 1));
-        if (!ok) break;
-        tc::fence_after_sync();
-        // visible keys of this row in this tile: lo <= j < limit
-        const int kpos0 = (t0 + t) * kPairUnit;
-        const int limit = min(vis_hi - kpos0, kTile);
-        const int lo0 = max(vis_lo - kpos0, 0);
-        const bool full = __all_sync(0xffffffffu, limit >= kTile && lo0 == 0);
-        const uint32_t span = uint32_t(max(limit - lo0, 0));
-        const uint32_t tS = tmem + lane_off + sb * 128;
-        uint32_t sr[128];
-        float mx = -INFINITY;
-        if (full && !idle) {
-          tc::tmem_ld32(tS, sr);
-          tc::tmem_ld32(tS + 32, sr + 32);
-          tc::tmem_ld32(tS + 64, sr + 64);
-          tc::tmem_ld32(tS + 96, sr + 96);
-          tc::tmem_wait_ld();
-        }
-        if (full || idle) {  // the scores are in registers: S_sb may take the next tile's scores
-          tc::fence_before_sync();
-          __syncwarp();
-          if (lane == 0) tc::mbar_arrive_remote(bar_even(B_SEMPTY0 + sb));
-          if (!idle) mx = row_max<false>(sr, 0, kTile) * sl2;
-        } else {
-          // A tile that the mask cuts is read 32 scores at a time, now and
-          // again for P, in loops: unrolled like the others its code
-          // came from memory once a launch, 4 to 11 us.
-#pragma unroll 1
-          for (int c = 0; c < 4; ++c) {
-            uint32_t s32[32];
-            tc::tmem_ld32(tS + 32 * c, s32);
-            tc::tmem_wait_ld();
-#pragma unroll
-            for (int j = 0; j < 32; ++j)
-              mx = fmaxf(mx, uint32_t(32 * c + j - lo0) < span ? __uint_as_float(s32[j]) : -INFINITY);
-          }
-          mx *= sl2;
-        }
-        // the running max after tile g - 1 (every tile but the stream's first
-        // waits, so each barrier is waited once per phase; a piece's first tile
-        // starts from -inf)
-        float m_in = -INFINITY;
-        if (g > 0) {
-          const uint32_t pq = (g - 1) & 1;
-          ok = __all_sync(0xffffffffu, wt(B_MREADY0 + 2 * quarter + int(pq), ((g - 1) >> 1) & 1));
-          if (!ok) break;
-          if (t > 0) m_in = mrow[pq * 128 + row];
-        }
-        const float m_up = fmaxf(m_in, mx);
-        const bool grow = m_up > m_in + 8.0f;  // also true when m_in is -inf and m_up finite
-        const float m = grow ? m_up : m_in;
-        mrow[(g & 1) * 128 + row] = m;
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(bar(B_MREADY0 + 2 * quarter + int(g & 1)));
-        if (m != m_own) {  // this warp's sum, against the new max
-          l = (m_own == -INFINITY) ? 0.f : l * tc::ex2(m_own - m);
-          m_own = m;
-        }
-        const float mu = (m == -INFINITY) ? 0.f : m;
-        // P buffer sb was last read by the PV of tile g - 2 (this warp waits
-        // for every such phase, in order)
-        if (g >= uint32_t(kSBufs)) {
-          ok = __all_sync(0xffffffffu, wt(B_PVDONE0 + sb, ((g / kSBufs) - 1) & 1));
+    // One call of next() serves the first piece and, between a piece's tiles
+    // and its O, the one behind it: the last PV is still running then.
+    bool have = false;
+    for (;;) {
+      int n = 0, rows_here = 0, slot = -1, trow = 0;
+      bool row_ok = false, idle = true;
+      int64_t at = 0;
+      float inv = 0.f;
+      if (have) {
+        n = pc.ub - pc.ua;
+        const int t0 = pc.tile.b0 + pc.ua;
+        rows_here = min(max(pc.tile.nrows - int(rank) * half_rows, 0), half_rows);
+        row_ok = row < rows_here;
+        idle = quarter * 32 >= rows_here;  // no row of this warp
+        // rows behind the last are masked like it (their sums go nowhere)
+        const int prow = pc.tile.row0 + int(rank) * half_rows + min(row, max(rows_here - 1, 0));
+        const int qpos = pc.q.kv - pc.q.nq + prow / a.G;
+        const int vis_hi = a.causal ? min(pc.q.kv, qpos + 1) : pc.q.kv;
+        const int vis_lo = a.window > 0 ? max(qpos - a.window + 1, 0) : 0;
+        float m_own = -INFINITY, l = 0.f;  // this warp's row sum and the max it is taken against
+        for (int t = 0; t < n && ok; ++t, ++g) {
+          if (int(g & 1) != half) continue;  // the other warp's tile
+          const uint32_t sb = g % kSBufs;
+          ok = __all_sync(0xffffffffu, wt(B_SFULL0 + sb, (g / kSBufs) & 1));
           if (!ok) break;
           tc::fence_after_sync();
-        }
-        if (!idle) {
-          const uint32_t tP = tmem + lane_off + kColP + sb * 64;
-          if (full) {
-            l += p_pass<false>(sr, 0, kTile, mu, sl2x2, tP);
-          } else {
-#pragma unroll 1
-            for (int c = 0; c < 4; ++c) {
-              uint32_t s32[32], pk[16];
-              tc::tmem_ld32(tS + 32 * c, s32);
-              tc::tmem_wait_ld();
-#pragma unroll
-              for (int j = 0; j < 32; j += 2) {
-                const int k = 32 * c + j - lo0;
-                const float p0 = uint32_t(k) < span ? tc::ex2(fmaf(__uint_as_float(s32[j]), sl2, -mu)) : 0.f;
-                const float p1 = uint32_t(k + 1) < span ? tc::ex2(fmaf(__uint_as_float(s32[j + 1]), sl2, -mu)) : 0.f;
-                l += p0 + p1;
-                pk[j / 2] = tc::pack_bf16x2(p0, p1);
-              }
-              tc::tmem_st16(tP + 16 * c, pk);
-            }
+          // visible keys of this row in this tile: lo <= j < limit
+          const int kpos0 = (t0 + t) * kPairUnit;
+          const int limit = min(vis_hi - kpos0, kTile);
+          const int lo0 = max(vis_lo - kpos0, 0);
+          const bool full = __all_sync(0xffffffffu, limit >= kTile && lo0 == 0);
+          const uint32_t span = uint32_t(max(limit - lo0, 0));
+          const uint32_t tS = tmem + lane_off + sb * 128;
+          uint32_t sr[128];
+          float mx = -INFINITY;
+          if (full && !idle) {
+            tc::tmem_ld32(tS, sr);
+            tc::tmem_ld32(tS + 32, sr + 32);
+            tc::tmem_ld32(tS + 64, sr + 64);
+            tc::tmem_ld32(tS + 96, sr + 96);
+            tc::tmem_wait_ld();
+          }
+          if (full || idle) {  // the scores are in registers: S_sb may take the next tile's scores
             tc::fence_before_sync();
             __syncwarp();
             if (lane == 0) tc::mbar_arrive_remote(bar_even(B_SEMPTY0 + sb));
-          }
-          if (t > 0 && __any_sync(0xffffffffu, grow)) {
-            // O holds the sum up to tile g - 1 against m_in once the PV that
-            // read P of tile g - 1 is complete (the next PV waits for this P).
-            // That phase is the latest one of its barrier: PV(g - 3) is
-            // complete (PV(g - 2) is, see above) and PV(g + 1) waits for PV(g).
-            const float corr = (m_in == -INFINITY) ? 0.f : tc::ex2(m_in - m);
-            const uint32_t pb = (g - 1) % kSBufs;
-            ok = __all_sync(0xffffffffu, wt(B_PVDONE0 + pb, ((g - 1) / kSBufs) & 1));
-            if (!ok) break;
-            tc::fence_after_sync();
-#pragma unroll
-            for (int c = 0; c < D / 32; ++c) {
-              uint32_t orr[32];
-              tc::tmem_ld32(tO + c * 32, orr);
+            if (!idle) mx = row_max<false>(sr, 0, kTile) * sl2;
+          } else {
+            // A tile that the mask cuts is read 32 scores at a time, now and
+            // again for P, in loops: unrolled like the others its code
+            // came from memory once a launch, 4 to 11 us.
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+              uint32_t s32[32];
+              tc::tmem_ld32(tS + 32 * c, s32);
               tc::tmem_wait_ld();
 #pragma unroll
-              for (int j = 0; j < 32; ++j) orr[j] = __float_as_uint(__uint_as_float(orr[j]) * corr);
-              tc::tmem_st32(tO + c * 32, orr);
+              for (int j = 0; j < 32; ++j)
+                mx = fmaxf(mx, uint32_t(32 * c + j - lo0) < span ? __uint_as_float(s32[j]) : -INFINITY);
             }
+            mx *= sl2;
           }
-          tc::tmem_wait_st();
+          // the running max after tile g - 1 (every tile but the stream's first
+          // waits, so each barrier is waited once per phase; a piece's first tile
+          // starts from -inf)
+          float m_in = -INFINITY;
+          if (g > 0) {
+            const uint32_t pq = (g - 1) & 1;
+            ok = __all_sync(0xffffffffu, wt(B_MREADY0 + 2 * quarter + int(pq), ((g - 1) >> 1) & 1));
+            if (!ok) break;
+            if (t > 0) m_in = mrow[pq * 128 + row];
+          }
+          const float m_up = fmaxf(m_in, mx);
+          const bool grow = m_up > m_in + 8.0f;  // also true when m_in is -inf and m_up finite
+          const float m = grow ? m_up : m_in;
+          mrow[(g & 1) * 128 + row] = m;
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(bar(B_MREADY0 + 2 * quarter + int(g & 1)));
+          if (m != m_own) {  // this warp's sum, against the new max
+            l = (m_own == -INFINITY) ? 0.f : l * tc::ex2(m_own - m);
+            m_own = m;
+          }
+          const float mu = (m == -INFINITY) ? 0.f : m;
+          // P buffer sb was last read by the PV of tile g - 2 (this warp waits
+          // for every such phase, in order)
+          if (g >= uint32_t(kSBufs)) {
+            ok = __all_sync(0xffffffffu, wt(B_PVDONE0 + sb, ((g / kSBufs) - 1) & 1));
+            if (!ok) break;
+            tc::fence_after_sync();
+          }
+          if (!idle) {
+            const uint32_t tP = tmem + lane_off + kColP + sb * 64;
+            if (full) {
+              l += p_pass<false>(sr, 0, kTile, mu, sl2x2, tP);
+            } else {
+#pragma unroll 1
+              for (int c = 0; c < 4; ++c) {
+                uint32_t s32[32], pk[16];
+                tc::tmem_ld32(tS + 32 * c, s32);
+                tc::tmem_wait_ld();
+#pragma unroll
+                for (int j = 0; j < 32; j += 2) {
+                  const int k = 32 * c + j - lo0;
+                  const float p0 = uint32_t(k) < span ? tc::ex2(fmaf(__uint_as_float(s32[j]), sl2, -mu)) : 0.f;
+                  const float p1 = uint32_t(k + 1) < span ? tc::ex2(fmaf(__uint_as_float(s32[j + 1]), sl2, -mu)) : 0.f;
+                  l += p0 + p1;
+                  pk[j / 2] = tc::pack_bf16x2(p0, p1);
+                }
+                tc::tmem_st16(tP + 16 * c, pk);
+              }
+              tc::fence_before_sync();
+              __syncwarp();
+              if (lane == 0) tc::mbar_arrive_remote(bar_even(B_SEMPTY0 + sb));
+            }
+            if (t > 0 && __any_sync(0xffffffffu, grow)) {
+              // O holds the sum up to tile g - 1 against m_in once the PV that
+              // read P of tile g - 1 is complete (the next PV waits for this P).
+              // That phase is the latest one of its barrier: PV(g - 3) is
+              // complete (PV(g - 2) is, see above) and PV(g + 1) waits for PV(g).
+              const float corr = (m_in == -INFINITY) ? 0.f : tc::ex2(m_in - m);
+              const uint32_t pb = (g - 1) % kSBufs;
+              ok = __all_sync(0xffffffffu, wt(B_PVDONE0 + pb, ((g - 1) / kSBufs) & 1));
+              if (!ok) break;
+              tc::fence_after_sync();
+#pragma unroll
+              for (int c = 0; c < D / 32; ++c) {
+                uint32_t orr[32];
+                tc::tmem_ld32(tO + c * 32, orr);
+                tc::tmem_wait_ld();
+#pragma unroll
+                for (int j = 0; j < 32; ++j) orr[j] = __float_as_uint(__uint_as_float(orr[j]) * corr);
+                tc::tmem_st32(tO + c * 32, orr);
+              }
+            }
+            tc::tmem_wait_st();
+          }
+          tc::fence_before_sync();
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive_remote(bar_even(B_PFULL0 + sb));
         }
-        tc::fence_before_sync();
+        if (!ok) break;
+        // ------------------------------------------------------ epilogue --
+        // What does not need O comes first: the last PV is still running.  The
+        // row's sum over both warps' tiles is taken against the final max (the
+        // larger of the two bases: the max never decreases along the stream).
+        float* xend = xjoin + (pieces & 1) * 512;
+        xend[half * 256 + row] = m_own;
+        xend[half * 256 + 128 + row] = l;
         __syncwarp();
-        if (lane == 0) tc::mbar_arrive_remote(bar_even(B_PFULL0 + sb));
+        if (lane == 0) tc::mbar_arrive(bar(B_JOIN0 + quarter));
+        ok = __all_sync(0xffffffffu, wt(B_JOIN0 + quarter, pieces & 1));
+        if (!ok) break;
+        ++pieces;
+        const float m_o = xend[(half ^ 1) * 256 + row], l_o = xend[(half ^ 1) * 256 + 128 + row];
+        const float m_fin = fmaxf(m_own, m_o);
+        float l_all = 0.f;
+        if (m_fin != -INFINITY) {
+          if (m_own != -INFINITY) l_all += l * tc::ex2(m_own - m_fin);
+          if (m_o != -INFINITY) l_all += l_o * tc::ex2(m_o - m_fin);
+        }
+        inv = l_all > 0.f ? 1.f / l_all : 0.f;
+        // A whole tile writes the final O (bf16, round to nearest even) and LSE;
+        // a piece of one its partial state (O in float32, LSE in log2 units).
+        slot = pc.slot;
+        const bool direct = slot < 0;
+        trow = int(rank) * half_rows + row;
+        const int packed = pc.tile.row0 + trow;
+        at = direct ? int64_t(pc.q.q0 + packed / a.G) * a.H + pc.h * a.G + packed % a.G
+                    : int64_t(slot) * a.R + trow;
+        if (row_ok && half == 0) {
+          const float l2 = l_all > 0.f ? m_fin + tc::lg2(l_all) : -INFINITY;
+          if (direct)
+            a.lse[at] = l2 * 0.69314718055994531f;
+          else
+            a.part_l[at] = l2;
+        }
       }
-      if (!ok) break;
-      // ------------------------------------------------------ epilogue --
-      // What does not need O comes first: the last PV is still running.  The
-      // row's sum over both warps' tiles is taken against the final max (the
-      // larger of the two bases: the max never decreases along the stream).
-      float* xend = xjoin + (pieces & 1) * 512;
-      xend[half * 256 + row] = m_own;
-      xend[half * 256 + 128 + row] = l;
-      __syncwarp();
-      if (lane == 0) tc::mbar_arrive(bar(B_JOIN0 + quarter));
-      ok = __all_sync(0xffffffffu, wt(B_JOIN0 + quarter, pieces & 1));
-      if (!ok) break;
-      ++pieces;
-      const float m_o = xend[(half ^ 1) * 256 + row], l_o = xend[(half ^ 1) * 256 + 128 + row];
-      const float m_fin = fmaxf(m_own, m_o);
-      float l_all = 0.f;
-      if (m_fin != -INFINITY) {
-        if (m_own != -INFINITY) l_all += l * tc::ex2(m_own - m_fin);
-        if (m_o != -INFINITY) l_all += l_o * tc::ex2(m_o - m_fin);
+      const bool more = w.next(a, pc);
+      if (!have) {
+        if (!more) break;
+        have = true;
+        continue;
       }
-      const float inv = l_all > 0.f ? 1.f / l_all : 0.f;
-      // A whole tile writes the final O (bf16, round to nearest even) and LSE;
-      // a piece of one its partial state (O in float32, LSE in log2 units).
-      const bool direct = pc.slot < 0;
-      const int trow = int(rank) * half_rows + row;
-      const int packed = pc.tile.row0 + trow;
-      const int64_t at = direct ? int64_t(pc.q.q0 + packed / a.G) * a.H + pc.h * a.G + packed % a.G
-                                : int64_t(pc.slot) * a.R + trow;
-      if (row_ok && half == 0) {
-        const float l2 = l_all > 0.f ? m_fin + tc::lg2(l_all) : -INFINITY;
-        if (direct)
-          a.lse[at] = l2 * 0.69314718055994531f;
-        else
-          a.part_l[at] = l2;
-      }
+      const bool direct = slot < 0;
       const int c0 = D / 2 * half;  // each warp writes half of the columns
       if (n > 0) {
         ok = __all_sync(0xffffffffu, wt(B_ODONE, items & 1));
@@ -644,7 +662,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_pair_kernel(const __grid_co
         } else if (row_ok) {
           // partial O: [slot][4 columns][row] float4, the rows of a warp side by side
           float4* dst = reinterpret_cast<float4*>(a.part_o) +
-                        (int64_t(pc.slot) * (D / 4) + (c0 + cc * 32) / 4) * a.R + trow;
+                        (int64_t(slot) * (D / 4) + (c0 + cc * 32) / 4) * a.R + trow;
 #pragma unroll
           for (int j = 0; j < 8; ++j)
             dst[int64_t(j) * a.R] =
@@ -652,6 +670,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_pair_kernel(const __grid_co
                             __uint_as_float(orr[4 * j + 2]) * inv, __uint_as_float(orr[4 * j + 3]) * inv);
         }
       }
+      if (!more) break;
     }
   }
 
