@@ -515,7 +515,7 @@ size_t cp_paged_attn_workspace_bytes(const cp_paged_desc* desc);
  * log, as cp_tile_attn_fwd gives them (0 and -inf where a row sees no key), so
  * that they merge with other partial states by cp_merge_partials.
  * q: [rows][heads_q][head_dim], q_stride elements between rows.  Rows from
- * cu_new[n_reqs] on are left as they were.
+ * cu_new[n_reqs] on are left as they were.  o and lse must not overlap the inputs.
  * Lengths are clamped to the table and to the rows of q.  Only pages with a visible key are
  * looked at: entries behind the last key, or in front of every row's window, may
  * hold anything, and so may the rest of the last page.  A page number outside

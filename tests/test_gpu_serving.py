@@ -322,7 +322,7 @@ def check_attention(kv, q, table, cu, lens, o, lse, causal=True, window=0, scale
         tol = tol + U16 * vmax + U16 * np.abs(want_o)
     err = np.abs(got_o - want_o)
     assert (err <= tol).all(), float((err - tol).max())
-    assert np.abs(got_l - want_l)[~none].max(initial=0.0) <= e_w + 4 * U32 * np.abs(want_l[~none]).max(initial=0.0)
+    assert np.abs(got_l[~none] - want_l[~none]).max(initial=0.0) <= e_w + 4 * U32 * np.abs(want_l[~none]).max(initial=0.0)
     if dtype == torch.bfloat16:
         assert np.linalg.norm(got_o - want_o) <= 2 * U16 * np.linalg.norm(want_o)
 
@@ -594,3 +594,96 @@ def test_multi_axis_positions_through_the_ring_and_back():
     rq, rk = P.rope_axes(rq[0], pos, sections, inverse=True), P.rope_axes(rk[0], pos, sections, inverse=True)
     for got, want in ((o, ro), (dq, rq), (dk, rk), (dv, rv)):
         assert np.abs(f64(got) - want).max() <= 1e-5 * max(1.0, np.abs(want).max())
+
+
+def test_offsets_past_32_bits():
+    # 40000 pages of 64 tokens, 8 heads, 128: the last pages start past 2^31 elements
+    pages, page, hkv, d, hq = 40000, 64, 8, 128, 16
+    kv = api.PagedKV(*(torch.empty((pages, page, hkv, d), dtype=torch.bfloat16, device=DEV) for _ in range(2)))
+    assert (pages - 3) * kv.k_cache.stride(0) > 2 ** 31
+    lens = [130, 70]
+    table = np.array([[39999, 7, 39990], [39995, 39998, -1]])
+    g = torch.Generator().manual_seed(50)
+    rows = sum(lens)
+    k, v = (torch.randn((rows, hkv, d), generator=g).to(torch.bfloat16).to(DEV) for _ in range(2))
+    slots = np.concatenate([table[r][np.arange(n) // page] * page + np.arange(n) % page for r, n in enumerate(lens)])
+    api.kv_append(kv, dev(slots), k, v)
+    at = torch.from_numpy(slots).to(DEV)
+    assert torch.equal(kv.k_cache.view(-1, hkv, d)[at], k) and torch.equal(kv.v_cache.view(-1, hkv, d)[at], v)
+    few_k, few_v = (np.zeros((6, page, hkv, d)) for _ in range(2))  # the five pages alone, for the plain way
+    small = np.array([[0, 1, 2], [3, 4, 5]])
+    for big, little in zip(table.ravel()[:5], small.ravel()):
+        few_k[little], few_v[little] = f64(kv.k_cache[int(big)]), f64(kv.v_cache[int(big)])
+    for new in ([1, 1], [40, 30]):
+        cu = np.concatenate([[0], np.cumsum(new)])
+        q = torch.randn((sum(new), hq, d), generator=g).to(torch.bfloat16).to(DEV)
+        p = api.PagedProblem(kv, hq, max_new=max(new))
+        o, lse = api.paged_attn_fwd(p, q, dev(table), dev(cu), dev(lens))
+        wo, wl = P.attention(f64(q), few_k, few_v, small, cu, lens)
+        assert np.linalg.norm(f64(o) - wo) <= 2 * U16 * np.linalg.norm(wo)
+        assert np.abs(f64(lse) - wl).max() <= 1e-4
+
+
+def test_a_group_wider_than_a_pairs_tile():
+    new, lens, hq = [3, 1, 9], [40, 130, 9], 130
+    for dtype, d in ((torch.bfloat16, 128), (torch.bfloat16, 64), (torch.float32, 64)):
+        kv, q, table, cu = paged_inputs(new, lens, hq, 1, d, 16, dtype, seed=51)
+        p = api.PagedProblem(kv, hq, max_new=9)
+        o, lse = api.paged_attn_fwd(p, q, dev(table), dev(cu), dev(lens))
+        check_attention(kv, q, table, cu, lens, o, lse)
+
+
+def test_a_serving_step_captured_and_replayed():
+    """extend, append with a rotation and attention in one graph; between
+    replays the host only copies the lengths that the step left and new rows."""
+    n, page, hq, hkv, d, dtype, width, pages, rows = 3, 16, 4, 2, 64, torch.bfloat16, 8, 24, 5
+    kv = make_cache(pages, page, hkv, d, dtype, "token")
+    rope = api.Rope([32], adjacent=True)
+    table, free = torch.full((n, width), -1, **I32), torch.arange(pages, **I32)
+    lens, add, n_free = torch.zeros(n, **I32), torch.zeros(n, **I32), torch.full((1,), pages, **I32)
+    x = torch.zeros((rows, hq + 2 * hkv, d), dtype=dtype, device=DEV)
+    p = api.PagedProblem(kv, hq, max_new=3)
+    ws = api.paged_workspace(p)
+    o, lse = torch.zeros((rows, hq, d), dtype=dtype, device=DEV), torch.zeros((rows, hq), device=DEV)
+    q_out = torch.zeros((rows, hq, d), dtype=dtype, device=DEV)
+
+    def step():
+        lens2, cu, slots, pos, n_free2 = api.kv_extend(page, table, lens, add, free, n_free, rows)
+        api.kv_append(kv, slots, x[:, hq:hq + hkv], x[:, hq + hkv:], rope=rope, pos=pos, q=x[:, :hq], q_out=q_out)
+        api.paged_attn_fwd(p, q_out, table, cu, lens2, ws=ws, out=o, lse=lse)
+        lens.copy_(lens2)
+        n_free.copy_(n_free2)
+        return cu
+
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        step()                                                  # nothing to add
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=s):
+            cu = step()
+    torch.cuda.current_stream().wait_stream(s)
+    g = torch.Generator().manual_seed(52)
+    keys, values = [[] for _ in range(n)], [[] for _ in range(n)]
+    for adds in ([2, 0, 3], [1, 3, 1], [1, 1, 1], [0, 2, 0]) * 3:
+        add.copy_(dev(adds))
+        x.copy_(torch.randn(x.shape, generator=g).to(dtype))
+        before = host(lens)
+        graph.replay()
+        c = host(cu)
+        assert c.tolist() == [0] + np.cumsum(adds).tolist() and (host(lens) == before + adds).all()
+        pos = np.zeros((1, rows), dtype=np.int64)
+        for r in range(n):
+            pos[0, c[r]:c[r + 1]] = before[r] + np.arange(adds[r])
+        rnd = lambda a: f64(torch.from_numpy(a).to(dtype))  # noqa: E731
+        qr = rnd(P.rope_axes(f64(x[:, :hq]), pos, [32], adjacent=True))
+        kr, vr = rnd(P.rope_axes(f64(x[:, hq:hq + hkv]), pos, [32], adjacent=True)), f64(x[:, hq + hkv:])
+        for r in range(n):
+            keys[r] += list(kr[c[r]:c[r + 1]])
+            values[r] += list(vr[c[r]:c[r + 1]])
+            if adds[r] == 0:
+                continue
+            kk, vv = (np.stack(a)[None] for a in (keys[r], values[r]))
+            wo, wl = P.attention(qr[c[r]:c[r + 1]], kk, vv, np.zeros((1, 1), dtype=np.int64), [0, adds[r]], [kk.shape[1]])
+            assert np.linalg.norm(f64(o)[c[r]:c[r + 1]] - wo) <= 4 * U16 * np.linalg.norm(wo)
+            assert np.abs(f64(lse)[c[r]:c[r + 1]] - wl).max() <= 2 * U16 * 8

@@ -220,7 +220,7 @@ def test_shares_are_even():
     lens = [131072, 5, 700, 40000]
     pieces, grid = api.paged_schedule(p, [0, 1, 2, 3, 4], lens, 4, 8192)
     load = np.bincount(pieces[:, 0], weights=(pieces[:, 6] - pieces[:, 5]), minlength=grid)
-    # units of 64 keys and one for every tile's ends, in shares that differ by at most one unit
-    units = 8 * sum(-(-n // 64) + 1 for n in lens)
+    # units of 64 keys and two for every tile's ends, in shares that differ by at most one unit
+    units = 8 * sum(-(-n // 64) + 2 for n in lens)
     assert load.max() <= 64 * -(-units // grid)
     assert np.median(load) >= 0.97 * load.max()

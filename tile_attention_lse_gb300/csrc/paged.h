@@ -190,10 +190,12 @@ struct PagedWalk {
   }
 };
 
-// Rows of a tile and keys of a unit of each kernel; kv-head groups wider than
-// kPairRows rows never reach the pair kernel.
-constexpr int kSliceUnit = 64, kSliceExtra = 1;
-constexpr int kPairUnit = 128, kPairExtra = 2, kPairRows = 128;
+// Keys of a unit of each kernel, and what a tile's ends cost in them (16
+// prompts of about 400 tokens: pair extra 2 161 us, 4 136, 6 129; 200 single
+// tokens over about 200 keys: slice extra 1 62 us, 2 55, 3 53, but one token over 777 keys
+// 12.2, 12.5 and 14.2).  kv-head groups wider than kPairRows never reach the pair kernel.
+constexpr int kSliceUnit = 64, kSliceExtra = 2;
+constexpr int kPairUnit = 128, kPairExtra = 6, kPairRows = 128;
 
 enum PagedKernel { kPagedSlice4, kPagedSlice16, kPagedSlice32, kPagedPair };
 inline int paged_rows(PagedKernel k, int G) {
