@@ -609,7 +609,7 @@ __global__ void __launch_bounds__(SliceLayout<S, D, R>::kThreads, 1)
   // order (a phase's parity tells it only from the next one)
   static_assert(NS % (W / S::kPerStage) == 0, "a worker's stages keep their slots");
   extern __shared__ __align__(1024) uint8_t smem[];
-  __shared__ int64_t s_scan[32];
+  __shared__ int64_t s_scan[64];
   __shared__ PagedStart s_start;
   __shared__ PieceInfo s_piece[kPieces];
   // piece published, its Q landed, its states joined (per entry); stage landed, stage read; all workers' states left
@@ -929,7 +929,7 @@ struct MergeParams {
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const __grid_constant__ MergeParams p) {
-  __shared__ int64_t s_scan[32];
+  __shared__ int64_t s_scan[64];
   __shared__ PagedStart s_start;
   const int n_pair = p.pair.grid * p.pair_parts;
   if constexpr (sizeof(T) == 2) {

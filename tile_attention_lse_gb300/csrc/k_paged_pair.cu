@@ -59,7 +59,7 @@ constexpr int kOffV = kOffK + kKStages * kKBytes;
 constexpr int kOffBar = kOffV + kVStages * kVBytes;
 constexpr int kOffX = kOffBar + 512;  // running max [2 tile parities][128], row-sum base and sum [2 piece parities][2 warps][2][128]
 constexpr int kOffScan = kOffX + (2 * 128 + 2 * 2 * 2 * 128) * 4;
-constexpr int kSmemBytes = kOffScan + 32 * 8 + int(sizeof(PagedStart));
+constexpr int kSmemBytes = kOffScan + 64 * 8 + int(sizeof(PagedStart));
 static_assert(kSmemBytes <= 232448, "shared memory budget of one CTA");
 
 // Barrier slots, the same layout in both CTAs.  "even": only the even CTA's
@@ -154,9 +154,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_pair_kernel(const __grid_co
   // this pair's share of the units
   const int pair = int(tc::cluster_id_x());
   int64_t* s_scan = reinterpret_cast<int64_t*>(smem + kOffScan);
-  PagedStart* s_start = reinterpret_cast<PagedStart*>(smem + kOffScan + 32 * 8);
+  PagedStart* s_start = reinterpret_cast<PagedStart*>(smem + kOffScan + 64 * 8);
   const PagedShare share = paged_locate<kPairUnit, kPairExtra, kThreads>(a, s_scan, s_start, pair);
   const int64_t units = share.first(pair + 1) - share.first(pair);
+  if (pair >= share.n) return;  // these SMs are the slice launch's
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < B_COUNT; ++i) {

@@ -39,10 +39,14 @@ struct PagedArgs {
   int32_t H, Hkv, G, d;
   int32_t R;  // packed rows of a tile
   int32_t row_min, row_max;  // requests of fewer or more packed rows are another launch's
+  // that launch, where the call has one (other_R 0: none)
+  int32_t other_R, other_min, other_max;
+  int32_t pairs, blocks;  // what the pair launch and the slice launch have at most
+  int32_t pair_cost, slice_cost;  // SM time of a unit of either (ns)
   int32_t causal, window;
   float scale_log2;  // softmax scale * log2(e)
   cp_dtype dtype;
-  int32_t grid;  // blocks (or pairs of blocks) that share the units
+  int32_t grid;  // blocks (or pairs of blocks) of the launch
   int* err;
 };
 
@@ -110,12 +114,42 @@ CPATTN_HD int64_t paged_div(int64_t x, int64_t y) {
   return ((x | y) >> 31) == 0 ? int64_t(uint32_t(x) / uint32_t(y)) : x / y;
 }
 
-// The shares of the blocks.
+// The shares of n blocks; the blocks behind them have none.
 struct PagedShare {
   int64_t total, each, more;  // block c: `each` units, one more for c < more
-  CPATTN_HD PagedShare(int64_t t, int grid) : total(t), each(paged_div(t, grid)), more(t - each * grid) {}
-  CPATTN_HD int64_t first(int c) const { return each * c + (c < more ? c : more); }
+  int32_t n;
+  CPATTN_HD PagedShare(int64_t t, int blocks) : total(t), n(blocks > 0 ? blocks : 1) {
+    each = paged_div(t, n);
+    more = t - each * n;
+  }
+  CPATTN_HD int64_t first(int c) const { return c >= n ? total : each * c + (c < more ? c : more); }
 };
+
+// Pairs of SMs that the many-row requests of a call get where it has few-row
+// ones too; the other SMs run the slice launch at the same time.
+CPATTN_HD int paged_pairs(const PagedArgs& a, int64_t pair_units, int64_t slice_units) {
+  if (slice_units == 0) return a.pairs;
+  if (pair_units == 0) return 0;
+  const int64_t x = pair_units * a.pair_cost, sum = x + slice_units * a.slice_cost;
+  // rounded down: a pair too few costs the many-row requests 1 in 76, one too
+  // many could leave the others half of what they need
+  const int k = int(float(x) / float(sum) * a.pairs);
+  return k < 1 ? 1 : (k > a.pairs - 2 ? a.pairs - 2 : k);
+}
+// Blocks of this launch that share its units.
+CPATTN_HD int paged_blocks(const PagedArgs& a, bool pair, int64_t mine, int64_t others) {
+  if (a.other_R == 0) return a.grid;
+  const int k = paged_pairs(a, pair ? mine : others, pair ? others : mine);
+  return pair ? k : a.blocks - 2 * k;
+}
+// The other launch's view of the requests.
+CPATTN_HD PagedArgs paged_other(const PagedArgs& a) {
+  PagedArgs o = a;
+  o.R = a.other_R;
+  o.row_min = a.other_min;
+  o.row_max = a.other_max;
+  return o;
+}
 
 // Where a unit lies: its tile and the units of the tile before it.
 struct PagedStart {
@@ -196,6 +230,13 @@ struct PagedWalk {
 // 12.2, 12.5 and 14.2).  kv-head groups wider than kPairRows never reach the pair kernel.
 constexpr int kSliceUnit = 64, kSliceExtra = 2;
 constexpr int kPairUnit = 128, kPairExtra = 6, kPairRows = 128;
+
+// Units, extra and so on of the launch that is not this one.
+template <int U>
+struct PagedOther {
+  static constexpr int kUnit = U == kPairUnit ? kSliceUnit : kPairUnit;
+  static constexpr int kExtra = U == kPairUnit ? kSliceExtra : kPairExtra;
+};
 
 enum PagedKernel { kPagedSlice4, kPagedSlice16, kPagedSlice32, kPagedPair };
 inline int paged_rows(PagedKernel k, int G) {

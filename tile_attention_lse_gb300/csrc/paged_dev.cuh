@@ -1,6 +1,8 @@
 // Device side of the paged attention's work division: where a unit lies.
 #pragma once
 
+#include <type_traits>
+
 #include "paged.h"
 
 namespace cpattn {
@@ -9,7 +11,7 @@ namespace cpattn {
 constexpr int kOwnTiles = 16;
 
 // Finds where the first unit of block c lies and returns the shares; the whole
-// block calls it, `sh` holds 32 int64 and `out` a PagedStart in shared memory
+// block calls it, `sh` holds 64 int64 and `out` a PagedStart in shared memory
 // (not written where c has no first unit).  The threads share the requests in
 // runs; the loops are warp-uniform so that lanes can help one another.
 template <int U, int E, int kThreads>
@@ -18,32 +20,47 @@ __device__ __forceinline__ PagedShare paged_locate(const PagedArgs& a, int64_t* 
   const int run = (a.n_reqs + kThreads - 1) / kThreads;
   const int r0 = tid * run;
   // units of one kv-head of this lane's i-th request
-  auto units = [&](int i, PagedReq& q, int& nt) -> int64_t {
+  auto units = [&](const PagedArgs& a, auto unit, auto extra, int i, PagedReq& q, int& nt) -> int64_t {
+    constexpr int kU = decltype(unit)::value, kE = decltype(extra)::value;
     q = PagedReq{0, 0, 0};
     if (r0 + i < a.n_reqs) q = paged_req(a, r0 + i);
     nt = paged_tiles(a, q);
     int64_t s = 0;
     if (nt <= kOwnTiles)
-      for (int t = 0; t < nt; ++t) s += paged_tile<U>(a, q, t).n + E;
+      for (int t = 0; t < nt; ++t) s += paged_tile<kU>(a, q, t).n + kE;
     for (uint32_t big = __ballot_sync(0xffffffffu, nt > kOwnTiles); big; big &= big - 1) {
       const int from = __ffs(big) - 1;
       const PagedReq x{__shfl_sync(0xffffffffu, q.q0, from), __shfl_sync(0xffffffffu, q.nq, from),
                        __shfl_sync(0xffffffffu, q.kv, from)};
       const int n = __shfl_sync(0xffffffffu, nt, from);
       int64_t part = 0;
-      for (int t = lane; t < n; t += 32) part += paged_tile<U>(a, x, t).n + E;
+      for (int t = lane; t < n; t += 32) part += paged_tile<kU>(a, x, t).n + kE;
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) part += __shfl_xor_sync(0xffffffffu, part, o);
       if (lane == from) s = part;
     }
     return s;
   };
+  using Unit = std::integral_constant<int, U>;
+  using Extra = std::integral_constant<int, E>;
   PagedReq q{};
   int nt = 0;
-  int64_t mine = 0, last = 0;
+  int64_t mine = 0, last = 0, other = 0;
   for (int i = 0; i < run; ++i) {
-    last = units(i, q, nt);
+    last = units(a, Unit{}, Extra{}, i, q, nt);
     mine += last * a.Hkv;
+  }
+  if (a.other_R > 0) {  // the other launch's units: how the SMs are divided
+    const PagedArgs b = paged_other(a);
+    for (int i = 0; i < run; ++i) {
+      PagedReq x;
+      int n;
+      other += units(b, std::integral_constant<int, PagedOther<U>::kUnit>{},
+                     std::integral_constant<int, PagedOther<U>::kExtra>{}, i, x, n) * a.Hkv;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) other += __shfl_xor_sync(0xffffffffu, other, o);
+    if (lane == 0) sh[32 + warp] = other;
   }
   int64_t x = mine;
 #pragma unroll
@@ -59,7 +76,12 @@ __device__ __forceinline__ PagedShare paged_locate(const PagedArgs& a, int64_t* 
     if (w < warp) before += sh[w];
     total += sh[w];
   }
-  const PagedShare share(total, a.grid);
+  int64_t others = 0;
+  if (a.other_R > 0) {
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) others += sh[32 + w];
+  }
+  const PagedShare share(total, paged_blocks(a, U == kPairUnit, total, others));
   const int64_t u = share.first(c);
   const uint32_t who = __ballot_sync(0xffffffffu, u >= before && u < before + mine);
   if (who) {  // this warp holds it: its lane's requests, then the tiles of the one
@@ -68,7 +90,7 @@ __device__ __forceinline__ PagedShare paged_locate(const PagedArgs& a, int64_t* 
     bool found = false;
     int r = 0;
     for (int i = 0; i < run; ++i) {
-      if (run > 1) last = units(i, q, nt);
+      if (run > 1) last = units(a, Unit{}, Extra{}, i, q, nt);
       const bool here = lane == from && !found && u < base + last * a.Hkv;
       if (__any_sync(0xffffffffu, here)) {
         r = i;

@@ -99,9 +99,10 @@ cp_status make_turns(const cp_rope* r, int32_t head_dim, RopeTurns* t) {
 // (32 requests of 8 tokens over 4000 keys, 4 heads a group: 101 us, 131 on
 // the pair kernel); those of more on the pair kernel (bound by the products and the
 // softmax).  Where both may come, both are launched, each for its own
-// requests (20 single tokens and 4 chunks of up to 509 over 6000
-// cached tokens: 251 us with all of them on the pair kernel, 231 on both).  A
-// single request of unknown length runs on the pair kernel whatever it brings.
+// requests and on its own share of the SMs, at the same time (20 single tokens and 4
+// chunks of up to 509 over 6000 cached tokens: 251 us with all of them on the
+// pair kernel, 177 one after the other, 164 together).  A single request of
+// unknown length runs on the pair kernel whatever it brings.
 struct PagedPlan {
   PagedKernel slice = kPagedSlice16;
   bool use_slice = true, use_pair = false;
@@ -134,9 +135,14 @@ cp_status check_paged(const cp_paged_desc* d) {
 // Walks every block's share on the host.
 template <int U, int E, typename F>
 void walk_all(const PagedArgs& a, F f) {
-  int64_t total = 0;
+  int64_t total = 0, others = 0;
   for (int r = 0; r < a.n_reqs; ++r) total += paged_req_units<U, E>(a, paged_req(a, r)) * a.Hkv;
-  const PagedShare share(total, a.grid);
+  if (a.other_R > 0) {
+    const PagedArgs o = paged_other(a);
+    for (int r = 0; r < a.n_reqs; ++r)
+      others += paged_req_units<PagedOther<U>::kUnit, PagedOther<U>::kExtra>(o, paged_req(o, r)) * a.Hkv;
+  }
+  const PagedShare share(total, paged_blocks(a, U == kPairUnit, total, others));
   PagedStart at{0, 0, 0, 0};
   for (int c = 0; c < a.grid; ++c) {
     const int64_t u0 = share.first(c), u1 = share.first(c + 1);
@@ -192,6 +198,7 @@ PagedArgs paged_args(const cp_paged_desc& d, int32_t n_reqs, int64_t rows, int32
   a.dtype = d.kv.dtype;
   a.causal = d.causal != 0;
   a.window = d.window;
+  a.page_shift = log2_of(d.kv.page_size);
   a.row_max = INT32_MAX;
   return a;
 }
@@ -202,8 +209,20 @@ void split_args(const PagedPlan& p, const PagedArgs& a, PagedArgs* pair, PagedAr
   pair->grid = pair_blocks(p);
   slice->grid = p.use_slice ? paged_slice_grid() : 0;
   if (p.use_pair && p.use_slice) {
-    pair->row_min = 17;
-    slice->row_max = 16;
+    pair->row_min = slice->other_min = 17;
+    slice->row_max = pair->other_max = 16;
+    slice->other_max = INT32_MAX;
+    pair->other_R = slice->R;
+    slice->other_R = pair->R;
+    pair->pairs = slice->pairs = pair->grid;
+    pair->blocks = slice->blocks = slice->grid;
+    // A slice unit's time on one SM by its boxes (32 KB at 85 GB/s from pages
+    // of 64 on, 53 at 16), a pair unit's on two: measured on batches of both.
+    const bool wide = a.d == 128;
+    const int page = 1 << a.page_shift;
+    pair->pair_cost = slice->pair_cost = page == 8 ? 2400 : 1800;
+    pair->slice_cost = slice->slice_cost =
+        page >= 64 ? (wide ? 480 : 350) : page == 32 ? (wide ? 500 : 360) : page == 16 ? (wide ? 640 : 450) : (wide ? 950 : 600);
   }
 }
 
@@ -411,7 +430,6 @@ cp_status cp_paged_attn_fwd(const cp_paged_desc* desc, int32_t n_reqs, int64_t r
   a.o = o;
   a.lse = lse;
   a.n_pages = c.n_pages;
-  a.page_shift = log2_of(c.page_size);
   const float scale = desc->softmax_scale > 0.f ? desc->softmax_scale : 1.f / std::sqrt(float(c.head_dim));
   a.scale_log2 = scale * 1.4426950408889634f;
   a.err = device_error_ptr();
@@ -427,6 +445,7 @@ cp_status cp_paged_attn_fwd(const cp_paged_desc* desc, int32_t n_reqs, int64_t r
   if (plan.use_pair) {
     r = paged_pair_grid(c.head_dim, &pair.grid);
     if (r != CP_OK) return r;
+    pair.pairs = slice.pairs = pair.grid;
     ProfScope ps(CP_K_PAGED, s);
     r = launch_paged_pair(pair, s);
     if (r != CP_OK) return r;
