@@ -434,11 +434,21 @@ class PagedProblem:
         self._ref = ctypes.byref(self._desc)
 
 
-# A call's checks and marshalling cost more host time than its launch (a few
-# microseconds, which a decode step of small calls feels), so they compare
-# singletons and device indices and look the raw stream up directly.
+# A call's checks, marshalling and output tensors cost more host time than its
+# launch (a few microseconds, which a step of small calls feels).  So the
+# checks compare singletons and device indices, the raw stream is looked up
+# directly, and new tensors are made below PyTorch's dispatcher where it offers
+# that (a table call's five outputs: 12 us through it, 4 us below).
 _I32, _F32 = torch.int32, torch.float32
 _raw_stream = torch._C._cuda_getCurrentRawStream
+try:
+    from torch._C._dynamo.guards import _empty_strided_cuda, _reinterpret_tensor
+except ImportError:  # the same by the public functions
+    def _empty_strided_cuda(size, stride, dtype):
+        return torch.empty_strided(size, stride, dtype=dtype, device="cuda")
+
+    def _reinterpret_tensor(x, size, stride, offset):
+        return x.as_strided(size, stride, offset)
 
 
 def _rows(x: torch.Tensor, what: str, heads: int, d: int, dtype, device: int):
@@ -458,12 +468,13 @@ def _ints(x: torch.Tensor, what: str, shape, device: int):
     return x.data_ptr()
 
 
-def _new(out, what, shape, dtype, device):
-    """The caller's output tensor (contiguous, of that shape and type), or a new one."""
+def _new(out, what, shape, dtype, device: int):
+    """The caller's output tensor (contiguous, of that shape and type), or a
+    new one on the current device."""
     if out is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    if out.shape != shape or out.dtype is not dtype or out.device != device or not out.is_contiguous():
-        raise ValueError(f"{what} is a contiguous {list(shape)} {dtype} tensor on {device}")
+        return _empty_strided_cuda(shape, (shape[1] * shape[2], shape[2], 1) if len(shape) == 3 else (shape[1], 1), dtype)
+    if out.shape != shape or out.dtype is not dtype or out.get_device() != device or not out.is_contiguous():
+        raise ValueError(f"{what} is a contiguous {list(shape)} {dtype} tensor on cuda:{device}")
     return out
 
 
@@ -493,13 +504,14 @@ def kv_extend(page_size: int, block_table, lens, add, free_pages, n_free, max_ro
     block_table [n_reqs, max_blocks] changes in place; returns (lens, cu_new,
     slots, pos, n_free) as new tensors."""
     n, width, pool, args, s = _tables(block_table, free_pages, n_free, lens=lens, add=add)
-    out = torch.empty(2 * n + 2 + 2 * max_rows, dtype=_I32, device=block_table.device)
+    out = _empty_strided_cuda((2 * n + 2 + 2 * max_rows,), (1,), _I32)
     at = out.data_ptr()
     rows_at = at + 4 * (2 * n + 2)
     _check(lib().cp_kv_extend(n, width, page_size, max_rows, pool, *args, at, at + 4 * n, rows_at,
                               rows_at + 4 * max_rows, rows_at - 4, s), "cp_kv_extend")
-    lens_out, cu, n_free_out, slots, pos = torch.unsafe_split_with_sizes(out, (n, n + 1, 1, max_rows, max_rows))
-    return lens_out, cu, slots, pos, n_free_out
+    one, view = (1,), _reinterpret_tensor
+    return (view(out, (n,), one, 0), view(out, (n + 1,), one, n), view(out, (max_rows,), one, 2 * n + 2),
+            view(out, (max_rows,), one, 2 * n + 2 + max_rows), view(out, one, one, 2 * n + 1))
 
 
 def kv_release(page_size: int, block_table, lens, done, free_pages, n_free):
@@ -526,13 +538,13 @@ def rope_axes(rope: Rope, pos, q, k=None, inverse: bool = False, q_out=None, k_o
     rows, hq, d = q.shape
     qs, hk, ks, kp, ko = _rows(q, "q", hq, d, dt, dev), 0, 0, None, None
     p, s = _positions(rope, pos, rows, dev), _stream_of(dev)
-    q_out = _new(q_out, "q_out", q.shape, dt, q.device)
+    q_out = _new(q_out, "q_out", (rows, hq, d), dt, dev)
     if k is not None:
         hk = k.shape[1]
         ks = _rows(k, "k", hk, d, dt, dev)
         if k.shape[0] != rows:
             raise ValueError("q and k have the same rows")
-        k_out = _new(k_out, "k_out", k.shape, dt, k.device)
+        k_out = _new(k_out, "k_out", (rows, hk, d), dt, dev)
         kp, ko = k.data_ptr(), k_out.data_ptr()
     _check(lib().cp_rope_axes(rope._ref, p, rows, d, _dtype_code(dt), hq, q.data_ptr(), qs, q_out.data_ptr(), hk, kp, ks,
                               ko, int(inverse), s), "cp_rope_axes")
@@ -559,7 +571,7 @@ def kv_append(kv: PagedKV, slots, k, v, rope: Rope | None = None, pos=None, q=No
             raise ValueError("q is [rows, heads_q, head_dim]")
         hq = q.shape[1]
         qs = _rows(q, "q", hq, d, dt, dev)
-        q_out = _new(q_out, "q_out", q.shape, dt, q.device)
+        q_out = _new(q_out, "q_out", (rows, hq, d), dt, dev)
         qp, qo = q.data_ptr(), q_out.data_ptr()
     _check(lib().cp_kv_append(kv._ref, at, rows, k.data_ptr(), ks, v.data_ptr(), vs, r, p, hq, qp, qs, qo, s),
            "cp_kv_append")
@@ -613,8 +625,8 @@ def paged_attn_fwd(p: PagedProblem, q, block_table, cu_new, kv_lens, ws: torch.T
     elif ws.get_device() != dev or not ws.is_contiguous():
         raise ValueError(f"ws is a contiguous tensor on cuda:{dev}")
     rows = q.shape[0]
-    out = _new(out, "out", q.shape, kv.dtype, kv.device)
-    lse = _new(lse, "lse", (rows, heads), _F32, kv.device)
+    out = _new(out, "out", (rows, heads, d), kv.dtype, dev)
+    lse = _new(lse, "lse", (rows, heads), _F32, dev)
     _check(lib().cp_paged_attn_fwd(p._ref, n, rows, width, q.data_ptr(), qs, table, cu, lens, out.data_ptr(),
                                    lse.data_ptr(), ws.data_ptr(), ws.nbytes, s), "cp_paged_attn_fwd")
     return out, lse
