@@ -101,7 +101,7 @@ cp_status make_turns(const cp_rope* r, int32_t head_dim, RopeTurns* t) {
 // softmax).  Where both may come, both are launched, each for its own
 // requests and on its own share of the SMs, at the same time (20 single tokens and 4
 // chunks of up to 509 over 6000 cached tokens: 251 us with all of them on the
-// pair kernel, 177 one after the other, 164 together).  A single request of
+// pair kernel, 177 one after the other, 164 together, 161 by now).  A single request of
 // unknown length runs on the pair kernel whatever it brings.
 struct PagedPlan {
   PagedKernel slice = kPagedSlice16;
