@@ -483,7 +483,8 @@ cp_status cp_rope_axes(const cp_rope* rope, const int32_t* pos, int64_t rows, in
  * into q_out [rows][heads_q][head_dim] in the same launch.  A row
  * whose slot is negative or behind the last page is left out: nothing of it
  * is written, q_out's row neither.  Slots that are named twice hold one of
- * the rows, or 16-byte pieces of both.  Errors as above. */
+ * the rows, or 16-byte pieces of both.  The inputs must not lie in the cache.
+ * Errors as above. */
 cp_status cp_kv_append(const cp_kv_cache* cache, const int32_t* slots, int64_t rows, const void* k, int64_t k_stride,
                        const void* v, int64_t v_stride, const cp_rope* rope, const int32_t* pos, int32_t heads_q,
                        const void* q, int64_t q_stride, void* q_out, void* stream);

@@ -15,6 +15,9 @@ relative to the value):
   the two roundings stay below u16 |O| each: the 2-norm is held to 2 u16.
 """
 
+import os
+import subprocess
+import sys
 import threading
 
 import numpy as np
@@ -687,3 +690,57 @@ def test_a_serving_step_captured_and_replayed():
             wo, wl = P.attention(qr[c[r]:c[r + 1]], kk, vv, np.zeros((1, 1), dtype=np.int64), [0, adds[r]], [kk.shape[1]])
             assert np.linalg.norm(f64(o)[c[r]:c[r + 1]] - wo) <= 4 * U16 * np.linalg.norm(wo)
             assert np.abs(f64(lse)[c[r]:c[r + 1]] - wl).max() <= 2 * U16 * 8
+
+
+FIRST_CALL = """
+import torch
+from tile_attention_lse_gb300 import api
+g = torch.Generator().manual_seed(60)
+i32 = dict(dtype=torch.int32, device="cuda:0")
+kv = api.PagedKV(*(torch.randn((9, 16, 2, 128), generator=g).to("cuda:0", torch.bfloat16) for _ in range(2)))
+x = torch.randn((40, 8, 128), generator=g).to("cuda:0", torch.bfloat16)
+lens, add = torch.tensor([20, 0], **i32), torch.tensor([39, 1], **i32)
+table, free, n_free = torch.tensor([[3, 4, -1, -1], [-1] * 4], **i32), torch.arange(5, 9, **i32), torch.tensor([4], **i32)
+rope = api.Rope([64])
+p = api.PagedProblem(kv, 4, max_new=MAX_NEW)
+ws = api.paged_workspace(p)
+
+def step():
+    t = table.clone()
+    lens2, cu, slots, pos, _ = api.kv_extend(16, t, lens, add, free, n_free, 40)
+    q = api.kv_append(kv, slots, x[:, 4:6], x[:, 6:], rope=rope, pos=pos, q=x[:, :4])
+    return api.paged_attn_fwd(p, q, t, cu, lens2, ws=ws)
+
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    o, lse = step()
+graph.replay()
+o2, lse2 = step()
+assert torch.equal(o, o2) and torch.equal(lse, lse2) and bool(torch.isfinite(lse).all()) and api.device_error() == 0
+"""
+
+
+@pytest.mark.parametrize("max_new", [1, 39])
+def test_the_first_calls_of_a_process_are_captured(max_new):
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    res = subprocess.run([sys.executable, "-c", FIRST_CALL.replace("MAX_NEW", str(max_new))], cwd=root,
+                         capture_output=True, text=True, timeout=300)
+    assert res.returncode == 0, res.stderr[-2000:]
+
+
+def test_serving_launches_are_counted_and_timed():
+    kv, q, table, cu = paged_inputs([1, 60], [40, 100], 4, 2, 64, 16, torch.bfloat16, seed=61)
+    p = api.PagedProblem(kv, 4, max_new=60)
+    args = (p, q, dev(table), dev(cu), dev([40, 100]))
+    plain = api.paged_attn_fwd(*args)
+    api.profile_read()
+    api.profile_enable(True)
+    timed = api.paged_attn_fwd(*args)
+    api.rope_axes(api.Rope([32]), dev(np.arange(61)), q)
+    api.kv_release(16, dev(table), dev([40, 100]), dev([0, 0]), dev([0]), dev([0]))
+    api.profile_enable(False)
+    got = api.profile_read()
+    assert all(torch.equal(a, b) for a, b in zip(plain, timed))
+    want = {"paged": 2, "paged_merge": 1, "head_rows": 1, "kv_tables": 1}
+    assert {k: n for k, (_, n) in got.items() if n} == want and all(got[k][0] > 0 for k in want)
