@@ -523,6 +523,7 @@ size_t cp_paged_attn_workspace_bytes(const cp_paged_desc* desc);
  * the cache where a key is visible reads as zeros and is reported: cp_get_device_error then
  * returns CP_ERR_INVALID_ARG.  A K/V value that is not finite reaches every
  * row whose tile of keys holds it, as in the other attention calls.
+ * A row with a NaN score has NaN in o and lse.
  * Results do not depend on timing: the same call gives the same bits.
  * Calls that share a workspace must not overlap on the GPU.
  * Errors: CP_ERR_INVALID_ARG, CP_ERR_UNSUPPORTED (sizes, heads), CP_ERR_ALIGNMENT,

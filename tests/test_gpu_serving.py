@@ -744,3 +744,27 @@ def test_serving_launches_are_counted_and_timed():
     assert all(torch.equal(a, b) for a, b in zip(plain, timed))
     want = {"paged": 2, "paged_merge": 1, "head_rows": 1, "kv_tables": 1}
     assert {k: n for k, (_, n) in got.items() if n} == want and all(got[k][0] > 0 for k in want)
+
+
+@pytest.mark.parametrize("dtype,new,max_new", [(torch.bfloat16, 3, 3), (torch.bfloat16, 8, 8), (torch.bfloat16, 90, 90),
+                                               (torch.float32, 1, 1), (torch.float32, 11, 11)])
+@pytest.mark.parametrize("ctx", [40, 9000])
+def test_a_row_that_is_not_a_number_says_so(dtype, new, max_new, ctx):
+    """A NaN in a row of q is in its O and its LSE, whether its tile is whole
+    or cut into pieces, and in no other row."""
+    lens = [ctx + new, 70]
+    kv, q, table, cu = paged_inputs([new, 1], lens, 4, 1, 128, 64, dtype, seed=62)
+    p = api.PagedProblem(kv, 4, max_new=max_new)
+    row = new // 2
+    bad = q.clone()
+    bad[row, 2, 5] = float("nan")
+    o, lse = api.paged_attn_fwd(p, bad, dev(table), dev(cu), dev(lens))
+    assert bool(torch.isnan(o[row, 2]).all()) and bool(torch.isnan(lse[row, 2]))
+    o[row, 2], lse[row, 2] = 0, 0
+    keep = torch.ones_like(lse, dtype=torch.bool)
+    keep[row, 2] = False
+    want_o, want_lse = api.paged_attn_fwd(p, q, dev(table), dev(cu), dev(lens))
+    assert bool(torch.isfinite(o).all()) and bool(torch.isfinite(lse).all())
+    # the other rows' states may be rescaled at other tiles: a few float32 roundings, and O's own
+    assert float((lse - want_lse)[keep].abs().max()) <= 64 * U32 * 16
+    assert float((o.double() - want_o.double())[keep].abs().max()) <= 2 * HALF[dtype] * float(want_o.abs().max()) + 64 * U32

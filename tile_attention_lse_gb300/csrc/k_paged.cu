@@ -5,7 +5,9 @@
 //   S_j = scale q . k_j over the visible keys (j < kv; causal: j <= i; window
 //   W: i - j < W), L = log sum_j exp S_j, O = sum_j exp(S_j - L) v_j, and O = 0,
 //   L = -inf for a row that sees none.  One pass over the keys with a running
-//   maximum and sum per row.
+//   maximum and sum per row.  The sum is 0 for a row that sees nothing and NaN
+//   where a score is NaN or +inf (the maximum passes over NaN): both states keep
+//   that through every join.
 //
 // What bounds it: a single token per request reads 4 d bytes (bf16) of K and V
 // per key and kv-head and does 8 d G flops on them, so HBM is the bound; the
@@ -323,10 +325,10 @@ struct SliceBf16 {
         l1 = fmaf(x[w].w, c1[w], l1);
       }
       if (part == 0 && (lane & 3) == 0) {
-        out0.put_lse(l0 > 0.f ? t0 + tc::lg2(l0) : -INFINITY);
-        out1.put_lse(l1 > 0.f ? t1 + tc::lg2(l1) : -INFINITY);
+        out0.put_lse(l0 == 0.f ? -INFINITY : t0 + tc::lg2(l0));
+        out1.put_lse(l1 == 0.f ? -INFINITY : t1 + tc::lg2(l1));
       }
-      const float v0 = l0 > 0.f ? 1.f / l0 : 0.f, v1 = l1 > 0.f ? 1.f / l1 : 0.f;
+      const float v0 = l0 == 0.f ? 0.f : 1.f / l0, v1 = l1 == 0.f ? 0.f : 1.f / l1;
 #pragma unroll 2
       for (int n = part; n < NT; n += kJoiners) {
         float o0[2] = {}, o1[2] = {};
@@ -541,11 +543,11 @@ struct SliceF32 {
         o[2] = fmaf(y.z, f, o[2]);
         o[3] = fmaf(y.w, f, o[3]);
       }
-      const float inv = sum > 0.f ? 1.f / sum : 0.f;
+      const float inv = sum == 0.f ? 0.f : 1.f / sum;
 #pragma unroll
       for (int e = 0; e < 4; ++e) o[e] *= inv;
       out.template put<4>(4 * c, o);
-      if (c == 0) out.put_lse(sum > 0.f ? top + log2f(sum) : -INFINITY);
+      if (c == 0) out.put_lse(sum == 0.f ? -INFINITY : top + log2f(sum));
     }
   }
   __device__ __forceinline__ void leave(float4* st, int warp, int lane) const {
@@ -887,30 +889,29 @@ __device__ __forceinline__ void merge_block(const PagedArgs& a, int c, int part,
     for (int o = kLanes / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(lanes, top, kPair ? 8 * o : o));
     float acc[N] = {};
     float sum = 0.f;
-    if (top != -INFINITY) {  // an empty state's O is 0
-      auto add = [&](float w, int j, const float* y) {
-        const float we = __shfl_sync(lanes, w, kPair ? which + 8 * j : 16 * which + j);
-        sum += we;
+    auto add = [&](float w, int j, const float* y) {
+      const float we = __shfl_sync(lanes, w, kPair ? which + 8 * j : 16 * which + j);
+      sum += we;
 #pragma unroll
-        for (int v = 0; v < N; ++v) acc[v] = fmaf(we, y[v], acc[v]);
-      };
-      for (int e0 = 0; e0 < n; e0 += kLanes) {
-        const float w = exp2f((e0 == 0 ? first : weigh(e0)) - top);
-        const int m = min(kLanes, n - e0);
-        int j = 0;
-        if (e0 == 0) {
+      for (int v = 0; v < N; ++v) acc[v] = fmaf(we, y[v], acc[v]);
+    };
+    for (int e0 = 0; e0 < n; e0 += kLanes) {
+      const float own = e0 == 0 ? first : weigh(e0);
+      const float w = own == -INFINITY ? 0.f : exp2f(own - top);  // an empty state's O is 0
+      const int m = min(kLanes, n - e0);
+      int j = 0;
+      if (e0 == 0) {
 #pragma unroll
-          for (; j < kEager; ++j) add(w, j, x[j]);
-        }
+        for (; j < kEager; ++j) add(w, j, x[j]);
+      }
 #pragma unroll 2
-        for (; j < m; ++j) {
-          float y[N];
-          load(e0 + j, r, y);
-          add(w, j, y);
-        }
+      for (; j < m; ++j) {
+        float y[N];
+        load(e0 + j, r, y);
+        add(w, j, y);
       }
     }
-    const float inv = sum > 0.f ? 1.f / sum : 0.f;
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
 #pragma unroll
     for (int v = 0; v < N; ++v) acc[v] *= inv;
     const int row = t.row0 + r;
@@ -918,7 +919,7 @@ __device__ __forceinline__ void merge_block(const PagedArgs& a, int c, int part,
 #pragma unroll
     for (int v = 0; v < N; v += 4)
       store_vec<T, 4>(static_cast<T*>(a.o) + out * D + 4 * (sl + kLanes * (v / 4)), acc + v);
-    if (sl == 0) a.lse[out] = sum > 0.f ? (top + log2f(sum)) * 0.69314718055994531f : -INFINITY;
+    if (sl == 0) a.lse[out] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.69314718055994531f;
   }
 }
 

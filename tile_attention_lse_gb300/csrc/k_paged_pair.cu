@@ -508,7 +508,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_pair_kernel(const __grid_co
           __syncwarp();
           if (lane == 0) tc::mbar_arrive(bar(B_MREADY0 + 2 * quarter + int(g & 1)));
           if (m != m_own) {  // this warp's sum, against the new max
-            l = (m_own == -INFINITY) ? 0.f : l * tc::ex2(m_own - m);
+            l *= tc::ex2(m_own - m);  // from -inf: 0, or NaN where a score was
             m_own = m;
           }
           const float mu = (m == -INFINITY) ? 0.f : m;
@@ -584,12 +584,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_pair_kernel(const __grid_co
         ++pieces;
         const float m_o = xend[(half ^ 1) * 256 + row], l_o = xend[(half ^ 1) * 256 + 128 + row];
         const float m_fin = fmaxf(m_own, m_o);
-        float l_all = 0.f;
-        if (m_fin != -INFINITY) {
-          if (m_own != -INFINITY) l_all += l * tc::ex2(m_own - m_fin);
-          if (m_o != -INFINITY) l_all += l_o * tc::ex2(m_o - m_fin);
-        }
-        inv = l_all > 0.f ? 1.f / l_all : 0.f;
+        const float l_all = m_fin == -INFINITY ? l + l_o : l * tc::ex2(m_own - m_fin) + l_o * tc::ex2(m_o - m_fin);
+        inv = l_all == 0.f ? 0.f : 1.f / l_all;
         // A whole tile writes the final O (bf16, round to nearest even) and LSE;
         // a piece of one its partial state (O in float32, LSE in log2 units).
         slot = pc.slot;
@@ -599,7 +595,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_pair_kernel(const __grid_co
         at = direct ? int64_t(pc.q.q0 + packed / a.G) * a.H + pc.h * a.G + packed % a.G
                     : int64_t(slot) * a.R + trow;
         if (row_ok && half == 0) {
-          const float l2 = l_all > 0.f ? m_fin + tc::lg2(l_all) : -INFINITY;
+          const float l2 = l_all == 0.f ? -INFINITY : m_fin + tc::lg2(l_all);
           if (direct)
             a.lse[at] = l2 * 0.69314718055994531f;
           else
