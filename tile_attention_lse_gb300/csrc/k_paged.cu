@@ -863,7 +863,7 @@ __device__ __forceinline__ void merge_block(const PagedArgs& a, int c, int part,
   // [4 columns][row] (float4), and 4 lanes with every fourth of them take a row, 8
   // rows a warp side by side.
   constexpr bool kPair = U == kPairUnit;
-  constexpr int kLanes = kPair ? 4 : 16, N = D / kLanes, kEager = kPair ? 1 : 2;
+  constexpr int kLanes = kPair ? 4 : 16, N = D / kLanes, kEager = kPair ? 1 : 2, kAtOnce = kPair ? 1 : 4;
   constexpr int kRowsAtOnce = 32 / kLanes;
   const int which = kPair ? lane & 7 : lane >> 4, sl = kPair ? lane >> 3 : lane & 15;
   const uint32_t lanes = kPair ? 0x01010101u << which : 0xffffu << (16 * which);  // a row's
@@ -904,11 +904,13 @@ __device__ __forceinline__ void merge_block(const PagedArgs& a, int c, int part,
 #pragma unroll
         for (; j < kEager; ++j) add(w, j, x[j]);
       }
-#pragma unroll 2
-      for (; j < m; ++j) {
-        float y[N];
-        load(e0 + j, r, y);
-        add(w, j, y);
+      for (; j < m; j += kAtOnce) {  // kAtOnce under way (behind the last one, that again)
+        float y[kAtOnce][N];
+#pragma unroll
+        for (int i = 0; i < kAtOnce; ++i) load(e0 + min(j + i, m - 1), r, y[i]);
+#pragma unroll
+        for (int i = 0; i < kAtOnce; ++i)
+          if (j + i < m) add(w, j + i, y[i]);
       }
     }
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
