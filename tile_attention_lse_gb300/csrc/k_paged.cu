@@ -360,16 +360,19 @@ struct SliceBf16 {
 };
 
 // --------------------------------------------------------- float32: FFMA ---
-// A stage of 32 keys is one worker's, or two workers' with half of the tile's
-// rows each.  First product: a lane owns a key
-// and the rows of Q come by broadcast, so nothing is summed across lanes and every
+// A stage of 32 keys (64 at head_dim 64 and 16 rows) is one worker's, or two workers' with half of the tile's
+// rows each.  First product: a lane owns a key, or two
+// (four requests of 100 tokens over 3000, 8 heads over 2, head_dim 64: 112 us, 97 with two: shared memory
+// gives a row's Q to twice the products; one request of 3 over 100: 12.1 us, 13.8;
+// head_dim 128 has no room for such stages), and the rows of Q come by broadcast, so nothing is summed across lanes and every
 // exponential is formed once; P changes hands through shared memory, and in the second product a lane
 // owns 4 columns (head_dim 64: of half of the keys).
 template <int D, int R>
 struct SliceF32 {
   using T = float;
   static constexpr int RW = R < 8 ? R : 8;  // rows of a worker
-  static constexpr int kWarps = R < 8 ? 4 : 8, kPerStage = R / RW, kKeys = 32, kStages = D == 128 ? 4 : 8;
+  static constexpr int KL = D == 64 && R >= 8 ? 2 : 1;  // keys of a lane
+  static constexpr int kWarps = R < 8 ? 4 : 8, kPerStage = R / RW, kKeys = 32 * KL, kStages = D == 128 || KL == 2 ? 4 : 8;
   static constexpr int kStageKeys = kKeys;
   static __device__ __forceinline__ int first_key(int) { return 0; }
   static constexpr int kAcc = 4 * RW;
@@ -409,40 +412,51 @@ struct SliceF32 {
 
   __device__ __forceinline__ void slice(const PagedArgs& a, uint32_t sq, uint32_t sk, uint32_t sv, int srow, float* sp,
                                         int key, bool full, int klo, int khi, int lane) {
-    uint64_t s2[RW];                   // sums over even and odd elements of the head
+    uint64_t s2[KL][RW];               // sums over even and odd elements of the head
 #pragma unroll
-    for (int r = 0; r < RW; ++r) s2[r] = 0;
-#pragma unroll 4
+    for (int x = 0; x < KL; ++x)
+#pragma unroll
+      for (int r = 0; r < RW; ++r) s2[x][r] = 0;
+#pragma unroll(KL == 2 ? 2 : 4)
     for (int c = 0; c < D / 4; ++c) {
-      uint64_t k0, k1;
-      lds2(sk + at(srow + lane, c), k0, k1);
+      uint64_t k0[KL], k1[KL];
+#pragma unroll
+      for (int x = 0; x < KL; ++x) lds2(sk + at(srow + lane + 32 * x, c), k0[x], k1[x]);
       uint64_t q0[RW], q1[RW];
 #pragma unroll
       for (int r = 0; r < RW; ++r) lds2(sq + q_at(first + r, c), q0[r], q1[r]);
 #pragma unroll
-      for (int r = 0; r < RW; ++r) s2[r] = tc::ffma2(q0[r], k0, s2[r]);
+      for (int x = 0; x < KL; ++x) {
 #pragma unroll
-      for (int r = 0; r < RW; ++r) s2[r] = tc::ffma2(q1[r], k1, s2[r]);
-    }
-    float s[RW];
+        for (int r = 0; r < RW; ++r) s2[x][r] = tc::ffma2(q0[r], k0[x], s2[x][r]);
 #pragma unroll
-    for (int r = 0; r < RW; ++r) {
-      float x, y;
-      tc::f32x2_split(s2[r], x, y);
-      s[r] = x + y;
+        for (int r = 0; r < RW; ++r) s2[x][r] = tc::ffma2(q1[r], k1[x], s2[x][r]);
+      }
     }
-    const int j = key + lane;
+    float s[KL][RW];
+#pragma unroll
+    for (int x = 0; x < KL; ++x)
+#pragma unroll
+      for (int r = 0; r < RW; ++r) {
+        float u, w;
+        tc::f32x2_split(s2[x][r], u, w);
+        s[x][r] = u + w;
+      }
     if (!full) {
 #pragma unroll
       for (int r = 0; r < RW; ++r) {
         const int pos = pos0 + (row0 + r) / a.G;
-        const bool see = j < kv && (!a.causal || j <= pos) && (a.window == 0 || pos - j < a.window);
-        s[r] = see ? s[r] : -INFINITY;
+#pragma unroll
+        for (int x = 0; x < KL; ++x) {
+          const int j = key + lane + 32 * x;
+          const bool see = j < kv && (!a.causal || j <= pos) && (a.window == 0 || pos - j < a.window);
+          s[x][r] = see ? s[x][r] : -INFINITY;
+        }
       }
     }
     float up[RW];
 #pragma unroll
-    for (int r = 0; r < RW; ++r) up[r] = s[r];
+    for (int r = 0; r < RW; ++r) up[r] = fmaxf(s[0][r], s[KL - 1][r]);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1)
 #pragma unroll
@@ -472,11 +486,17 @@ struct SliceF32 {
 #pragma unroll
     for (int r = 0; r < RW; ++r) {
       const float base = m[r] == -INFINITY ? 0.f : m[r];
-      s[r] = exp2f(fmaf(s[r], a.scale_log2, -base));
-      l[r] += s[r];
+#pragma unroll
+      for (int x = 0; x < KL; ++x) {
+        s[x][r] = exp2f(fmaf(s[x][r], a.scale_log2, -base));
+        l[r] += s[x][r];
+      }
     }
 #pragma unroll
-    for (int r = 0; r < RW; r += 4) *p_at(sp, lane, r) = make_float4(s[r], s[r + 1], s[r + 2], s[r + 3]);
+    for (int x = 0; x < KL; ++x)
+#pragma unroll
+      for (int r = 0; r < RW; r += 4)
+        *p_at(sp, lane + 32 * x, r) = make_float4(s[x][r], s[x][r + 1], s[x][r + 2], s[x][r + 3]);
     __syncwarp();
     constexpr int kn = D == 128 ? kKeys : kKeys / 2;
     const int c = D == 128 ? lane : lane & 15, x0 = D == 128 ? 0 : (lane >> 4) * kn;
