@@ -106,7 +106,7 @@ __device__ __forceinline__ PieceInfo piece_info(const PagedArgs& a, const PagedP
   i.n = end > i.key0 ? (end - i.key0 + kStageKeys - 1) / kStageKeys : 0;
   i.lo = p.tile.lo;
   i.hi = p.tile.hi;
-  const int first = i.pos0 + i.row0 / a.G, last = i.pos0 + (i.row0 + i.nrows - 1) / a.G;
+  const int first = i.pos0 + paged_token(a, i.row0), last = i.pos0 + paged_token(a, i.row0 + i.nrows - 1);
   i.full_hi = a.causal ? min(i.kv, first + 1) : i.kv;
   i.full_lo = a.window > 0 ? max(0, last - a.window + 1) : 0;
   i.slot = p.slot;
@@ -124,7 +124,8 @@ struct SliceOut {
     in = r < p.nrows;
     whole = p.slot < 0;
     const int x = p.row0 + r;
-    const int64_t row = int64_t(p.q0 + x / a.G) * a.H + p.h * a.G + x % a.G, prow = int64_t(p.slot) * R + r;
+    const int t = paged_token(a, x);
+    const int64_t row = int64_t(p.q0 + t) * a.H + p.h * a.G + (x - t * a.G), prow = int64_t(p.slot) * R + r;
     o = static_cast<T*>(a.o) + row * D;
     part = a.part_o + prow * D;
     lse = whole ? a.lse + row : a.part_l + prow;
@@ -176,7 +177,7 @@ struct SliceBf16 {
     for (int i = 0; i < kRows; ++i) {
       m[i] = -INFINITY;
       l[i] = 0.f;
-      const int pos = p.pos0 + (p.row0 + (lane >> 2) + 8 * i) / a.G;
+      const int pos = p.pos0 + paged_token(a, p.row0 + (lane >> 2) + 8 * i);
       hi[i] = a.causal ? min(p.kv, pos + 1) : p.kv;
       lo[i] = a.window > 0 ? pos - a.window + 1 : 0;
     }
@@ -445,7 +446,7 @@ struct SliceF32 {
     if (!full) {
 #pragma unroll
       for (int r = 0; r < RW; ++r) {
-        const int pos = pos0 + (row0 + r) / a.G;
+        const int pos = pos0 + paged_token(a, row0 + r);
 #pragma unroll
         for (int x = 0; x < KL; ++x) {
           const int j = key + lane + 32 * x;
@@ -657,18 +658,21 @@ __global__ void __launch_bounds__(SliceLayout<S, D, R>::kThreads, 1)
   }
 
   grid_launch_dependents();
-  if (tid == 0) {
-    for (int i = 0; i < 3 * kPieces; ++i) tc::mbar_init(tc::smem_u32(s_bar + i), i / kPieces == 1 ? 32 : (i / kPieces == 2 ? kJoiners : 1));
-    for (int i = 0; i < NS; ++i) {
-      tc::mbar_init(bar_full(i), 2);  // both producers
-      tc::mbar_init(bar_empty(i), S::kPerStage);
-    }
-    tc::mbar_init(bar_state, W);
-    s_abort = 0;
+  // a thread a barrier: one thread's loop over them took 0.4 us
+  static_assert(3 * kPieces + 2 * NS + 1 <= 64, "two warps' barriers");
+  if (tid < 3 * kPieces + 2 * NS + 1) {
+    constexpr int full = 3 * kPieces, empty = full + NS, state = empty + NS;
+    tc::mbar_init(tc::smem_u32(s_bar + tid), tid < kPieces       ? 1
+                                             : tid < 2 * kPieces ? 32
+                                             : tid < full        ? kJoiners
+                                             : tid < empty       ? 2  // both producers
+                                             : tid < state       ? S::kPerStage
+                                                                 : W);
     tc::fence_mbar_init();
-    tc::prefetch_tmap(&sp.tmk);
-    tc::prefetch_tmap(&sp.tmv);
   }
+  if (tid == 64) s_abort = 0;
+  if (tid == 96) tc::prefetch_tmap(&sp.tmk);
+  if (tid == 128) tc::prefetch_tmap(&sp.tmv);
   const PagedShare share = paged_locate<kSliceUnit, kSliceExtra, L::kThreads>(a, s_scan, &s_start, blockIdx.x);
   const int64_t u0 = share.first(blockIdx.x), u1 = share.first(blockIdx.x + 1);
   if (u1 <= u0) {
@@ -726,7 +730,8 @@ __global__ void __launch_bounds__(SliceLayout<S, D, R>::kThreads, 1)
       for (int e = of_k ? lane : R * CH; e < R * CH; e += 32) {  // Q, zeros behind the tile's rows
         const int r = e / CH, c = e % CH, row = i.row0 + r;
         const bool in = r < i.nrows;
-        const int64_t off = in ? int64_t(i.q0 + row / a.G) * a.q_stride + int64_t(i.h * a.G + row % a.G) * D + c * V : 0;
+        const int tok = paged_token(a, row);
+        const int64_t off = in ? int64_t(i.q0 + tok) * a.q_stride + int64_t(i.h * a.G + row - tok * a.G) * D + c * V : 0;
         cp_async16(sbase + L::kOffQ + (k % kPieces) * L::kQBytes + S::q_at(r, c), static_cast<const T*>(a.q) + off, in);
       }
       if (of_k) asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar_q(k)) : "memory");
@@ -937,7 +942,8 @@ __device__ __forceinline__ void merge_block(const PagedArgs& a, int c, int part,
 #pragma unroll
     for (int v = 0; v < N; ++v) acc[v] *= inv;
     const int row = t.row0 + r;
-    const int64_t out = int64_t(q.q0 + row / a.G) * a.H + st.h * a.G + row % a.G;
+    const int tok = paged_token(a, row);
+    const int64_t out = int64_t(q.q0 + tok) * a.H + st.h * a.G + (row - tok * a.G);
 #pragma unroll
     for (int v = 0; v < N; v += 4)
       store_vec<T, 4>(static_cast<T*>(a.o) + out * D + 4 * (sl + kLanes * (v / 4)), acc + v);

@@ -170,19 +170,18 @@ __global__ void __launch_bounds__(kThreads, 1) paged_pair_kernel(const __grid_co
   const int64_t units = share.first(pair + 1) - share.first(pair);
   if (pair >= share.n) return;  // these SMs are the slice launch's
 
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < B_COUNT; ++i) {
-      uint32_t cnt = 1;
-      if ((i >= B_PFULL0 && i < B_PFULL0 + kSBufs) || (i >= B_SEMPTY0 && i < B_SEMPTY0 + kSBufs))
-        cnt = 8;  // a tile's 4 softmax warps x 2 CTAs
-      if (i == B_OEMPTY) cnt = 16;  // all 8 softmax warps x 2 CTAs
-      if (i == B_DRAIN) cnt = 2;    // both issuers
-      if (i >= B_JOIN0) cnt = 2;
-      tc::mbar_init(bar(i), cnt);
-    }
-    *abort_flag = 0;
+  static_assert(B_COUNT <= kThreads, "a thread a barrier");
+  if (const int i = threadIdx.x; i < B_COUNT) {
+    uint32_t cnt = 1;
+    if ((i >= B_PFULL0 && i < B_PFULL0 + kSBufs) || (i >= B_SEMPTY0 && i < B_SEMPTY0 + kSBufs))
+      cnt = 8;  // a tile's 4 softmax warps x 2 CTAs
+    if (i == B_OEMPTY) cnt = 16;  // all 8 softmax warps x 2 CTAs
+    if (i == B_DRAIN) cnt = 2;    // both issuers
+    if (i >= B_JOIN0) cnt = 2;
+    tc::mbar_init(bar(i), cnt);
     tc::fence_mbar_init();
   }
+  if (threadIdx.x == 0) *abort_flag = 0;
   if (warp == 1) {
     tc::tmem_alloc_pair(tc::smem_u32(tmem_slot), 512);
     tc::tmem_relinquish_pair();
@@ -299,7 +298,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_pair_kernel(const __grid_co
         if (!ok) break;
         if (lane == 0) {
           if (even) tc::mbar_arrive_expect_tx(bar(B_QFULL0 + qb), (D / 32) * 128u * uint32_t(half_rows));
-          const int tok = pc.q.q0 + (pc.tile.row0 + int(rank) * half_rows) / a.G, h = pc.h * a.G;
+          const int tok = pc.q.q0 + paged_token(a, pc.tile.row0 + int(rank) * half_rows), h = pc.h * a.G;
           tc::tma_load_3d_pair(sQ + qb * kQBytes, &p.tmq, bar_even(B_QFULL0 + qb), 0, h, tok);
           if (D == 128) tc::tma_load_3d_pair(sQ + qb * kQBytes + kQHalf, &p.tmq, bar_even(B_QFULL0 + qb), 64, h, tok);
         }
@@ -592,7 +591,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_pair_kernel(const __grid_co
         const bool direct = slot < 0;
         trow = int(rank) * half_rows + row;
         const int packed = pc.tile.row0 + trow;
-        at = direct ? int64_t(pc.q.q0 + packed / a.G) * a.H + pc.h * a.G + packed % a.G
+        const int tok = paged_token(a, packed);
+        at = direct ? int64_t(pc.q.q0 + tok) * a.H + pc.h * a.G + (packed - tok * a.G)
                     : int64_t(slot) * a.R + trow;
         if (row_ok && half == 0) {
           const float l2 = l_all == 0.f ? -INFINITY : m_fin + tc::lg2(l_all);

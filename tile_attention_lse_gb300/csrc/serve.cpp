@@ -194,6 +194,7 @@ PagedArgs paged_args(const cp_paged_desc& d, int32_t n_reqs, int64_t rows, int32
   a.H = d.heads_q;
   a.Hkv = d.kv.heads_kv;
   a.G = a.H / a.Hkv;
+  a.g_inv = paged_inverse(uint32_t(a.G));
   a.d = d.kv.head_dim;
   a.dtype = d.kv.dtype;
   a.causal = d.causal != 0;
@@ -206,6 +207,8 @@ void split_args(const PagedPlan& p, const PagedArgs& a, PagedArgs* pair, PagedAr
   *pair = *slice = a;
   pair->R = paged_rows(kPagedPair, p.use_pair ? a.G : 1);
   slice->R = paged_rows(p.slice, a.G);
+  pair->r_inv = slice->other_r_inv = paged_inverse(uint32_t(pair->R));
+  slice->r_inv = pair->other_r_inv = paged_inverse(uint32_t(slice->R));
   pair->grid = pair_blocks(p);
   slice->grid = p.use_slice ? paged_slice_grid() : 0;
   if (p.use_pair && p.use_slice) {
