@@ -713,7 +713,7 @@ __global__ void __launch_bounds__(SliceLayout<S, D, R>::kThreads, 1)
       const int key = x.i.key0 + ((f + lane) << bs);
       return seen(x.i, key) ? a.table[int64_t(x.r) * a.max_blocks + (key >> a.page_shift)] : a.n_pages;
     };
-    uint32_t g = 0;
+    uint32_t g = 0, q_rows = 0x01010101u * R;  // rows of the places of Q that may hold something
     bool ok = true;
     Next at = come();
     int32_t pages = window(at, 0);
@@ -727,7 +727,12 @@ __global__ void __launch_bounds__(SliceLayout<S, D, R>::kThreads, 1)
         }
       }
       if (!i.valid) break;
-      for (int e = of_k ? lane : R * CH; e < R * CH; e += 32) {  // Q, zeros behind the tile's rows
+      // Q, and zeros behind the tile's rows where the place does not hold them yet
+      static_assert(kPieces <= 4 && R < 256, "rows of each place in a byte");
+      const int byte = 8 * (k % kPieces), had = int(q_rows >> byte) & 255;
+      q_rows = (q_rows & ~(255u << byte)) | (uint32_t(i.nrows) << byte);
+      const int copies = of_k ? max(i.nrows, had) * CH : 0;
+      for (int e = lane; e < copies; e += 32) {
         const int r = e / CH, c = e % CH, row = i.row0 + r;
         const bool in = r < i.nrows;
         const int tok = paged_token(a, row);
