@@ -302,13 +302,22 @@ struct SliceBf16 {
     }
   }
 
-  // Joins the workers' states at `st` (float4s [worker][kAcc / 4 + kRows / 2][lane])
-  // and writes them out.  Loops stay loops: one warp runs this once per
+  // A worker's state: float4s [MT][NT / 2][row half][lane] of O (its row lane / 4, or
+  // 8 further, in two n-tiles), then m and l of both rows [MT][lane].  Lanes and halves
+  // without a row of the tile are left out on both sides: with 4 heads a group three
+  // quarters of what would cross shared memory.
+  static __device__ __forceinline__ bool any_row(const PieceInfo& p, int i, int lane) {
+    return (lane >> 2) + 16 * i < p.nrows;
+  }
+  static __device__ __forceinline__ bool upper(const PieceInfo& p, int i) { return p.nrows > 16 * i + 8; }
+
+  // Joins the workers' states and writes them out.  Loops stay loops: one warp runs this once per
   // piece, and unrolled it waited for its own instructions (4 to 9 us a piece, 1 us so).
   static __device__ __forceinline__ void join(const PagedArgs& a, const PieceInfo& p, const float4* st, int part,
                                               int lane) {
 #pragma unroll 1
     for (int i = 0; i < MT; ++i) {  // this lane's rows 8 * 2 i + lane / 4 and 8 further
+      if (!any_row(p, i, lane)) break;
       const SliceOut<T, D, R> out0(a, p, (lane >> 2) + 16 * i), out1(a, p, (lane >> 2) + 16 * i + 8);
       float c0[kWarps], c1[kWarps], t0 = -INFINITY, t1 = -INFINITY, l0 = 0.f, l1 = 0.f;
       float4 x[kWarps];  // m and l of the two rows
@@ -330,33 +339,42 @@ struct SliceBf16 {
         out1.put_lse(l1 == 0.f ? -INFINITY : t1 + tc::lg2(l1));
       }
       const float v0 = l0 == 0.f ? 0.f : 1.f / l0, v1 = l1 == 0.f ? 0.f : 1.f / l1;
-#pragma unroll 2
-      for (int n = part; n < NT; n += kJoiners) {
-        float o0[2] = {}, o1[2] = {};
+      auto half = [&](const SliceOut<T, D, R>& out, const float* c, float v, int n, const float4* at) {
+        float o[4] = {};
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
-          const float4 y = st[w * kState + (i * NT + n) * 32 + lane];
-          o0[0] = fmaf(y.x, c0[w], o0[0]);
-          o0[1] = fmaf(y.y, c0[w], o0[1]);
-          o1[0] = fmaf(y.z, c1[w], o1[0]);
-          o1[1] = fmaf(y.w, c1[w], o1[1]);
+          const float4 y = at[w * kState];
+          o[0] = fmaf(y.x, c[w], o[0]);
+          o[1] = fmaf(y.y, c[w], o[1]);
+          o[2] = fmaf(y.z, c[w], o[2]);
+          o[3] = fmaf(y.w, c[w], o[3]);
         }
-        o0[0] *= v0;
-        o0[1] *= v0;
-        o1[0] *= v1;
-        o1[1] *= v1;
-        out0.template put<2>(8 * n + 2 * (lane & 3), o0);
-        out1.template put<2>(8 * n + 2 * (lane & 3), o1);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[e] *= v;
+        out.template put<2>(16 * n + 2 * (lane & 3), o);
+        out.template put<2>(16 * n + 8 + 2 * (lane & 3), o + 2);
+      };
+#pragma unroll 2
+      for (int n = part; n < NT / 2; n += kJoiners) {
+        const float4* at = st + ((i * (NT / 2) + n) * 2) * 32 + lane;
+        half(out0, c0, v0, n, at);
+        if (upper(p, i)) half(out1, c1, v1, n, at + 32);
       }
     }
   }
-  __device__ __forceinline__ void leave(float4* st, int warp, int lane) const {
+  __device__ __forceinline__ void leave(const PieceInfo& p, float4* st, int warp, int lane) const {
     float4* x = st + warp * kState + lane;
 #pragma unroll
-    for (int i = 0; i < kAcc / 4; ++i) x[i * 32] = make_float4(acc[4 * i], acc[4 * i + 1], acc[4 * i + 2], acc[4 * i + 3]);
+    for (int i = 0; i < MT; ++i) {
+      if (!any_row(p, i, lane)) break;
 #pragma unroll
-    for (int i = 0; i < kRows / 2; ++i)
+      for (int n = 0; n < NT / 2; ++n) {
+        const float* y = acc + (i * NT + 2 * n) * 4;
+        x[((i * (NT / 2) + n) * 2) * 32] = make_float4(y[0], y[1], y[4], y[5]);
+        if (upper(p, i)) x[((i * (NT / 2) + n) * 2 + 1) * 32] = make_float4(y[2], y[3], y[6], y[7]);
+      }
       x[(kAcc / 4 + i) * 32] = make_float4(m[2 * i], m[2 * i + 1], l[2 * i], l[2 * i + 1]);
+    }
   }
 };
 
@@ -571,7 +589,7 @@ struct SliceF32 {
       if (c == 0) out.put_lse(sum == 0.f ? -INFINITY : top + log2f(sum));
     }
   }
-  __device__ __forceinline__ void leave(float4* st, int warp, int lane) const {
+  __device__ __forceinline__ void leave(const PieceInfo&, float4* st, int warp, int lane) const {
     float4* x = st + warp * kState + lane;
 #pragma unroll
     for (int r = 0; r < RW; r += 2) {
@@ -832,7 +850,7 @@ __global__ void __launch_bounds__(SliceLayout<S, D, R>::kThreads, 1)
     st.end();
     // the state's place is free once the piece before it is joined
     if (k > 0 && !wait(bar_joined(k - 1), phase(k - 1))) break;
-    st.leave(states, warp, lane);
+    st.leave(p, states, warp, lane);
     __syncwarp();
     if (lane == 0) tc::mbar_arrive(bar_state);
   }
