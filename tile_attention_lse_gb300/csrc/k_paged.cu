@@ -14,10 +14,10 @@
 // kernel's job is to keep enough loads in flight on every SM.  Warps have parts:
 //   producers walk the block's share, up to four pieces ahead, and load it, one
 //             K (and Q by 16-byte copies), one V: by TMA, a box per page and 128
-//             bytes of the head, into a ring of stages of 32 KB (head_dim 64:
-//             16 KB).  A box costs its issuer about 55 ns whatever it
+//             bytes of the head, into a ring of stages of 32 KB (of
+//             128 keys at head_dim 64).  A box costs its issuer about 55 ns whatever it
 //             holds, 2 KB at pages of 16: two issuers share them;
-//   workers   take the stages in turn (bf16: four of them each, float32: one); a worker has its own
+//   workers   take the stages in turn (bf16: four or eight of them each, float32: one or two); a worker has its own
 //             slice of a stage's keys and its own running maximum, sum and O, so
 //             no barrier stands between them; at the end of a piece it leaves its state
 //             in shared memory and goes on with the next one;
@@ -36,6 +36,7 @@
 // float32: FFMA throughout, for the arithmetic's sake.
 #include <cuda_bf16.h>
 
+#include <algorithm>
 #include <atomic>
 #include <mutex>
 
@@ -86,7 +87,7 @@ struct PieceInfo {
   int32_t pos0;                // position of the request's first new token
   int32_t kv;
   int32_t key0, n;             // first stage's first key, stages
-  int32_t lo, hi;              // keys that some row sees
+  int32_t lo, hi;              // keys that some row sees, up to the piece's end
   int32_t full_lo, full_hi;    // keys that every row sees
   int32_t slot;
 };
@@ -105,7 +106,7 @@ __device__ __forceinline__ PieceInfo piece_info(const PagedArgs& a, const PagedP
   const int end = min((p.tile.b0 + p.ub) * kSliceUnit, p.tile.hi);
   i.n = end > i.key0 ? (end - i.key0 + kStageKeys - 1) / kStageKeys : 0;
   i.lo = p.tile.lo;
-  i.hi = p.tile.hi;
+  i.hi = end;  // the last stage may reach into the next piece's keys
   const int first = i.pos0 + paged_token(a, i.row0), last = i.pos0 + paged_token(a, i.row0 + i.nrows - 1);
   i.full_hi = a.causal ? min(i.kv, first + 1) : i.kv;
   i.full_lo = a.window > 0 ? max(0, last - a.window + 1) : 0;
@@ -148,8 +149,10 @@ template <int D, int R>
 struct SliceBf16 {
   using T = __nv_bfloat16;
   // 32 rows of 128 columns: the states of four workers are what shared memory holds
-  static constexpr int kWarps = D * R > 64 * 32 && R > 16 ? 4 : 8, kPerStage = 4, kKeys = 16;  // kPerStage: workers of a stage
-  static constexpr int kStages = D == 128 ? 4 : 8;
+  static constexpr int kWarps = D * R > 64 * 32 && R > 16 ? 4 : 8;
+  // kPerStage: workers of a stage.  Stages of 32 KB: a stage costs a producer as much
+  // as several boxes (head_dim 64, pages of 16, contexts of 60000: 105 us with 16 KB, 88)
+  static constexpr int kPerStage = D == 128 ? 4 : 8, kKeys = 16, kStages = 4;
   static constexpr int kStageKeys = kPerStage * kKeys;
   static __device__ __forceinline__ int first_key(int warp) { return (warp % kPerStage) * kKeys; }  // a worker's slice of a stage
   static constexpr int MT = R / 16, NT = D / 8;
@@ -1005,7 +1008,7 @@ cp_status run_slice(const PagedArgs& a, bool after_pair, cudaStream_t s) {
     ready[dev].store(true, std::memory_order_release);
   }
   SliceParams p;
-  const int page = 1 << a.page_shift, box = page < S::kStageKeys ? page : S::kStageKeys;
+  const int page = 1 << a.page_shift, most = std::min(S::kStageKeys, kSliceUnit), box = std::min(page, most);
   p.head_inner = a.head_stride <= a.token_stride;
   if (!make_tmap_pages(&p.tmk, a.k, a, box) || !make_tmap_pages(&p.tmv, a.v, a, box)) return CP_ERR_CUDA;
   p.a = a;
