@@ -225,7 +225,7 @@ void split_args(const PagedPlan& p, const PagedArgs& a, PagedArgs* pair, PagedAr
     const int page = 1 << a.page_shift;
     pair->pair_cost = slice->pair_cost = page == 8 ? 2400 : 1800;
     pair->slice_cost = slice->slice_cost =
-        page >= 64 ? (wide ? 480 : 350) : page == 32 ? (wide ? 500 : 360) : page == 16 ? (wide ? 640 : 450) : (wide ? 950 : 600);
+        page >= 64 ? (wide ? 480 : 290) : page == 32 ? (wide ? 500 : 290) : page == 16 ? (wide ? 640 : 340) : (wide ? 950 : 520);
   }
 }
 
