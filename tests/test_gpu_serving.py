@@ -768,3 +768,39 @@ def test_a_row_that_is_not_a_number_says_so(dtype, new, max_new, ctx):
     # the other rows' states may be rescaled at other tiles: a few float32 roundings, and O's own
     assert float((lse - want_lse)[keep].abs().max()) <= 64 * U32 * 16
     assert float((o.double() - want_o.double())[keep].abs().max()) <= 2 * HALF[dtype] * float(want_o.abs().max()) + 64 * U32
+
+
+# The first table call of its process: no earlier, larger one has raised the
+# kernel's limit of dynamic shared memory.
+EXTEND_FIRST = """
+import torch
+from tile_attention_lse_gb300 import api
+n, i32 = N_REQS, dict(dtype=torch.int32, device="cuda:0")
+table, free = torch.full((n, 2), -1, **i32), torch.arange(n, **i32)
+lens, cu, slots, pos, n_free = api.kv_extend(16, table, torch.zeros(n, **i32), torch.ones(n, **i32), free,
+                                             torch.full((1,), n, **i32), n)
+at = torch.arange(n + 1, **i32)
+assert torch.equal(lens, torch.ones_like(lens)) and torch.equal(cu, at) and int(n_free) == 0
+assert torch.equal(slots, (n - 1 - at[:n]) * 16) and not bool(pos.any())
+assert torch.equal(table[:, 0], n - 1 - at[:n]) and bool((table[:, 1] == -1).all())
+"""
+
+
+@pytest.mark.parametrize("n", [6016, 6017, 6079, 6144, 6145])
+def test_the_first_extend_of_a_process_takes_any_number_of_requests(n):
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    res = subprocess.run([sys.executable, "-c", EXTEND_FIRST.replace("N_REQS", str(n))], cwd=root, capture_output=True,
+                         text=True, timeout=300)
+    assert res.returncode == 0, res.stderr[-2000:]
+
+
+@pytest.mark.parametrize("n", [6078, 6079, 6144, 6145, 16384])
+def test_extend_of_thousands_of_requests(n):
+    rng = np.random.default_rng(n)
+    table, lens, add, free, n_free, rows = table_case(n, 16, 4, rng.integers(0, 3, n), rng.integers(0, 60, n), 2 * n, 7, n)
+    t, want_t = dev(table), table.copy()
+    want = P.extend(lens, add, want_t, free, n_free, 16, rows)
+    got = api.kv_extend(16, t, dev(lens), dev(add), dev(free), dev([n_free]), rows)
+    for g, w, what in zip(got, want, ("lens", "cu", "slots", "pos", "n_free")):
+        assert np.array_equal(host(g).ravel(), np.ravel(w)), what
+    assert np.array_equal(host(t), want_t)

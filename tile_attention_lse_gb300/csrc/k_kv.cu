@@ -374,7 +374,9 @@ cp_status launch_head_rows(const HeadRows& a, cp_dtype dtype, cudaStream_t s) {
 
 cp_status launch_kv_extend(const KvTables& a, cudaStream_t s) {
   const size_t smem = size_t(a.n_reqs) * 8;
-  if (smem > 48 * 1024 &&
+  // what needs no opt-in is 48 KB of dynamic and static shared memory together;
+  // the kernel's static arrays are less than 1 KB
+  if (smem > 47 * 1024 &&
       cudaFuncSetAttribute(kv_extend_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxTableReqs * 8) !=
           cudaSuccess)
     return CP_ERR_CUDA;
