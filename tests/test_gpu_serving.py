@@ -804,3 +804,16 @@ def test_extend_of_thousands_of_requests(n):
     for g, w, what in zip(got, want, ("lens", "cu", "slots", "pos", "n_free")):
         assert np.array_equal(host(g).ravel(), np.ravel(w)), what
     assert np.array_equal(host(t), want_t)
+
+
+def test_calls_by_public_functions_alone():
+    # where PyTorch lacks the private shortcuts to streams and tensors
+    script = """
+import sys
+import torch
+del torch._C._cuda_getCurrentRawStream
+sys.modules["torch._C._dynamo.guards"] = None
+""" + FIRST_CALL.replace("MAX_NEW", "39")
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    res = subprocess.run([sys.executable, "-c", script], cwd=root, capture_output=True, text=True, timeout=300)
+    assert res.returncode == 0, res.stderr[-2000:]

@@ -2,6 +2,9 @@
 paged attention over the blocks of its launch (no GPU calls)."""
 
 import ctypes
+import os
+import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -224,3 +227,29 @@ def test_shares_are_even():
     units = 8 * sum(-(-n // 64) + 2 for n in lens)
     assert load.max() <= 64 * -(-units // grid)
     assert np.median(load) >= 0.97 * load.max()
+
+
+# A PyTorch that was built without CUDA lacks these private functions.
+WITHOUT_CUDA = """
+import sys
+import torch
+del torch._C._cuda_getCurrentRawStream
+sys.modules["torch._C._dynamo.guards"] = None
+from tile_attention_lse_gb300 import api
+t = torch.zeros((9, 16, 2, 128), dtype=torch.bfloat16)
+p = api.PagedProblem(api.PagedKV(t, t), 8, max_new=3)
+assert api.validate_paged(p) == 0 and api.paged_workspace_bytes(p) > 0
+assert len(api.paged_schedule(p, [0, 3], [40], 3, 4)[0]) > 0
+assert len(api.hybrid_schedule([128, 256], 4, 128)[0]) == 2
+try:
+    api.kv_extend(16, *(torch.zeros(s, dtype=torch.int32) for s in ((1, 4), (1,), (1,), (4,), (1,))), 3)
+except ValueError:
+    print("refused")
+"""
+
+
+def test_the_package_imports_without_cuda_in_pytorch():
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    res = subprocess.run([sys.executable, "-c", WITHOUT_CUDA], cwd=root, capture_output=True, text=True, timeout=300,
+                         env=dict(os.environ, CUDA_VISIBLE_DEVICES=""))
+    assert res.returncode == 0 and res.stdout.strip() == "refused", res.stderr[-2000:]

@@ -440,7 +440,11 @@ class PagedProblem:
 # directly, and new tensors are made below PyTorch's dispatcher where it offers
 # that (a table call's five outputs: 12 us through it, 4 us below).
 _I32, _F32 = torch.int32, torch.float32
-_raw_stream = torch._C._cuda_getCurrentRawStream
+try:
+    _raw_stream = torch._C._cuda_getCurrentRawStream
+except AttributeError:  # a PyTorch without CUDA: the host-only calls still work
+    def _raw_stream(device):
+        return torch.cuda.current_stream(device).cuda_stream
 try:
     from torch._C._dynamo.guards import _empty_strided_cuda, _reinterpret_tensor
 except ImportError:  # the same by the public functions
