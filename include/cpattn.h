@@ -441,7 +441,11 @@ cp_status cp_kv_extend(int32_t n_reqs, int32_t max_blocks, int32_t page_size, in
 /* Gives the pages of the requests with done[r] != 0 back: they are appended
  * to free_pages (request by request, in table order; what n_pool cannot hold
  * is dropped), their table entries become -1 and lens_out[r] = 0; the others
- * keep theirs.  block_table and free_pages change in place. */
+ * keep theirs.  A negative entry holds no page and is passed over, so pages in
+ * front of a window that the caller gave back to the pool before are marked
+ * by -1; every other entry has to be a page of this request alone (one that is
+ * in the pool already, or in another row too, would be handed out twice).
+ * block_table and free_pages change in place. */
 cp_status cp_kv_release(int32_t n_reqs, int32_t max_blocks, int32_t page_size, int32_t n_pool, const int32_t* lens,
                         const int32_t* done, int32_t* free_pages, const int32_t* n_free, int32_t* block_table,
                         int32_t* lens_out, int32_t* n_free_out, void* stream);

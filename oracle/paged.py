@@ -41,14 +41,15 @@ def extend(lens, add, table, free, n_free, page, max_rows):
 
 
 def release(lens, done, table, free, n_free, page):
-    """Returns (lens, n_free) and changes `table` and `free`."""
+    """Returns (lens, n_free) and changes `table` and `free`; entries below zero
+    hold no page."""
     lens_out = [int(x) for x in lens]
     n_free = min(max(int(n_free), 0), len(free))
     for r in range(len(lens)):
         if not done[r]:
             continue
         for j in range(min(-(-max(int(lens[r]), 0) // page), table.shape[1])):
-            if n_free < len(free):
+            if table[r, j] >= 0 and n_free < len(free):
                 free[n_free] = table[r, j]
                 n_free += 1
             table[r, j] = -1

@@ -817,3 +817,52 @@ sys.modules["torch._C._dynamo.guards"] = None
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     res = subprocess.run([sys.executable, "-c", script], cwd=root, capture_output=True, text=True, timeout=300)
     assert res.returncode == 0, res.stderr[-2000:]
+
+
+@pytest.mark.parametrize("room", [0, 40, 5000])
+def test_release_passes_over_pages_that_were_given_back(room):
+    # requests with a window: -1 in front (all of the table, some, none), a hole,
+    # more than 1024 pages in one request, the pool too small for all
+    page, width = 16, 1300
+    lens = np.array([20800, 0, 33, 400, 16 * 1100, 70, 1, 64])
+    rng = np.random.default_rng(70)
+    have = -(-lens // page)
+    table = np.full((len(lens), width), -7, dtype=np.int64)
+    ids = rng.permutation(int(have.sum()))
+    at = 0
+    for r, n in enumerate(have):
+        table[r, :n] = ids[at:at + n]
+        at += n
+    table[0, :1100] = -1
+    table[3, :have[3]] = -1
+    table[4, [0, 7, 1024, 1099]] = [-1, -5, -2 ** 31, -1]
+    done = np.array([1, 1, 0, 1, 1, 1, 0, 1])
+    pool, n_free = np.concatenate([[100001, 100002], np.full(room, -9)]), 2
+    t, f = dev(table), dev(pool)
+    want_t, want_f = table.copy(), pool.copy()
+    want = P.release(lens, done, want_t, want_f, n_free, page)
+    got = api.kv_release(page, t, dev(lens), dev(done), f, dev([n_free]))
+    assert np.array_equal(host(got[0]), want[0]) and int(got[1]) == want[1]
+    assert np.array_equal(host(t), want_t) and np.array_equal(host(f), want_f)
+    # what the pool then holds is exactly the pages of the requests that ended, each once
+    freed = sorted(x for r in np.nonzero(done)[0] for x in table[r, :have[r]] if x >= 0)
+    back = sorted(host(f)[n_free:want[1]])
+    assert min(back, default=0) >= 0 and len(back) == min(len(freed), room)
+    assert back == freed if room >= len(freed) else set(back) <= set(freed)
+
+
+def test_window_pages_given_back_are_granted_again():
+    # a request slides its window, the caller gives the pages in front back, the
+    # request ends, a new one takes all pages: each once, none missing
+    page, width, pages = 16, 8, 8
+    table, lens = torch.full((2, width), -1, **I32), torch.zeros(2, **I32)
+    free, n_free = torch.arange(pages, **I32), torch.full((1,), pages, **I32)
+    lens, _, _, _, n_free = api.kv_extend(page, table, lens, dev([100, 0]), free, n_free, 100)
+    gone = host(table)[0, :3]                        # the caller: three pages in front of the window
+    free[int(n_free):int(n_free) + 3] = dev(gone)
+    table[0, :3] = -1
+    n_free = n_free + 3
+    lens, n_free = api.kv_release(page, table, lens, dev([1, 0]), free, n_free)
+    assert int(n_free) == pages and sorted(host(free)) == list(range(pages))
+    lens, cu, slots, pos, n_free = api.kv_extend(page, table, lens, dev([0, 128]), free, n_free, 128)
+    assert int(n_free) == 0 and sorted(host(slots)) == list(range(128)) and sorted(host(table)[1]) == list(range(pages))

@@ -520,7 +520,8 @@ def kv_extend(page_size: int, block_table, lens, add, free_pages, n_free, max_ro
 
 def kv_release(page_size: int, block_table, lens, done, free_pages, n_free):
     """Gives the pages of the requests with done != 0 back (cp_kv_release);
-    block_table and free_pages change in place; returns (lens, n_free)."""
+    block_table and free_pages change in place; returns (lens, n_free).  Entries
+    below zero (pages given back before) are passed over."""
     n, width, pool, args, s = _tables(block_table, free_pages, n_free, lens=lens, done=done)
     lens_out, n_free_out = torch.empty_like(lens), torch.empty_like(n_free)
     _check(lib().cp_kv_release(n, width, page_size, pool, *args, lens_out.data_ptr(), n_free_out.data_ptr(), s),
