@@ -305,21 +305,21 @@ size_t cp_static_ws_capacity(void);
  * attention met a page number outside its cache, or CP_ERR_CUDA. */
 cp_status cp_get_device_error(void* stream);
 
-/* Failure-detection check: sets the cycle budget of the tcgen05 kernels'
- * main-loop waits (mbarrier and pacing waits) for launches made after this
- * call, process-wide.  cycles <= 0 restores the default of 4e9 cycles (about
- * two seconds); more than the default returns CP_ERR_INVALID_ARG.  While a
- * shorter budget is set, launches run a separately compiled copy of each
- * tcgen05 kernel (the default copies never read the budget, so the setting
- * costs nothing when unused) whose waits probe their barrier without
- * suspending and give up once `cycles` have passed: a budget of a few cycles
- * makes any wait that is not already complete run out.  The block then
- * raises its abort flag, its
- * other roles leave their loops, its TMA copies and MMAs are drained with the
- * default budget, TMEM is freed, and cp_get_device_error reports
- * CP_ERR_TIMEOUT (the outputs of that call are invalid).  The pages have no
- * counterpart ("04 · Megatron-LM 实现" §7.2 shows only the deadlock a missing
- * barrier participant causes).  Not for production use. */
+/* Failure-detection check: sets the cycle budget of the main-loop waits
+ * (mbarrier and pacing waits) of the tcgen05 kernels and of the paged
+ * attention for launches made after this call, process-wide.  cycles <= 0
+ * restores the default of 4e9 cycles (about two seconds); more than the default
+ * returns CP_ERR_INVALID_ARG.  While a shorter budget is set, launches run a
+ * separately compiled copy of each of these kernels (the default copies never
+ * read the budget, so the setting costs nothing when unused) whose waits probe
+ * their barrier without suspending and give up once `cycles` have passed: a
+ * budget of a few cycles makes any wait that is not already complete run out.
+ * The block then raises its abort flag, its other roles leave their loops, its
+ * TMA copies and MMAs are drained with the default budget, TMEM is freed, and
+ * cp_get_device_error reports CP_ERR_TIMEOUT (the outputs of that call are
+ * invalid).  The pages have no counterpart ("04 · Megatron-LM 实现" §7.2 shows
+ * only the deadlock a missing barrier participant causes).  Not for production
+ * use. */
 cp_status cp_debug_set_wait_limit(int64_t cycles);
 
 /* Host-only statistics of the task graph built for a descriptor (no GPU use):

@@ -629,6 +629,7 @@ struct SliceParams {
   int32_t box_shift;     // log2 keys of a box
   int32_t head_inner;    // the head dimension comes before the token dimension
   int32_t after_pair;
+  long long wait_limit;
 };
 
 __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int c0, int c1, int c2,
@@ -640,7 +641,9 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map
       : "memory");
 }
 
-template <typename S, int D, int R>
+// kShortWaits: the copy launched while cp_debug_set_wait_limit has set a
+// short wait budget; the default copy never reads the limit.
+template <typename S, int D, int R, bool kShortWaits>
 __global__ void __launch_bounds__(SliceLayout<S, D, R>::kThreads, 1)
     paged_slice_kernel(const __grid_constant__ SliceParams sp) {
   using T = typename S::T;
@@ -671,7 +674,7 @@ __global__ void __launch_bounds__(SliceLayout<S, D, R>::kThreads, 1)
   auto phase = [](int k) { return uint32_t(k / kPieces) & 1u; };
   // whole-warp bounded wait; false: some wait of the block gave up
   auto wait = [&](uint32_t bar, uint32_t parity) -> bool {
-    return __all_sync(0xffffffffu, tc::mbar_wait(bar, parity, &s_abort, a.err));
+    return __all_sync(0xffffffffu, tc::wait_bounded<kShortWaits>(bar, parity, &s_abort, a.err, sp.wait_limit));
   };
   if (sbase & 1023) {  // the swizzled layouts need a 1 KB aligned base
     if (tid == 0 && a.err) atomicCAS(a.err, 0, 2);
@@ -741,7 +744,8 @@ __global__ void __launch_bounds__(SliceLayout<S, D, R>::kThreads, 1)
     for (int k = 0; ok; ++k) {
       const PieceInfo& i = at.i;
       if (of_k) {
-        if (k >= kPieces && !wait(bar_joined(k), phase(k) ^ 1)) break;
+        ok = k < kPieces || wait(bar_joined(k), phase(k) ^ 1);
+        if (!ok) break;
         if (lane == 0) {
           s_piece[k % kPieces] = i;
           tc::mbar_arrive(bar_piece(k));
@@ -797,9 +801,12 @@ __global__ void __launch_bounds__(SliceLayout<S, D, R>::kThreads, 1)
       at = ahead;
       pages = ahead_pages;
     }
-    // Every copy has landed before the block ends (the workers wait for theirs
-    // unless a wait gave up).
-    if (!ok && lane == 0) {
+    // Every copy has landed before the block ends, whatever this warp left its
+    // loop for: the workers may have given up on the last stages.  (A slot's phase
+    // before its last one is complete: its stage was read.  Where the other
+    // producer stopped earlier the last phases stay open; then the default
+    // budget passes, which the copies do not take.)
+    if (lane == 0) {
       volatile int never = 0;
       for (uint32_t s = g > uint32_t(NS) ? g - NS : 0; s < g; ++s) tc::mbar_wait(bar_full(s), (s / NS) & 1, &never, nullptr);
     }
@@ -998,14 +1005,16 @@ __global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const __grid
 template <typename S, int D, int R>
 cp_status run_slice(const PagedArgs& a, bool after_pair, cudaStream_t s) {
   using L = SliceLayout<S, D, R>;
-  auto* kern = paged_slice_kernel<S, D, R>;
-  static std::atomic<bool> ready[64] = {};  // per device (an idempotent first set-up)
+  const long long limit = wait_limit_cycles();
+  const bool short_waits = limit < tc::kWaitCycles;
+  auto* kern = short_waits ? paged_slice_kernel<S, D, R, true> : paged_slice_kernel<S, D, R, false>;
+  static std::atomic<bool> ready[2][64] = {};  // per copy and device (an idempotent first set-up)
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return CP_ERR_CUDA;
-  if (!ready[dev].load(std::memory_order_acquire)) {
+  if (!ready[short_waits][dev].load(std::memory_order_acquire)) {
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kBytes) != cudaSuccess)
       return CP_ERR_CUDA;
-    ready[dev].store(true, std::memory_order_release);
+    ready[short_waits][dev].store(true, std::memory_order_release);
   }
   SliceParams p;
   const int page = 1 << a.page_shift, most = std::min(S::kStageKeys, kSliceUnit), box = std::min(page, most);
@@ -1015,6 +1024,7 @@ cp_status run_slice(const PagedArgs& a, bool after_pair, cudaStream_t s) {
   p.box_shift = 0;
   while ((1 << p.box_shift) < box) ++p.box_shift;
   p.after_pair = after_pair;
+  p.wait_limit = limit;
   return launch_early(kern, dim3(unsigned(a.grid)), dim3(L::kThreads), L::kBytes, after_pair, s, p);
 }
 
