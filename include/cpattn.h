@@ -542,7 +542,8 @@ cp_status cp_paged_attn_fwd(const cp_paged_desc* desc, int32_t n_reqs, int64_t r
  * blocks: block, request, kv-head, first packed row of the tile (token * group + head
  * in group, counted in the request), packed rows, first key and end of the
  * piece's keys, and the slot of its partial state (-1: the tile is whole and goes to
- * the outputs).  Pass null arrays to read the sizes first. */
+ * the outputs).  Pass null arrays to read the sizes first.  n_reqs >= 1; it
+ * refuses the sizes that cp_paged_attn_fwd refuses. */
 cp_status cp_paged_schedule(const cp_paged_desc* desc, int32_t n_reqs, int64_t rows, int32_t max_blocks,
                             const int32_t* cu_new, const int32_t* kv_lens, int32_t* grid, int64_t* n,
                             int32_t* pieces);

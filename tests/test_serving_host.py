@@ -253,3 +253,25 @@ def test_the_package_imports_without_cuda_in_pytorch():
     res = subprocess.run([sys.executable, "-c", WITHOUT_CUDA], cwd=root, capture_output=True, text=True, timeout=300,
                          env=dict(os.environ, CUDA_VISIBLE_DEVICES=""))
     assert res.returncode == 0 and res.stdout.strip() == "refused", res.stderr[-2000:]
+
+
+def test_the_division_refuses_what_the_attention_refuses():
+    p = _problem()
+    cu, lens = np.array([0, 1], dtype=np.int32), np.array([777], dtype=np.int32)
+
+    def schedule(rows=1, blocks=64, n=1, cu=cu, lens=lens):
+        grid, count = ctypes.c_int32(-1), ctypes.c_int64(-1)
+        at = [None if x is None else x.ctypes.data for x in (cu, lens)]
+        return api.lib().cp_paged_schedule(p._ref, n, rows, blocks, *at, ctypes.byref(grid), ctypes.byref(count), None)
+
+    assert schedule() == OK
+    assert schedule(n=0) == INVALID and schedule(rows=-1) == INVALID and schedule(blocks=0) == INVALID
+    assert schedule(cu=None) == INVALID and schedule(lens=None) == INVALID
+    # table widths and rows at the limits, past them, and where a 32-bit or a
+    # 64-bit product would wrap around to a small number
+    assert schedule(blocks=1 << 26) == OK
+    for blocks in ((1 << 26) + 1, 1 << 27, 1 << 28, 2 ** 31 - 1):
+        assert schedule(blocks=blocks) == UNSUP == _attn(p, blocks=blocks), blocks
+    assert schedule(rows=(1 << 29) - 257) == OK
+    for rows in ((1 << 29) - 256, 1 << 30, 1 << 31, 1 << 60, 1 << 62, 2 ** 63 - 1):
+        assert schedule(rows=rows) == UNSUP == _attn(p, rows=rows), rows

@@ -132,6 +132,14 @@ cp_status check_paged(const cp_paged_desc* d) {
   return CP_OK;
 }
 
+// Sizes of a call on a checked descriptor: packed rows (less a tile) and keys are 32-bit numbers.
+cp_status check_paged_sizes(const cp_paged_desc& d, int64_t rows, int32_t max_blocks) {
+  if (rows >= (int64_t(1) << 31) || rows * (d.heads_q / d.kv.heads_kv) >= (int64_t(1) << 31) - 1024 ||
+      int64_t(max_blocks) * d.kv.page_size > (int64_t(1) << 30))
+    return CP_ERR_UNSUPPORTED;
+  return CP_OK;
+}
+
 // Walks every block's share on the host.
 template <int U, int E, typename F>
 void walk_all(const PagedArgs& a, F f) {
@@ -380,9 +388,11 @@ size_t cp_paged_attn_workspace_bytes(const cp_paged_desc* desc) {
 cp_status cp_paged_schedule(const cp_paged_desc* desc, int32_t n_reqs, int64_t rows, int32_t max_blocks,
                             const int32_t* cu_new, const int32_t* kv_lens, int32_t* grid, int64_t* n,
                             int32_t* pieces) {
-  const cp_status st = check_paged(desc);
+  cp_status st = check_paged(desc);
   if (st != CP_OK) return st;
   if (n_reqs < 1 || rows < 0 || max_blocks < 1 || !cu_new || !kv_lens) return CP_ERR_INVALID_ARG;
+  st = check_paged_sizes(*desc, rows, max_blocks);
+  if (st != CP_OK) return st;
   const PagedPlan plan = pick_kernels(*desc, n_reqs);
   PagedArgs pair, slice;
   split_args(plan, paged_args(*desc, n_reqs, rows, max_blocks, cu_new, kv_lens), &pair, &slice);
@@ -407,13 +417,12 @@ cp_status cp_paged_schedule(const cp_paged_desc* desc, int32_t n_reqs, int64_t r
 cp_status cp_paged_attn_fwd(const cp_paged_desc* desc, int32_t n_reqs, int64_t rows, int32_t max_blocks,
                             const void* q, int64_t q_stride, const int32_t* block_table, const int32_t* cu_new,
                             const int32_t* kv_lens, void* o, float* lse, void* ws, size_t ws_bytes, void* stream) {
-  const cp_status st = check_paged(desc);
+  cp_status st = check_paged(desc);
   if (st != CP_OK) return st;
   if (n_reqs < 0 || rows < 0 || max_blocks < 1) return CP_ERR_INVALID_ARG;
   const cp_kv_cache& c = desc->kv;
-  if (rows * (desc->heads_q / c.heads_kv) >= (int64_t(1) << 31) - 1024 ||
-      int64_t(max_blocks) * c.page_size > (int64_t(1) << 30))
-    return CP_ERR_UNSUPPORTED;
+  st = check_paged_sizes(*desc, rows, max_blocks);
+  if (st != CP_OK) return st;
   if (n_reqs == 0 || rows == 0) return CP_OK;
   if (!q || !block_table || !cu_new || !kv_lens || !o || !lse || !ws || !aligned(ws, 256)) return CP_ERR_INVALID_ARG;
   if (q_stride < int64_t(desc->heads_q) * c.head_dim) return CP_ERR_INVALID_ARG;
