@@ -538,7 +538,8 @@ cp_status cp_paged_attn_fwd(const cp_paged_desc* desc, int32_t n_reqs, int64_t r
 
 /* Host only: how cp_paged_attn_fwd divides a call with these lengths (HOST
  * arrays cu_new [n_reqs + 1] and kv_lens [n_reqs]) over the *grid blocks of its
- * launch, for tests and tools.  pieces [*n][8] int32, in the order of the
+ * launches on the current device (without a device: as if every pair of 148 SMs could run
+ * a pair of blocks), for tests and tools.  pieces [*n][8] int32, in the order of the
  * blocks: block, request, kv-head, first packed row of the tile (token * group + head
  * in group, counted in the request), packed rows, first key and end of the
  * piece's keys, and the slot of its partial state (-1: the tile is whole and goes to

@@ -866,3 +866,32 @@ def test_window_pages_given_back_are_granted_again():
     assert int(n_free) == pages and sorted(host(free)) == list(range(pages))
     lens, cu, slots, pos, n_free = api.kv_extend(page, table, lens, dev([0, 128]), free, n_free, 128)
     assert int(n_free) == 0 and sorted(host(slots)) == list(range(128)) and sorted(host(table)[1]) == list(range(pages))
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("new,lens", [([700], [9000]), ([1, 300, 1, 90], [5000, 4000, 64, 900]), ([3, 1], [20, 9000])])
+def test_the_schedule_is_the_launches_division(d, new, lens):
+    # the states that the launches leave in the workspace are those of the pieces that
+    # the host's division cuts: the same slots, the same rows of each
+    hq, hkv, page = 8, 2, 16
+    kv, q, table, cu = paged_inputs(new, lens, hq, hkv, d, page, torch.bfloat16, seed=71)
+    p = api.PagedProblem(kv, hq, max_new=max(new))
+    pieces, grid = api.paged_schedule(p, cu, lens, int(cu[-1]), table.shape[1])
+    ws = api.paged_workspace(p)
+    ws.fill_(255)
+    api.paged_attn_fwd(p, q, dev(table), dev(cu), dev(lens), ws=ws)
+    pair, some = max(new) * hq // hkv > 32, len(new) > 1
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    R = (256 if pair else 16, 16)                              # packed rows of a state
+    blocks = (sms // 2 if pair else sms, sms if pair and some else 0)
+    states = sum(2 * n * r for n, r in zip(blocks, R))
+    part_l = ws.view(torch.int32)[states * d:states * (d + 1)]
+    wrote = host(part_l != -1).astype(bool)
+    first = grid - sms if pair and some else grid               # blocks of the pair launch, or of the only one
+    want = np.zeros(states, dtype=bool)
+    for block, r, h, row0, nrows, k0, k1, slot in pieces.tolist():
+        if slot < 0:
+            continue
+        at = slot * R[0] if block < first else 2 * blocks[0] * R[0] + (slot - 2 * first) * R[1]
+        want[at:at + nrows] = True
+    assert want.any() and np.array_equal(wrote, want)

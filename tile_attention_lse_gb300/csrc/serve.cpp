@@ -396,6 +396,11 @@ cp_status cp_paged_schedule(const cp_paged_desc* desc, int32_t n_reqs, int64_t r
   const PagedPlan plan = pick_kernels(*desc, n_reqs);
   PagedArgs pair, slice;
   split_args(plan, paged_args(*desc, n_reqs, rows, max_blocks, cu_new, kv_lens), &pair, &slice);
+  int32_t pairs = 0;
+  if (plan.use_pair && paged_pair_grid(desc->kv.head_dim, &pairs) == CP_OK)
+    pair.pairs = slice.pairs = pair.grid = pairs;  // what the launch takes on this device
+  else
+    cudaGetLastError();  // no device: half of the SMs
   if (grid) *grid = pair.grid + slice.grid;
   int64_t count = 0;
   int first = 0;
