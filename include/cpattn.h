@@ -474,8 +474,9 @@ typedef struct {
  * launch; q_stride, k_stride: elements between rows of the inputs (slices of
  * one projection), outputs contiguous.  inverse = 1 applies the transpose
  * R(pos)^T, which is the gradient.  A contiguous input may be its own output.
- * Angles are exact to 2^-64 turns before they are rounded to float32, for
- * every int32 position up to the rounding of base^-e to 53 bits.
+ * An angle is off by at most 2^-26 + 2^-32 + |position| 2^-53 turns for bases
+ * from 1 on (its rounding to float32, the bits below 2^-32 turns, and base^-e / 2 pi in 53
+ * bits): 1.1e-7 rad up to positions of 2^24, 1.6e-6 at 2^31.
  * Errors: CP_ERR_INVALID_ARG, CP_ERR_UNSUPPORTED (head_dim, n % 8 != 0),
  * CP_ERR_ALIGNMENT (a pointer or stride off 16 bytes). */
 cp_status cp_rope_axes(const cp_rope* rope, const int32_t* pos, int64_t rows, int32_t head_dim, cp_dtype dtype,

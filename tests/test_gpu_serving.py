@@ -895,3 +895,34 @@ def test_the_schedule_is_the_launches_division(d, new, lens):
         at = slot * R[0] if block < first else 2 * blocks[0] * R[0] + (slot - 2 * first) * R[1]
         want[at:at + nrows] = True
     assert want.any() and np.array_equal(wrote, want)
+
+
+def exact_turns(base, pairs, pos):
+    """Sine and cosine of pos base^(-i / pairs) for i < pairs, from 70 decimal digits."""
+    from decimal import Decimal, getcontext
+    getcontext().prec = 70
+    two_pi = 2 * Decimal("3.14159265358979323846264338327950288419716939937510582097494459230781640628620899863")
+    ln = Decimal(base).ln()
+    out = np.zeros((2, pairs))
+    for i in range(pairs):
+        x = (Decimal(int(pos)) * (-ln * i / pairs).exp()) % two_pi
+        x -= two_pi * (x / two_pi).to_integral_value()
+        term, sums = Decimal(1), [Decimal(0), Decimal(0)]
+        for n in range(60):                                     # x^59 / 59! < 1e-50 for |x| <= pi
+            sums[n % 2] += term if n % 4 < 2 else -term
+            term = term * x / (n + 1)
+        out[:, i] = float(sums[1]), float(sums[0])
+    return out
+
+
+@pytest.mark.parametrize("pos", [2 ** 31 - 1, -2 ** 31, 2 ** 30 + 12345, -987654321, 2 ** 24 + 1, 1000003, -131071, 17])
+@pytest.mark.parametrize("base", [10000.0, 500000.0, 1.0])
+def test_angles_are_as_exact_as_the_header_says(pos, base):
+    # a pair (1, 0) turns into its cosine and sine: off by the angle's error, 2^-26
+    # + 2^-32 + |pos| 2^-53 turns, and by one unit in the last place of sincospif
+    x = torch.zeros((1, 1, 128), device=DEV)
+    x[..., :64] = 1.0
+    y = f64(api.rope_axes(api.Rope([64], base=base), dev([pos]), x))[0, 0]
+    sine, cosine = exact_turns(int(base), 64, pos)
+    tol = 2 * np.pi * (2.0 ** -26 + 2.0 ** -32 + abs(pos) * 2.0 ** -53) + 2.0 ** -23
+    assert np.abs(y[:64] - cosine).max() <= tol and np.abs(y[64:] - sine).max() <= tol
