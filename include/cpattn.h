@@ -401,8 +401,8 @@ cp_status cp_ring_plan_tables(const cp_attn_desc* desc, int32_t which, int64_t* 
 /* The pages of a cache, for K and V alike: element i of head g of token t of
  * page n is at n * page_stride + t * token_stride + g * head_stride + i
  * (strides in elements, multiples of 16 bytes; head_dim contiguous), so that
- * [page][token][head] and [page][head][token] orders both fit, and so do K and
- * V side by side in one allocation.  Slot n * page_size + t names a token. */
+ * pages, tokens and heads may lie in any order, [page][token][head] and
+ * [page][head][token] among them, and K and V side by side in one allocation.  Slot n * page_size + t names a token. */
 typedef struct {
   void* k;
   void* v;

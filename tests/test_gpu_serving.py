@@ -926,3 +926,30 @@ def test_angles_are_as_exact_as_the_header_says(pos, base):
     sine, cosine = exact_turns(int(base), 64, pos)
     tol = 2 * np.pi * (2.0 ** -26 + 2.0 ** -32 + abs(pos) * 2.0 ** -53) + 2.0 ** -23
     assert np.abs(y[:64] - cosine).max() <= tol and np.abs(y[64:] - sine).max() <= tol
+
+
+@pytest.mark.parametrize("dtype,d", [(torch.bfloat16, 128), (torch.bfloat16, 64), (torch.float32, 64)])
+@pytest.mark.parametrize("order", [(1, 0, 2), (2, 0, 1), (2, 1, 0), (1, 2, 0), (0, 2, 1)])
+def test_pages_tokens_and_heads_in_any_order(order, dtype, d):
+    # order: the memory order of pages (0), tokens (1) and heads (2), outermost first
+    new, lens, hq, hkv, page = [1, 90, 2], [300, 200, 33], 8, 2, 32
+    kv, q, table, cu = paged_inputs(new, lens, hq, hkv, d, page, dtype, seed=72)
+    back = [order.index(i) for i in range(3)]
+    k, v = (x.permute(*order, 3).contiguous().permute(*back, 3) for x in (kv.k_cache, kv.v_cache))
+    other = api.PagedKV(k, v)
+    assert tuple(np.argsort([-s for s in k.stride()[:3]], kind="stable")) == order
+    # every token is written again through the slots
+    rows = sum(lens)
+    slots = np.concatenate([table[r][np.arange(n) // page] * page + np.arange(n) % page for r, n in enumerate(lens)])
+    at = torch.from_numpy(slots).to(DEV)
+    flat = [x.reshape(-1, hkv, d)[at].contiguous() for x in (kv.k_cache, kv.v_cache)]
+    other.k_cache.fill_(float("nan")), other.v_cache.fill_(float("nan"))
+    api.kv_append(other, dev(slots), *flat)
+    for a, b in ((other.k_cache, flat[0]), (other.v_cache, flat[1])):
+        assert torch.equal(a.reshape(-1, hkv, d)[at], b) and int(torch.isnan(a[..., 0]).sum()) == (a.shape[0] * page - rows) * hkv
+    for max_new in (90, 2):
+        args = (q, dev(table), dev(cu), dev(lens))
+        o, lse = api.paged_attn_fwd(api.PagedProblem(other, hq, max_new=max_new), *args)
+        check_attention(kv, q, table, cu, lens, o, lse)
+        want = api.paged_attn_fwd(api.PagedProblem(kv, hq, max_new=max_new), *args)
+        assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
