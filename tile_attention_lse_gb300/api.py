@@ -506,7 +506,8 @@ def kv_extend(page_size: int, block_table, lens, add, free_pages, n_free, max_ro
     """Pages, slots and positions for `add` new tokens of every request (cp_kv_extend).
 
     block_table [n_reqs, max_blocks] changes in place; returns (lens, cu_new,
-    slots, pos, n_free) as new tensors."""
+    slots, pos, n_free), views of one new allocation that lives as long as any
+    of them (clone what is kept for long)."""
     n, width, pool, args, s = _tables(block_table, free_pages, n_free, lens=lens, add=add)
     out = _empty_strided_cuda((2 * n + 2 + 2 * max_rows,), (1,), _I32)
     at = out.data_ptr()
@@ -559,7 +560,8 @@ def rope_axes(rope: Rope, pos, q, k=None, inverse: bool = False, q_out=None, k_o
 def kv_append(kv: PagedKV, slots, k, v, rope: Rope | None = None, pos=None, q=None, q_out=None):
     """Writes k and v [rows, heads_kv, head_dim] into the slots of the cache
     (cp_kv_append); with rope, k is rotated by pos on the way and q into the
-    returned q_out."""
+    returned q_out.  Rows whose slot is outside the cache (a padded batch's) are
+    left out: their q_out rows stay as they were, unset in a new q_out."""
     dev, dt, heads, d = kv._index, kv.dtype, kv.heads_kv, kv.head_dim
     rows = k.shape[0]
     ks, vs = _rows(k, "k", heads, d, dt, dev), _rows(v, "v", heads, d, dt, dev)

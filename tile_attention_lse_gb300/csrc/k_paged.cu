@@ -50,10 +50,6 @@ namespace cpattn {
 
 namespace {
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool read) {
-  const int n = read ? 16 : 0;
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
-}
 template <int N>
 __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");

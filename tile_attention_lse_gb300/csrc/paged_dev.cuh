@@ -1,4 +1,5 @@
-// Device side of the paged attention's work division: where a unit lies.
+// Device side of the paged attention's work division (where a unit lies), and
+// what its kernels share.
 #pragma once
 
 #include <type_traits>
@@ -125,6 +126,11 @@ __device__ __forceinline__ PagedShare paged_locate(const PagedArgs& a, int64_t* 
   }
   __syncthreads();
   return share;
+}
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool read) {
+  const int n = read ? 16 : 0;
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
 }
 
 // The merge kernel may start early; it waits for its predecessor here.

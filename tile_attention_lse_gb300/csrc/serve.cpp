@@ -227,8 +227,11 @@ void split_args(const PagedPlan& p, const PagedArgs& a, PagedArgs* pair, PagedAr
     slice->other_R = pair->R;
     pair->pairs = slice->pairs = pair->grid;
     pair->blocks = slice->blocks = slice->grid;
-    // A slice unit's time on one SM by its boxes (32 KB at 85 GB/s from pages
-    // of 64 on, 53 at 16), a pair unit's on two: measured on batches of both.
+    // What gave the shortest times on batches of both, by page size: a slice
+    // unit's time on one SM (64 keys of K and V, at head_dim 128 32 KB: 480 ns are
+    // 68 GB/s) and twice a pair unit's on its two, for both head_dims alike as the softmax
+    // bounds it (alone, 1024 tokens over 8192 to 40960: 1.54 us at head_dim 64 and
+    // 1.71 at 128 in pages of 64, 2.11 and 2.10 in pages of 8, whose boxes bound it).
     const bool wide = a.d == 128;
     const int page = 1 << a.page_shift;
     pair->pair_cost = slice->pair_cost = page == 8 ? 2400 : 1800;
