@@ -953,3 +953,76 @@ def test_pages_tokens_and_heads_in_any_order(order, dtype, d):
         check_attention(kv, q, table, cu, lens, o, lse)
         want = api.paged_attn_fwd(api.PagedProblem(kv, hq, max_new=max_new), *args)
         assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
+
+
+@pytest.mark.parametrize("dtype,max_new", [(torch.bfloat16, 3), (torch.bfloat16, 64), (torch.float32, 3)])
+def test_lengths_outside_the_table_and_the_rows_are_clamped(dtype, max_new):
+    # the same bits as a call with the clamped lengths: a request longer than its
+    # table, one of negative length, offsets in front of and behind the rows of q
+    lens, page = [48, 48, 48], 16
+    kv, q, table, _ = paged_inputs([0, 0, 0], lens, 4, 2, 128, page, dtype, seed=73, tail=9)
+    table = table[:, :3]                                     # 48 keys of each
+    p = api.PagedProblem(kv, 4, max_new=max_new)
+    for cu, n, cu_c, n_c in (([-3, 2, 99, 120], [1000, -5, 7], [0, 2, 9, 9], [48, 0, 7]),
+                             ([0, 0, -4, 6], [48, 2 ** 31 - 1, 2 ** 31 - 1], [0, 0, 0, 6], [48, 48, 48]),
+                             ([4, 9, 9, 9], [-2 ** 31, 3, 1], [4, 9, 9, 9], [0, 3, 1])):
+        got, want = [], []
+        for c, x, out in ((cu, n, got), (cu_c, n_c, want)):
+            o, lse = torch.full(q.shape, 7.0, dtype=dtype, device=DEV), torch.full(q.shape[:2], 7.0, device=DEV)
+            out += api.paged_attn_fwd(p, q, dev(table), dev(c), dev(x), out=o, lse=lse)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+        inside = np.zeros(q.shape[0], dtype=bool)
+        inside[cu_c[0]:cu_c[-1]] = True
+        assert np.array_equal(host((got[1] != 7).all(1)), inside) and np.array_equal(host((got[1] == 7).all(1)), ~inside)
+        check = [r for r in range(3) if cu_c[r + 1] > cu_c[r]]
+        for r in check:
+            rows = slice(cu_c[r], cu_c[r + 1])
+            check_attention(kv, q[rows], table[r:r + 1], [0, cu_c[r + 1] - cu_c[r]], n_c[r:r + 1], got[0][rows], got[1][rows])
+
+
+def test_tables_append_and_release_on_another_stream_captured():
+    # every table call in one graph on a stream of its own, replayed until the pool has been through twice;
+    # q is rotated in place
+    page, n, width, pages, rows = 16, 4, 4, 10, 20
+    kv = make_cache(pages, page, 2, 64, torch.float32, "token", fill=0.0)
+    rope = api.Rope([8, 24], interleaved=True)
+    table, lens, free = torch.full((n, width), -1, **I32), torch.zeros(n, **I32), torch.arange(pages, **I32)
+    add, done, n_free = torch.zeros(n, **I32), torch.zeros(n, **I32), torch.full((1,), pages, **I32)
+    x = torch.randn((rows, 4, 64), generator=torch.Generator().manual_seed(74)).to(DEV)
+    q = torch.zeros((rows, 2, 64), device=DEV)
+
+    def step():
+        lens2, cu, slots, pos, free2 = api.kv_extend(page, table, lens, add, free, n_free, rows)
+        api.kv_append(kv, slots, x[:, :2], x[:, 2:], rope=rope, pos=torch.stack([pos, pos // 3]), q=q, q_out=q)
+        lens3, free3 = api.kv_release(page, table, lens2, done, free, free2)
+        lens.copy_(lens3)
+        n_free.copy_(free3)
+        return slots, pos
+
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        step()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=s):
+            slots, pos = step()
+    torch.cuda.current_stream().wait_stream(s)
+    t_h, l_h, f_h, nf_h = np.full((n, width), -1), np.zeros(n, dtype=np.int64), np.arange(pages), pages
+    rng = np.random.default_rng(75)
+    for i in range(12):
+        adds, ends = rng.integers(0, 9, n), (rng.random(n) < 0.4).astype(np.int64)
+        add.copy_(dev(adds))
+        done.copy_(dev(ends))
+        q.copy_(x[:, :2])
+        graph.replay()
+        l_h, _, want_s, want_p, nf_h = P.extend(l_h, adds, t_h, f_h, nf_h, page, rows)
+        l_h, nf_h = P.release(l_h, ends, t_h, f_h, nf_h, page)
+        assert np.array_equal(host(slots), want_s) and np.array_equal(host(pos), want_p)
+        assert np.array_equal(host(table), t_h) and np.array_equal(host(free), f_h) and int(n_free) == nf_h
+        there = want_s >= 0
+        want = P.rope_axes(f64(x[:, :2]), np.stack([want_p, want_p // 3]), [8, 24], interleaved=True)
+        tol = 12 * float(x.abs().max()) * U32 + U32 * 1.5 * float(x.abs().max())
+        assert np.abs(f64(q) - want)[there].max(initial=0.0) <= tol
+        assert torch.equal(q[dev(~there, torch.bool)], x[:, :2][dev(~there, torch.bool)])    # rows without a slot stay
+        flat = f64(kv.k_cache).reshape(-1, 2, 64)
+        assert np.abs(flat[want_s[there]] - want[there]).max(initial=0.0) <= tol
