@@ -550,6 +550,102 @@ cp_status cp_paged_schedule(const cp_paged_desc* desc, int32_t n_reqs, int64_t r
                             const int32_t* cu_new, const int32_t* kv_lens, int32_t* grid, int64_t* n,
                             int32_t* pieces);
 
+/* ------------------------------------------------------------------------
+ * Cross attention: packed query sequences attend over packed key sequences of
+ * other lengths (a decoder over its encoder's states; with equal lengths self
+ * attention), with an optional bias of the relative position and optional dropout,
+ * forward and backward.  Lengths live in device memory and are read there: no call waits for
+ * the host, and each can be captured into a CUDA graph and replayed on new lengths,
+ * biases and random numbers.
+ *
+ * Sequence b has the nq queries in rows cu_q[b] .. cu_q[b + 1] - 1 of q (with len_q
+ * the first len_q[b] of them only) and the nk keys in rows cu_k[b] .. cu_k[b + 1] - 1
+ * of k and v (with len_k the first len_k[b] only: a padded batch).  cu_q and
+ * cu_k do not decrease; what lies outside the tensors is left out.
+ *  score  s_ij = softmax_scale q_i . k_j [+ bias[bucket(j - (i + nk - nq))][h]];
+ *  mask   causal: j <= i + nk - nq, so that the ends are aligned (new queries
+ *         behind cached keys); else every query sees all nk keys;
+ *  P      = exp(s - lse), lse_i = log sum_j exp s_ij; a row that sees no key has o = 0, lse = -inf;
+ *  o_i    = sum_j P_ij keep_ij / (1 - p) v_j.
+ * Grouped heads as everywhere: q-head h reads kv-head h / (heads_q / heads_kv).
+ *
+ * Buckets of a relative position x = j - (i + nk - nq): rel_both = 0 counts the
+ * distance n = max(-x, 0) in `per` = rel_buckets buckets; rel_both = 1 the distance n = |x| in
+ * per = rel_buckets / 2, with the keys behind the query (x > 0) in the second half.  With
+ * e = per / 2, distances below e have a bucket each, and bucket e + t starts at the distance
+ * ceil(e (rel_max_distance / e)^(t / (per - e)) (1 - 1e-12)), t = 0 .. per - e - 1
+ * (floating point; the last factor puts a distance that lies on a border behind it).
+ * Table entries below -1e30 mask their pairs (a row of only such sees no key, and
+ * their gradient is 0); the others are finite.
+ *
+ * Dropout: keep_ij comes from Philox4x32 with 7 rounds (Salmon et al., 2011), drawn
+ * again wherever it is needed and never stored: counter words (j / 8, i,
+ * b * heads_q + h, low half of rng[1]), key rng[0] (low half first); of the four words of a draw,
+ * element e = j % 8 takes the low 15 bits of half e % 2 (0: low) of word e / 2, and is
+ * kept iff that number >= round(dropout * 2^15).  1 - p is taken after
+ * that rounding.  rng [2] (seed, offset) lies in device memory; the backward takes the same two numbers.
+ * ------------------------------------------------------------------------ */
+typedef struct {
+  int32_t heads_q;
+  int32_t heads_kv;        /* divides heads_q                                  */
+  int32_t head_dim;        /* 64 or 128                                        */
+  cp_dtype dtype;          /* of q, k, v, o, their gradients and the bias table */
+  int32_t causal;
+  int32_t max_q;           /* about how many queries a sequence has at most:
+                              chooses the forward's kernel, any number is computed right; 0: many */
+  int32_t rel_buckets;     /* 0: no bias; up to 64, even with rel_both, 2 or more a direction */
+  int32_t rel_max_distance; /* where the last bucket begins at the latest: half of a
+                              direction's buckets to 65536                     */
+  int32_t rel_both;        /* keys behind the query have buckets of their own  */
+  float dropout;           /* 0 <= p < 1; 0: none, rng is not read             */
+  float softmax_scale;     /* 0 -> 1/sqrt(head_dim)                            */
+} cp_cross_desc;
+
+/* Host-only check of a descriptor (the errors that the calls below return). */
+cp_status cp_validate_cross_desc(const cp_cross_desc* desc);
+
+/* Bytes of workspace of cp_cross_attn_fwd (backward = 0), or of both calls
+ * (backward = 1), whatever the lengths.  0 if the arguments are invalid.  256-byte aligned;
+ * contents need no initialisation and are clobbered. */
+size_t cp_cross_attn_workspace_bytes(const cp_cross_desc* desc, int32_t n_seqs, int64_t rows_q, int64_t rows_k,
+                                     int32_t backward);
+
+/* Forward: o [rows_q][heads_q][head_dim], lse [rows_q][heads_q] float32, natural log (as cp_tile_attn_fwd gives
+ * them, and without dropout fit to be merged by cp_merge_partials).  q [rows_q][heads_q][head_dim], k and v
+ * [rows_k][heads_kv][head_dim] with row strides in elements (slices of one projection).  bias
+ * [rel_buckets][heads_q] (NULL iff rel_buckets is 0).  rest (bf16 with a bias only, layout of o; NULL: not wanted): what o
+ * lost to its rounding, o + rest being the output to 2^-17; cp_cross_attn_bwd needs it for an exact gradient of
+ * the table.  Rows that no sequence owns are not read, and
+ * left as they were in o, rest and lse.  o and lse must not overlap the inputs.  A K/V value that is not finite reaches
+ * every row of its sequence whose tile of keys holds it, as in the other attention calls, but no
+ * other sequence.  A row with a NaN score has NaN in o and lse.  Results do not depend on
+ * timing: the same call gives the same bits.  Calls that share a workspace must not overlap on the GPU.
+ * Errors: CP_ERR_INVALID_ARG, CP_ERR_UNSUPPORTED (sizes, heads; dropout in bf16 with more than 128 q-heads
+ * a kv-head), CP_ERR_ALIGNMENT (a pointer or stride off 16 bytes), CP_ERR_WORKSPACE. */
+cp_status cp_cross_attn_fwd(const cp_cross_desc* desc, int32_t n_seqs, int64_t rows_q, int64_t rows_k, const void* q,
+                            int64_t q_stride, const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                            const int32_t* cu_q, const int32_t* cu_k, const int32_t* len_q, const int32_t* len_k,
+                            const void* bias, const uint64_t* rng, void* o, void* rest, float* lse, void* ws,
+                            size_t ws_bytes, void* stream);
+
+/* Backward: with dS_ij = P_ij (keep_ij / (1 - p) dO_i . v_j - dO_i . o_i),
+ *   dq_i = softmax_scale sum_j dS_ij k_j,  dk_j = softmax_scale sum_i dS_ij q_i,  dv_j = sum_i P_ij keep_ij / (1 - p) dO_i,
+ *   dbias[b][h] = sum of dS_ij over the pairs of bucket b, all sequences,
+ * grouped heads summed into their kv-head.  o, rest and lse are the forward's for the same inputs and rng; without rest
+ * (bf16) dbias has the error that the rounding of o makes in dO . o, up to 2^-9 of the sum over each bucket of P |dO| |o|.
+ * dout has the layout of q (row stride in elements).
+ * dq, dk and dv [rows][heads][head_dim] are contiguous; rows that no sequence owns (and keys that no query
+ * sees) get zeros.  dbias [rel_buckets][heads_q], given iff bias is.  The outputs must not overlap the inputs.
+ * In bf16 the dq contributions of the key tiles are added in float32 by hardware reductions whose order is not
+ * fixed, so dq may differ in the last bits between calls; all other sums have a fixed order.  ws: as for the
+ * forward, with backward = 1.  Errors: as for the forward. */
+cp_status cp_cross_attn_bwd(const cp_cross_desc* desc, int32_t n_seqs, int64_t rows_q, int64_t rows_k, const void* q,
+                            int64_t q_stride, const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                            const void* o, const void* rest, const float* lse, const void* dout, int64_t dout_stride,
+                            const int32_t* cu_q, const int32_t* cu_k, const int32_t* len_q, const int32_t* len_k,
+                            const void* bias, const uint64_t* rng, void* dq, void* dk, void* dv, void* dbias, void* ws,
+                            size_t ws_bytes, void* stream);
+
 /* Kernel classes reported by cp_profile_read. */
 typedef enum {
   CP_K_PARTITION = 0, /* partition index kernel                          */
@@ -565,7 +661,12 @@ typedef enum {
   CP_K_HEAD_ROWS = 10, /* multi-axis rotation, rows into a paged cache   */
   CP_K_PAGED = 11,    /* attention over a paged cache                    */
   CP_K_PAGED_MERGE = 12, /* join of its cut tiles                        */
-  CP_K_COUNT = 13
+  CP_K_CROSS = 13,       /* cross attention forward                      */
+  CP_K_CROSS_MERGE = 14, /* join of its cut tiles                        */
+  CP_K_CROSS_PREP = 15,  /* its bias spread, its backward's preparation  */
+  CP_K_CROSS_BWD = 16,   /* cross attention backward                     */
+  CP_K_CROSS_POST = 17,  /* its sums and conversions                     */
+  CP_K_COUNT = 18
 } cp_kernel_class;
 
 /* Benchmark instrumentation (no effect on results).  With timing on, every

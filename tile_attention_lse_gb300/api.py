@@ -32,9 +32,11 @@ EXPORTS = ("cp_status_string", "cp_validate_desc", "cp_partition_indices", "cp_p
            "cp_static_ws_capacity", "cp_ring_bwd_schedule", "cp_permute_rope", "cp_hybrid_schedule",
            "cp_ring_plan_tables", "cp_token_seq_pos", "cp_debug_set_wait_limit",
            "cp_kv_extend", "cp_kv_release", "cp_rope_axes", "cp_kv_append", "cp_validate_paged_desc",
-           "cp_paged_attn_workspace_bytes", "cp_paged_attn_fwd", "cp_paged_schedule")
+           "cp_paged_attn_workspace_bytes", "cp_paged_attn_fwd", "cp_paged_schedule",
+           "cp_validate_cross_desc", "cp_cross_attn_workspace_bytes", "cp_cross_attn_fwd", "cp_cross_attn_bwd")
 KERNEL_CLASSES = ("partition", "permute", "tile_fwd", "merge", "delta", "tile_bwd", "convert", "tables", "rope",
-                  "kv_tables", "head_rows", "paged", "paged_merge")
+                  "kv_tables", "head_rows", "paged", "paged_merge", "cross", "cross_merge", "cross_prep", "cross_bwd",
+                  "cross_post")
 
 
 class CpError(RuntimeError):
@@ -104,6 +106,22 @@ class CpPagedDesc(ctypes.Structure):
     ]
 
 
+class CpCrossDesc(ctypes.Structure):
+    _fields_ = [
+        ("heads_q", ctypes.c_int32),
+        ("heads_kv", ctypes.c_int32),
+        ("head_dim", ctypes.c_int32),
+        ("dtype", ctypes.c_int32),
+        ("causal", ctypes.c_int32),
+        ("max_q", ctypes.c_int32),
+        ("rel_buckets", ctypes.c_int32),
+        ("rel_max_distance", ctypes.c_int32),
+        ("rel_both", ctypes.c_int32),
+        ("dropout", ctypes.c_float),
+        ("softmax_scale", ctypes.c_float),
+    ]
+
+
 _lib = None
 
 
@@ -148,6 +166,12 @@ def lib():
             "cp_paged_schedule": ([ctypes.POINTER(CpPagedDesc), I32, I64, I32, P, P, P, P, P], I32),
             "cp_paged_attn_workspace_bytes": ([ctypes.POINTER(CpPagedDesc)], SZ),
             "cp_paged_attn_fwd": ([ctypes.POINTER(CpPagedDesc), I32, I64, I32, P, I64, P, P, P, P, P, P, SZ, P], I32),
+            "cp_validate_cross_desc": ([ctypes.POINTER(CpCrossDesc)], I32),
+            "cp_cross_attn_workspace_bytes": ([ctypes.POINTER(CpCrossDesc), I32, I64, I64, I32], SZ),
+            "cp_cross_attn_fwd": ([ctypes.POINTER(CpCrossDesc), I32, I64, I64, P, I64, P, I64, P, I64] + [P] * 10 + [SZ, P],
+                                  I32),
+            "cp_cross_attn_bwd": ([ctypes.POINTER(CpCrossDesc), I32, I64, I64, P, I64, P, I64, P, I64, P, P, P, P, I64]
+                                  + [P] * 11 + [SZ, P], I32),
         }
         for name, (args, res) in sig.items():
             fn = getattr(L, name)
@@ -637,6 +661,138 @@ def paged_attn_fwd(p: PagedProblem, q, block_table, cu_new, kv_lens, ws: torch.T
     _check(lib().cp_paged_attn_fwd(p._ref, n, rows, width, q.data_ptr(), qs, table, cu, lens, out.data_ptr(),
                                    lse.data_ptr(), ws.data_ptr(), ws.nbytes, s), "cp_paged_attn_fwd")
     return out, lse
+
+
+# -------------------------------------------------------- cross attention ---
+class RelBuckets:
+    """Buckets of the relative position (cp_cross_desc): `buckets` of them, the
+    last one from at most `max_distance` on; both: keys behind the query have
+    half of them for themselves."""
+
+    def __init__(self, buckets: int, max_distance: int = 128, both: bool = True):
+        self.buckets, self.max_distance, self.both = int(buckets), int(max_distance), bool(both)
+
+
+class CrossProblem:
+    """Attention of packed query sequences over packed key sequences (cp_cross_desc).
+
+    max_q: about how many queries a sequence has at most (chooses the forward's
+    kernel; 0: many); rel: a bias by buckets of the relative position; dropout: of the probabilities."""
+
+    def __init__(self, heads_q: int, heads_kv: int, head_dim: int, dtype: torch.dtype = torch.bfloat16,
+                 causal: bool = False, max_q: int = 0, rel: RelBuckets | None = None, dropout: float = 0.0,
+                 softmax_scale: float = 0.0):
+        self.heads_q, self.heads_kv, self.head_dim, self.dtype = int(heads_q), int(heads_kv), int(head_dim), dtype
+        self.rel, self.dropout = rel, float(dropout)
+        r = (rel.buckets, rel.max_distance, int(rel.both)) if rel is not None else (0, 0, 0)
+        self._desc = CpCrossDesc(self.heads_q, self.heads_kv, self.head_dim, _dtype_code(dtype), int(bool(causal)),
+                                 int(max_q), *r, self.dropout, float(softmax_scale))
+        self._ref = ctypes.byref(self._desc)
+
+
+def validate_cross(p: CrossProblem) -> int:
+    return int(lib().cp_validate_cross_desc(p._ref))
+
+
+def cross_workspace_bytes(p: CrossProblem, n_seqs: int, rows_q: int, rows_k: int, backward: bool = False) -> int:
+    return int(lib().cp_cross_attn_workspace_bytes(p._ref, n_seqs, rows_q, rows_k, int(backward)))
+
+
+def cross_workspace(p: CrossProblem, n_seqs: int, rows_q: int, rows_k: int, backward: bool = False,
+                    device="cuda") -> torch.Tensor:
+    """A workspace for cross_attn_fwd, and with backward for cross_attn_bwd too."""
+    n = cross_workspace_bytes(p, n_seqs, rows_q, rows_k, backward)
+    if n == 0:
+        raise CpError(validate_cross(p) or -1, "cp_cross_attn_workspace_bytes")
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def _cross_inputs(p: CrossProblem, q, k, v, cu_q, cu_k, len_q, len_k, bias, rng):
+    """Device index, sizes and leading arguments of both directions (checks included)."""
+    dev, d, dt = q.get_device(), p.head_dim, p.dtype
+    qs = _rows(q, "q", p.heads_q, d, dt, dev)
+    ks, vs = _rows(k, "k", p.heads_kv, d, dt, dev), _rows(v, "v", p.heads_kv, d, dt, dev)
+    rows_q, rows_k = q.shape[0], k.shape[0]
+    if v.shape[0] != rows_k:
+        raise ValueError("k and v have the same rows")
+    n = cu_q.numel() - 1
+    if n < 0:
+        raise ValueError("cu_q is [n_seqs + 1]")
+    cu = (_ints(cu_q, "cu_q", (n + 1,), dev), _ints(cu_k, "cu_k", (n + 1,), dev))
+    lens = tuple(None if x is None else _ints(x, what, (n,), dev) for x, what in ((len_q, "len_q"), (len_k, "len_k")))
+    if (p.rel is None) != (bias is None):
+        raise ValueError("a bias table comes with the problem's rel, and the other way round")
+    if bias is not None:
+        shape = (p.rel.buckets, p.heads_q)
+        if bias.shape != shape or bias.dtype is not dt or bias.get_device() != dev or not bias.is_contiguous():
+            raise ValueError(f"bias is a contiguous {list(shape)} {dt} tensor on cuda:{dev}")
+        bias = bias.data_ptr()
+    if p.dropout > 0.0:
+        if rng is None or rng.dtype is not torch.int64 or rng.shape != (2,) or rng.get_device() != dev \
+                or not rng.is_contiguous():
+            raise ValueError(f"dropout takes rng, a contiguous [2] int64 tensor (seed, offset) on cuda:{dev}")
+        rng = rng.data_ptr()
+    else:
+        rng = None
+    return dev, n, rows_q, rows_k, (q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs), cu + lens, bias, rng
+
+
+def _cross_ws(p, ws, n, rows_q, rows_k, backward, dev):
+    if ws is None:
+        return cross_workspace(p, n, rows_q, rows_k, backward, torch.device("cuda", dev))
+    if ws.get_device() != dev or not ws.is_contiguous():
+        raise ValueError(f"ws is a contiguous tensor on cuda:{dev}")
+    return ws
+
+
+def cross_attn_fwd(p: CrossProblem, q, k, v, cu_q, cu_k, len_q=None, len_k=None, bias=None, rng=None,
+                   for_backward: bool = False, ws: torch.Tensor | None = None, out=None, lse=None):
+    """Attention of q [rows_q, heads_q, head_dim] over k and v [rows_k, heads_kv, head_dim],
+    sequence by sequence (cp_cross_attn_fwd) -> (o, lse).  Rows that no sequence owns are
+    left as they were (unset in a new o and lse).  for_backward: -> (o, lse, rest), rest what o lost
+    to its rounding (bf16 with a bias; None elsewhere), which cross_attn_bwd takes."""
+    dev, n, rows_q, rows_k, qkv, cu, bias, rng = _cross_inputs(p, q, k, v, cu_q, cu_k, len_q, len_k, bias, rng)
+    s = _stream_of(dev)
+    ws = _cross_ws(p, ws, n, rows_q, rows_k, False, dev)
+    heads, d = p.heads_q, p.head_dim
+    out = _new(out, "out", (rows_q, heads, d), p.dtype, dev)
+    lse = _new(lse, "lse", (rows_q, heads), _F32, dev)
+    rest = None
+    if for_backward and bias is not None and p.dtype is torch.bfloat16:
+        rest = _new(None, "rest", (rows_q, heads, d), p.dtype, dev)
+    _check(lib().cp_cross_attn_fwd(p._ref, n, rows_q, rows_k, *qkv, *cu, bias, rng, out.data_ptr(),
+                                   None if rest is None else rest.data_ptr(), lse.data_ptr(), ws.data_ptr(), ws.nbytes, s),
+           "cp_cross_attn_fwd")
+    return (out, lse, rest) if for_backward else (out, lse)
+
+
+def cross_attn_bwd(p: CrossProblem, q, k, v, o, lse, dout, cu_q, cu_k, len_q=None, len_k=None, bias=None, rng=None,
+                   rest=None, ws: torch.Tensor | None = None, dq=None, dk=None, dv=None, dbias=None):
+    """Gradients (cp_cross_attn_bwd) -> (dq, dk, dv, dbias); dbias is None without a bias.
+    o, lse and rest are cross_attn_fwd's for the same inputs and rng.  Rows that no
+    sequence owns get zeros."""
+    dev, n, rows_q, rows_k, qkv, cu, bias, rng = _cross_inputs(p, q, k, v, cu_q, cu_k, len_q, len_k, bias, rng)
+    s = _stream_of(dev)
+    ws = _cross_ws(p, ws, n, rows_q, rows_k, True, dev)
+    heads, d, dt = p.heads_q, p.head_dim, p.dtype
+    ds = _rows(dout, "dout", heads, d, dt, dev)
+    if dout.shape[0] != rows_q:
+        raise ValueError("dout has q's rows")
+    for x, what, shape, t in ((o, "o", (rows_q, heads, d), dt), (lse, "lse", (rows_q, heads), _F32)) \
+            + (() if rest is None else ((rest, "rest", (rows_q, heads, d), dt),)):
+        if x.shape != shape or x.dtype is not t or x.get_device() != dev or not x.is_contiguous():
+            raise ValueError(f"{what} is a contiguous {list(shape)} {t} tensor on cuda:{dev}")
+    dq = _new(dq, "dq", (rows_q, heads, d), dt, dev)
+    dk, dv = (_new(x, what, (rows_k, p.heads_kv, d), dt, dev) for x, what in ((dk, "dk"), (dv, "dv")))
+    if bias is not None:
+        dbias = _new(dbias, "dbias", (p.rel.buckets, heads), dt, dev)
+    elif dbias is not None:
+        raise ValueError("dbias comes with a bias")
+    _check(lib().cp_cross_attn_bwd(p._ref, n, rows_q, rows_k, *qkv, o.data_ptr(), None if rest is None else rest.data_ptr(),
+                                   lse.data_ptr(), dout.data_ptr(), ds, *cu, bias, rng, dq.data_ptr(), dk.data_ptr(),
+                                   dv.data_ptr(), None if dbias is None else dbias.data_ptr(), ws.data_ptr(), ws.nbytes, s),
+           "cp_cross_attn_bwd")
+    return dq, dk, dv, dbias
 
 
 def device_error() -> int:

@@ -21,6 +21,7 @@
 namespace cpattn {
 
 struct PagedArgs {
+  static constexpr bool kDense = false, kBias = false, kDrop = false;
   const void* q;  // [rows][H][d], q_stride elements between rows
   int64_t q_stride;
   const void* k;  // pages: element (page, token, head, i) at page * page_stride + ...
@@ -96,12 +97,13 @@ struct PagedTile {
   int32_t row0, nrows, b0, n, lo, hi;
 };
 
-CPATTN_HD int32_t paged_tiles(const PagedArgs& a, const PagedReq& q) {
+template <class A>
+CPATTN_HD int32_t paged_tiles(const A& a, const PagedReq& q) {
   return paged_quot(uint32_t(q.nq) * uint32_t(a.G) + uint32_t(a.R) - 1, uint32_t(a.R), a.r_inv);  // rows * G < 2^31 - R
 }
 
-template <int U>
-CPATTN_HD PagedTile paged_tile(const PagedArgs& a, const PagedReq& q, int t) {
+template <int U, class A>
+CPATTN_HD PagedTile paged_tile(const A& a, const PagedReq& q, int t) {
   PagedTile x;
   x.row0 = t * a.R;
   const int32_t left = q.nq * a.G - x.row0;
@@ -117,8 +119,8 @@ CPATTN_HD PagedTile paged_tile(const PagedArgs& a, const PagedReq& q, int t) {
 }
 
 // Units of one kv-head of a request.
-template <int U, int E>
-CPATTN_HD int64_t paged_req_units(const PagedArgs& a, const PagedReq& q) {
+template <int U, int E, class A>
+CPATTN_HD int64_t paged_req_units(const A& a, const PagedReq& q) {
   const int nt = paged_tiles(a, q);
   int64_t s = 0;
   for (int t = 0; t < nt; ++t) s += paged_tile<U>(a, q, t).n + E;
@@ -159,8 +161,9 @@ CPATTN_HD int paged_blocks(const PagedArgs& a, bool pair, int64_t mine, int64_t 
   return pair ? k : a.blocks - 2 * k;
 }
 // The other launch's view of the requests.
-CPATTN_HD PagedArgs paged_other(const PagedArgs& a) {
-  PagedArgs o = a;
+template <class A>
+CPATTN_HD A paged_other(const A& a) {
+  A o = a;
   o.R = a.other_R;
   o.r_inv = a.other_r_inv;
   o.row_min = a.other_min;
@@ -192,7 +195,8 @@ struct PagedWalk {
   int32_t slot0;
   bool first;
 
-  CPATTN_HD void start(const PagedArgs& a, const PagedStart& s, int64_t units, int block) {
+  template <class A>
+  CPATTN_HD void start(const A& a, const PagedStart& s, int64_t units, int block) {
     at = s;
     left = units;
     slot0 = 2 * block;
@@ -203,7 +207,8 @@ struct PagedWalk {
     }
   }
 
-  CPATTN_HD bool next(const PagedArgs& a, PagedPiece& p) {
+  template <class A>
+  CPATTN_HD bool next(const A& a, PagedPiece& p) {
     if (left <= 0) return false;
     while (at.t >= nt) {  // the next kv-head, or the next request that has a row
       at.t = 0;

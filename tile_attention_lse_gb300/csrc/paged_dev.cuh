@@ -15,13 +15,13 @@ constexpr int kOwnTiles = 16;
 // block calls it, `sh` holds 64 int64 and `out` a PagedStart in shared memory
 // (not written where c has no first unit).  The threads share the requests in
 // runs; the loops are warp-uniform so that lanes can help one another.
-template <int U, int E, int kThreads>
-__device__ __forceinline__ PagedShare paged_locate(const PagedArgs& a, int64_t* sh, PagedStart* out, int c) {
+template <int U, int E, int kThreads, class A>
+__device__ __forceinline__ PagedShare paged_locate(const A& a, int64_t* sh, PagedStart* out, int c) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int run = (a.n_reqs + kThreads - 1) / kThreads;
   const int r0 = tid * run;
   // units of one kv-head of this lane's i-th request
-  auto units = [&](const PagedArgs& a, auto unit, auto extra, int i, PagedReq& q, int& nt) -> int64_t {
+  auto units = [&](const A& a, auto unit, auto extra, int i, PagedReq& q, int& nt) -> int64_t {
     constexpr int kU = decltype(unit)::value, kE = decltype(extra)::value;
     q = PagedReq{0, 0, 0};
     if (r0 + i < a.n_reqs) q = paged_req(a, r0 + i);
@@ -52,7 +52,7 @@ __device__ __forceinline__ PagedShare paged_locate(const PagedArgs& a, int64_t* 
     mine += last * a.Hkv;
   }
   if (a.other_R > 0) {  // the other launch's units: how the SMs are divided
-    const PagedArgs b = paged_other(a);
+    const A b = paged_other(a);
     for (int i = 0; i < run; ++i) {
       PagedReq x;
       int n;

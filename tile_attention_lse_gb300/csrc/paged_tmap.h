@@ -34,4 +34,8 @@ inline bool make_tmap_pages(CUtensorMap* map, const void* base, const PagedArgs&
              run < 256 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B : CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+inline bool make_tmap_keys(CUtensorMap* map, const PagedArgs& a, bool of_v, int box) {
+  return make_tmap_pages(map, of_v ? a.v : a.k, a, box);
+}
+
 }  // namespace cpattn

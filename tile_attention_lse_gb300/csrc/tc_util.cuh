@@ -410,6 +410,12 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
   return r;
 }
 
+// What two values lose when they are rounded to bf16, as bf16 (value + rest: 2^-17).
+__device__ __forceinline__ uint32_t rest_bf16x2(float lo, float hi) {
+  const uint32_t r = pack_bf16x2(lo, hi);
+  return pack_bf16x2(lo - __uint_as_float(r << 16), hi - __uint_as_float(r & 0xffff0000u));
+}
+
 // ---------------------------------------------- clusters of two CTAs ---
 // A cluster of two CTAs on two SMs runs cta_group::2 MMAs: one M = 256 MMA
 // covers 128 rows in each CTA, A (and the accumulator) split by rows between
