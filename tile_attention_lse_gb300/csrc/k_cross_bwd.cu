@@ -24,7 +24,7 @@
 //    products may read them: 0 times what follows need not be 0.
 //  - Dropout: a lane draws for 8 keys and every eighth query of its 64; the 8 lanes of
 //    those keys exchange the bits, which become byte masks (16 registers) for P and dP.
-//  - Bias: P and dS of a tile stay in float32 registers for the table's gradient (the sum
+//  - Bias: dS of a tile stays in float32 registers for the table's gradient (the sum
 //    over a far bucket nearly cancels: rounded to bf16 it would be off by 2^-9 sqrt(n / w)
 //    for n keys of which w lie near).  A tile beyond `reach` adds its sum to one number.  Another one sums its
 //    diagonals by passing sums from lane to lane while the columns go by (down for those that
@@ -78,9 +78,13 @@ __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
 constexpr int kThreads = 512;
 constexpr int kLaunchRegs = 128;  // per thread at launch (65536 / 512)
 constexpr int kSmallRegs = 72;    // warpgroup 0
-constexpr int kMathRegs = 152;    // warpgroups 1, 2: key-row math
-constexpr int kDqRegs = 136;      // warpgroup 3: dQ read-out
-static_assert(128 * (kSmallRegs + kDqRegs) + 256 * kMathRegs == kThreads * kLaunchRegs,
+// warpgroups 1, 2 (key-row math) and 3 (dQ read-out, D columns a thread)
+template <int D>
+constexpr int kMathRegs = D == 128 ? 144 : 152;
+template <int D>
+constexpr int kDqRegs = D == 128 ? 152 : 136;
+static_assert(128 * (kSmallRegs + kDqRegs<128>) + 256 * kMathRegs<128> == kThreads * kLaunchRegs &&
+                  128 * (kSmallRegs + kDqRegs<64>) + 256 * kMathRegs<64> == kThreads * kLaunchRegs,
               "setmaxnreg shares must add up to the launch allocation");
 
 template <int D>
@@ -485,7 +489,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_kernel(const __grid_con
     // ------------------------------------------------- key-row math warps --
     // Eight warps, two per TMEM lane quarter: warp w serves key rows
     // 32 (w % 4) .. +31 and query columns 64 h .. 64 h + 63, h = (w - 4) / 4.
-    tc::setmaxnreg_inc<kMathRegs>();
+    tc::setmaxnreg_inc<kMathRegs<D>>();
     const int quarter = warp & 3;
     const int half = (warp - 4) >> 2;
     const int j = quarter * 32 + lane;  // key row of the tile = TMEM lane
@@ -549,11 +553,11 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_kernel(const __grid_con
         const bool open = __all_sync(0xffffffffu, i_lo <= half * 64 && i_hi >= half * 64 + 64);  // no masking
         const uint32_t i_span = uint32_t(max(i_hi - i_lo, 0));
         auto seen = [&](int i) { return uint32_t(half * 64 + i - i_lo) < i_span; };
-        auto seen_pair = [&](int i) { return (seen(i) ? 0x0000ffffu : 0u) | (seen(i + 1) ? 0xffff0000u : 0u); };
         const float4* L4 = reinterpret_cast<const float4*>(sL + st * 128 + half * 64);  // -L2
         const float4* D4 = reinterpret_cast<const float4*>(sD + st * 128 + half * 64);  // -D / r
-        uint32_t sr[64];        // scores; with a bias P and then dS in float32
-        uint32_t pk[32];        // P, then dS, as bf16 pairs
+        // scores, then P in float32 (dQ and dK are off by 0.0030 of their norm with a rounded P in dS, by 0.0024
+        // so), then, with a bias, dS; and bf16 pairs of 32 of P, then of dS
+        uint32_t sr[64], pk[32];
         tc::tmem_ld32(tS + lane_off + half * 64, sr);
         tc::tmem_ld32(tS + lane_off + half * 64 + 32, sr + 32);
         tc::tmem_wait_ld();
@@ -579,29 +583,17 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_kernel(const __grid_con
               tc::f32x2_split(tc::ffma2(tc::f32x2(__uint_as_float(sr[i]), __uint_as_float(sr[i + 1])), mul2, l2), y0, y1);
               y0 = tc::ex2(y0);
               y1 = tc::ex2(y1);
-              if (kBias) {
-                if (!open) {  // (an overflowed exponential becomes 0 too)
-                  y0 = seen(i) ? y0 : 0.f;
-                  y1 = seen(i + 1) ? y1 : 0.f;
-                }
-                sr[i] = __float_as_uint(y0);
-                sr[i + 1] = __float_as_uint(y1);
+              if (!open) {  // (an overflowed exponential becomes 0 too)
+                y0 = seen(i) ? y0 : 0.f;
+                y1 = seen(i + 1) ? y1 : 0.f;
               }
-              pk[i / 2] = tc::pack_bf16x2(y0, y1);
+              sr[i] = __float_as_uint(y0);
+              sr[i + 1] = __float_as_uint(y1);
+              pk[e4 * 2 + e2] = tc::pack_bf16x2(y0, y1);
+              if constexpr (kDrop) pk[e4 * 2 + e2] &= keep_pair(i);
             }
           }
-          if (!kBias && !open) {  // clear the invisible pairs' bf16 halves
-#pragma unroll
-            for (int e = 0; e < 16; ++e) pk[cc * 16 + e] &= seen_pair(cc * 32 + 2 * e);
-          }
-          if constexpr (kDrop) {
-            uint32_t pd[16];
-#pragma unroll
-            for (int e = 0; e < 16; ++e) pd[e] = pk[cc * 16 + e] & keep_pair(cc * 32 + 2 * e);
-            tc::tmem_st16(tS + lane_off + half * 64 + cc * 16, pd);
-          } else {
-            tc::tmem_st16(tS + lane_off + half * 64 + cc * 16, pk + cc * 16);
-          }
+          tc::tmem_st16(tS + lane_off + half * 64 + cc * 16, pk);
         }
         tc::tmem_wait_st();
         tc::fence_before_sync();
@@ -628,26 +620,19 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_kernel(const __grid_con
               }
               const uint64_t dd = tc::fadd2(tc::f32x2(__uint_as_float(dr[e]), __uint_as_float(dr[e + 1])),
                                             tc::f32x2(dv4[2 * e2], dv4[2 * e2 + 1]));
-              const uint32_t w2 = pk[i / 2];
-              const uint64_t pp = kBias ? tc::f32x2(__uint_as_float(sr[i]), __uint_as_float(sr[i + 1]))
-                                        : tc::f32x2(__uint_as_float(w2 << 16), __uint_as_float(w2 & 0xFFFF0000u));
               float d0, d1;
-              tc::f32x2_split(tc::fmul2(pp, dd), d0, d1);
+              tc::f32x2_split(tc::fmul2(tc::f32x2(__uint_as_float(sr[i]), __uint_as_float(sr[i + 1])), dd), d0, d1);
+              if (!open) {  // 0 times what a row behind the end holds
+                d0 = seen(i) ? d0 : 0.f;
+                d1 = seen(i + 1) ? d1 : 0.f;
+              }
               if (kBias) {
-                if (!open) {  // 0 times what a row behind the end holds
-                  d0 = seen(i) ? d0 : 0.f;
-                  d1 = seen(i + 1) ? d1 : 0.f;
-                }
                 sr[i] = __float_as_uint(d0);
                 sr[i + 1] = __float_as_uint(d1);
                 sum2 = tc::fadd2(sum2, tc::f32x2(d0, d1));
               }
               pk[i / 2] = tc::pack_bf16x2(d0, d1);
             }
-          }
-          if (!kBias && !open) {
-#pragma unroll
-            for (int e = 0; e < 16; ++e) pk[cc * 16 + e] &= seen_pair(cc * 32 + 2 * e);
           }
         }
         tc::fence_before_sync();
@@ -741,7 +726,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_kernel(const __grid_con
     // dP^T.  The four warps then stage the tile in 32-column chunks (two
     // staging buffers) and one thread adds each chunk into the accumulator
     // with a TMA reduction.  Rows behind the sequence's end add zeros.
-    tc::setmaxnreg_inc<kDqRegs>();
+    tc::setmaxnreg_inc<kDqRegs<D>>();
     const int quarter = warp & 3;
     const int i = quarter * 32 + lane;  // query row of the tile = TMEM lane
     const uint32_t lane_off = uint32_t(quarter * 32) << 16;
