@@ -54,7 +54,11 @@ cp_status check_sizes(const cp_cross_desc& d, int32_t n_seqs, int64_t rows_q, in
 
 // The distances that the buckets of a direction start at: 0, 1, .. for the first
 // half, then e (max / e)^(t / (per - e)), e = per / 2, t = 0, 1, ..
+// (Those of the last call are kept, by what they come from: the powers cost as much host time as a launch.)
 RelStarts rel_starts(const cp_cross_desc& d) {
+  static thread_local RelStarts kept = {};
+  static thread_local int32_t buckets = 0, distance = 0, both = 0;
+  if (buckets == d.rel_buckets && distance == d.rel_max_distance && both == d.rel_both) return kept;
   RelStarts s{};
   s.both = d.rel_both != 0;
   s.per = s.both ? d.rel_buckets / 2 : d.rel_buckets;
@@ -67,6 +71,10 @@ RelStarts rel_starts(const cp_cross_desc& d) {
       s.start[b] = int32_t(std::ceil(x * (1.0 - 1e-12)));
     }
   }
+  kept = s;
+  buckets = d.rel_buckets;
+  distance = d.rel_max_distance;
+  both = d.rel_both;
   return s;
 }
 struct RelLayout {

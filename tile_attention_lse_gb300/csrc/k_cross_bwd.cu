@@ -23,7 +23,7 @@
 //    counts on a barrier of its own and warp 3 clears the rows behind the end before the
 //    products may read them: 0 times what follows need not be 0.
 //  - Dropout: a lane draws for 8 keys and every eighth query of its 64; the 8 lanes of
-//    those keys exchange the bits, which become byte masks (16 registers) for P and dP.
+//    those keys exchange byte masks, 16 registers for P and dP.
 //  - Bias: dS of a tile stays in float32 registers for the table's gradient (the sum
 //    over a far bucket nearly cancels: rounded to bf16 it would be off by 2^-9 sqrt(n / w)
 //    for n keys of which w lie near).  A tile beyond `reach` adds its sum to one number.  Another one sums its
@@ -74,6 +74,36 @@ __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
   asm("prmt.b32 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(sel));
   return r;
 }
+
+// Of 8 lanes every one has drawn for one query and 8 keys, and wants the bytes (0 or 255) of its own key and all 8
+// queries: an 8 x 8 transpose of bytes in three exchanges.  (Bits gathered in a byte, fetched
+// lane by lane and spread again took twice the instructions.)
+struct KeepTurn {
+  uint32_t send2, low2, high2, send1, low1, high1;  // byte selectors of the second and third exchange
+  bool upper;
+  __device__ __forceinline__ explicit KeepTurn(int lane) {
+    upper = lane & 4;
+    const bool b = lane & 2, c = lane & 1;
+    send2 = b ? 0x5410u : 0x7632u;
+    low2 = b ? 0x3254u : 0x5410u;
+    high2 = b ? 0x3276u : 0x7610u;
+    send1 = c ? 0x6420u : 0x7531u;
+    low1 = c ? 0x3514u : 0x5240u;
+    high1 = c ? 0x3716u : 0x7260u;
+  }
+  // out: queries 0 .. 3 and 4 .. 7
+  __device__ __forceinline__ void go(const Draw& d, uint32_t add, uint32_t* out) const {
+    const uint32_t k0 = prmt(keep_halves(d.w[0], add), keep_halves(d.w[1], add), 0xFDB9u);  // keys 0 .. 3 of this query
+    const uint32_t k4 = prmt(keep_halves(d.w[2], add), keep_halves(d.w[3], add), 0xFDB9u);
+    uint32_t got = __shfl_xor_sync(0xffffffffu, upper ? k0 : k4, 4);
+    const uint32_t x = upper ? got : k0, y = upper ? k4 : got;  // queries (lane & 3) and 4 further, this half's 4 keys
+    got = __shfl_xor_sync(0xffffffffu, prmt(x, y, send2), 2);
+    const uint32_t x2 = prmt(x, got, low2), y2 = prmt(y, got, high2);
+    got = __shfl_xor_sync(0xffffffffu, prmt(x2, y2, send1), 1);
+    out[0] = prmt(x2, got, low1);
+    out[1] = prmt(y2, got, high1);
+  }
+};
 
 constexpr int kThreads = 512;
 constexpr int kLaunchRegs = 128;  // per thread at launch (65536 / 512)
@@ -497,6 +527,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_kernel(const __grid_con
     const uint64_t sl2x2 = tc::f32x2(a.scale_log2, a.scale_log2);
     DropKey dkey{};
     if (kDrop) dkey = drop_key(a.rng, a.drop_min);
+    const KeepTurn turn(lane);
     uint32_t gt = 0, ni = 0;
     bool ok = true;
     while (ok && share.next(&w)) {
@@ -509,28 +540,25 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_kernel(const __grid_con
         const QTile qt = wk.tile(a, it);
         const uint32_t st = gt & 1;
         const int qpos0 = qt.i0 + it.off;
-        // byte masks: keep[l][t / 4], byte t % 4: query 64 half + 8 t + l
+        // byte masks of the 64 queries: keep[i / 8][i % 8 / 4], byte i % 4
         uint32_t keep[8][2] = {};
         if constexpr (kDrop) {
-          uint32_t mine[2] = {0, 0};
 #pragma unroll
           for (int u = 0; u < 8; ++u) {
             const Draw dr = draw(dkey, uint32_t(kpos) >> 3, uint32_t(qt.i0 + 64 * half + 8 * u + (lane & 7)),
                                  uint32_t(it.seq) * uint32_t(a.H) + uint32_t(qt.h));
-            mine[u >> 2] |= keep_bits(dr, dkey.add) << (8 * (u & 3));
+            turn.go(dr, dkey.add, keep[u]);
           }
-#pragma unroll
-          for (int l = 0; l < 8; ++l)
-#pragma unroll
-            for (int u = 0; u < 2; ++u)
-              keep[l][u] = ((__shfl_sync(0xffffffffu, mine[u], (lane & 24) + l) >> (lane & 7)) & 0x01010101u) * 0xffu;
         }
         // the mask of queries i, i + 1 of this warp's 64 as two 16-bit halves, and of one query as a word
         auto keep_pair = [&](int i) {
-          const uint32_t u = uint32_t(i >> 3) & 3u;
-          return prmt(keep[i & 7][i >> 5], keep[(i & 7) + 1][i >> 5], u * 0x11u + (u + 4) * 0x1100u);
+          const uint32_t r = keep[i >> 3][(i >> 2) & 1], u = uint32_t(i) & 3u;
+          return prmt(r, r, u * 0x11u + (u + 1) * 0x1100u);
         };
-        auto keep_word = [&](int i) { return prmt(keep[i & 7][i >> 5], 0, (uint32_t(i >> 3) & 3u) * 0x1111u); };
+        auto keep_word = [&](int i) {
+          const uint32_t r = keep[i >> 3][(i >> 2) & 1];
+          return prmt(r, r, (uint32_t(i) & 3u) * 0x1111u);
+        };
         // the bias: query i of the 64 lies at relative position x0 - i; `top` is the largest of
         // the warp, the smallest is 94 below
         const int x0 = kpos - qpos0 - 64 * half;
