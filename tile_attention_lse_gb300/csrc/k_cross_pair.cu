@@ -398,8 +398,8 @@ __global__ void __launch_bounds__(kThreads, 1) cross_pair_kernel(const __grid_co
           rel_back = rel[-a.reach];
           rel_fore = rel[a.reach];
         }
-        DropKey dkey{};
-        if (kDrop) dkey = drop_key(a.rng, a.drop_min);
+        DropKeys dkey{};
+        if (kDrop) dkey = drop_keys(drop_key(a.rng, a.drop_min));
         const uint32_t seq_head = uint32_t(pc.r) * uint32_t(a.H) + uint32_t(head);
         float m_own = -INFINITY, l = 0.f;  // this warp's row sum and the max it is taken against
         for (int t = 0; t < n && ok; ++t, ++g) {

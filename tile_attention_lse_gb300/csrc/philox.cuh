@@ -28,19 +28,40 @@ __device__ __forceinline__ DropKey drop_key(const uint64_t* rng, uint32_t thresh
   return DropKey{uint32_t(seed), uint32_t(seed >> 32), uint32_t(offset), (0x8000u - threshold) * 0x10001u};
 }
 
+// The same with the keys of all rounds formed beforehand, where there are registers for them: the adds are a fifth
+// of a draw's instructions on the pipe that bounds it.
+struct DropKeys {
+  uint32_t k0[7], k1[7], c3, add;
+};
+__device__ __forceinline__ DropKeys drop_keys(const DropKey& key) {
+  DropKeys x;
+  x.c3 = key.c3;
+  x.add = key.add;
+#pragma unroll
+  for (int r = 0; r < 7; ++r) {
+    x.k0[r] = key.k0 + uint32_t(r) * 0x9E3779B9u;
+    x.k1[r] = key.k1 + uint32_t(r) * 0xBB67AE85u;
+    asm volatile("" : "+r"(x.k0[r]), "+r"(x.k1[r]));  // not to be formed again
+  }
+  return x;
+}
+__device__ __forceinline__ uint32_t round_key0(const DropKey& key, int r) { return key.k0 + uint32_t(r) * 0x9E3779B9u; }
+__device__ __forceinline__ uint32_t round_key1(const DropKey& key, int r) { return key.k1 + uint32_t(r) * 0xBB67AE85u; }
+__device__ __forceinline__ uint32_t round_key0(const DropKeys& key, int r) { return key.k0[r]; }
+__device__ __forceinline__ uint32_t round_key1(const DropKeys& key, int r) { return key.k1[r]; }
+
 // Counter: keys 8 block .. 8 block + 7 of query i (counted in its sequence), and
 // sequence * heads + head.
-__device__ __forceinline__ Draw draw(const DropKey& key, uint32_t block, uint32_t i, uint32_t seq_head) {
-  uint32_t c0 = block, c1 = i, c2 = seq_head, c3 = key.c3, k0 = key.k0, k1 = key.k1;
+template <class K>
+__device__ __forceinline__ Draw draw(const K& key, uint32_t block, uint32_t i, uint32_t seq_head) {
+  uint32_t c0 = block, c1 = i, c2 = seq_head, c3 = key.c3;
 #pragma unroll
   for (int r = 0; r < 7; ++r) {
     const uint64_t a = uint64_t(c0) * 0xD2511F53u, b = uint64_t(c2) * 0xCD9E8D57u;
-    c0 = uint32_t(b >> 32) ^ c1 ^ k0;
+    c0 = uint32_t(b >> 32) ^ c1 ^ round_key0(key, r);
     c1 = uint32_t(b);
-    c2 = uint32_t(a >> 32) ^ c3 ^ k1;
+    c2 = uint32_t(a >> 32) ^ c3 ^ round_key1(key, r);
     c3 = uint32_t(a);
-    k0 += 0x9E3779B9u;
-    k1 += 0xBB67AE85u;
   }
   return Draw{{c0, c1, c2, c3}};
 }
