@@ -354,7 +354,7 @@ cp_status cp_cross_attn_bwd(const cp_cross_desc* desc, int32_t n_seqs, int64_t r
     if (st != CP_OK) return st;
   }
   if (!empty && n_seqs > 0) {
-    ProfScope ps(CP_K_CROSS_BWD, s, desc->dtype == CP_BF16 ? 1 : 2);
+    ProfScope ps(CP_K_CROSS_BWD, s);
     st = desc->dtype == CP_BF16 ? launch_cross_bwd(a, s) : launch_cross_bwd_f32(a, s);
     if (st != CP_OK) return st;
   }

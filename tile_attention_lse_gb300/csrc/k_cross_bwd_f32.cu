@@ -2,7 +2,7 @@
 // by tiles of keys, dQ by tiles of queries.  The formulas stand in cross.h; no atomics,
 // every sum has one owner and one order.
 //
-// Both kernels form S and dP of a tile of 64 keys and 64 queries: thread (ty, tx) of 16 x 16 owns
+// Items of both form S and dP of a tile of 64 keys and 64 queries: thread (ty, tx) of 16 x 16 owns
 // keys ty + 16 a and queries tx + 16 b, a, b < 4, and walks the head dimension in 16-byte
 // steps on packed pairs (two FMAs an instruction); rows in shared memory are D + 4 floats apart, so that
 // 8 lanes' rows fall on different banks.  P and dS change hands through shared memory, and in the second
@@ -145,101 +145,106 @@ __device__ __forceinline__ void store(void* to, int64_t row, int heads, int head
   }
 }
 
+// dK, dV and the table's gradient of a tile of keys and a kv-head.
 template <int D>
-__global__ void __launch_bounds__(kThreads, 1) cross_bwd_kv_kernel(const __grid_constant__ CrossBwd a) {
-  extern __shared__ __align__(16) uint8_t raw[];
-  Smem<D>& m = *reinterpret_cast<Smem<D>*>(raw);
+__device__ __forceinline__ void key_item(const CrossBwd& a, Smem<D>& m, int64_t w, const DropKey& dkey) {
   const int ty = threadIdx.x >> 4, tid = threadIdx.x;
-  DropKey dkey{};
-  if (a.rng) dkey = drop_key(a.rng, a.drop_min);
-  const int64_t n = int64_t(*a.k_tiles.count) * a.Hkv;
-  for (int64_t w = blockIdx.x; w < n; w += gridDim.x) {
-    const CrossTile ct = a.k_tiles.list[w / a.Hkv];
-    const int g = int(w % a.Hkv);
-    const PagedReq q = paged_req(a, ct.seq);
-    Tile t;
-    t.seq = ct.seq;
-    t.key0 = ct.first;
-    t.keys = min(kB, q.kv - ct.first);
-    t.off = q.kv - q.nq;
-    const int64_t krow = paged_key_row(a, ct.seq) + ct.first;
-    const int qlo = cross_first_query(a, q, ct.first);
-    uint64_t dk[4][D / 32] = {}, dv[4][D / 32] = {};
-    __syncthreads();
-    load_rows<D>(m.k, a.k, a.k_stride, krow, g, t.keys);
-    load_rows<D>(m.v, a.v, a.v_stride, krow, g, t.keys);
-    for (int hj = 0; hj < a.G; ++hj) {
-      t.head = g * a.G + hj;
-      float sum = 0.f;  // thread b: the table's gradient of bucket b
-      int lo = 1, hi = 0;
-      if (a.rel && tid < a.buckets) rel_range(a.starts, tid, &lo, &hi);
-      for (t.query0 = qlo; t.query0 < q.nq; t.query0 += kB) {
-        t.queries = min(kB, q.nq - t.query0);
-        const int64_t row = q.q0 + t.query0;
-        load_rows<D>(m.q, a.q, a.q_stride, row, t.head, t.queries);
-        load_rows<D>(m.o, a.dout, a.do_stride, row, t.head, t.queries);
-        load_l_d(a, m.l, m.d, t.head, row, t.queries);
-        __syncthreads();
-        probabilities<D>(a, m, t, dkey);
-        __syncthreads();
-        second<D>(dv, m.o, [&](int x, int i) { return m.p[ty + 16 * i][x]; });
-        second<D>(dk, m.q, [&](int x, int i) { return m.s[ty + 16 * i][x]; });
-        if (a.rel) {  // diagonals of dS, then each bucket's of them
-          const int x0 = t.key0 - t.query0 - t.off - (kB - 1);  // relative position of diagonal 0
-          if (tid < 2 * kB - 1) {
-            float s = 0.f;
-            const int d = tid - (kB - 1);  // key - query
-            for (int i = max(0, -d); i < min(kB, kB - d); ++i) s += m.s[i + d][i];
-            m.diag[tid] = s;
-          }
-          __syncthreads();
-          const int d1 = min(hi - x0, 2 * kB - 2);
-          for (int d = max(lo - x0, 0); d <= d1; ++d) sum += m.diag[d];
-        }
-        __syncthreads();
-      }
-      if (a.rel && tid < a.bucket_stride) a.part[(int64_t(ct.id) * a.H + t.head) * a.bucket_stride + tid] = sum;
-    }
-    store<D>(a.dk, krow, a.Hkv, g, t.keys, dk, a.scale * a.drop_scale);
-    store<D>(a.dv, krow, a.Hkv, g, t.keys, dv, a.drop_scale);
-  }
-}
-
-template <int D>
-__global__ void __launch_bounds__(kThreads, 1) cross_bwd_q_kernel(const __grid_constant__ CrossBwd a) {
-  extern __shared__ __align__(16) uint8_t raw[];
-  Smem<D>& m = *reinterpret_cast<Smem<D>*>(raw);
-  const int ty = threadIdx.x >> 4;
-  DropKey dkey{};
-  if (a.rng) dkey = drop_key(a.rng, a.drop_min);
-  const int64_t n = int64_t(*a.q_tiles.count) * a.H;
-  for (int64_t w = blockIdx.x; w < n; w += gridDim.x) {
-    const CrossTile ct = a.q_tiles.list[w / a.H];
-    const PagedReq q = paged_req(a, ct.seq);
-    Tile t;
-    t.seq = ct.seq;
-    t.head = int(w % a.H);
-    t.query0 = ct.first;
-    t.queries = min(kB, q.nq - ct.first);
-    t.off = q.kv - q.nq;
-    const int64_t row = q.q0 + ct.first, krow = paged_key_row(a, ct.seq);
-    const int end = a.causal ? min(q.kv, ct.first + t.queries + t.off) : q.kv;  // keys that some query sees
-    uint64_t dq[4][D / 32] = {};
-    __syncthreads();
-    load_rows<D>(m.q, a.q, a.q_stride, row, t.head, t.queries);
-    load_rows<D>(m.o, a.dout, a.do_stride, row, t.head, t.queries);
-    load_l_d(a, m.l, m.d, t.head, row, t.queries);
-    for (t.key0 = 0; t.key0 < end; t.key0 += kB) {
-      t.keys = min(kB, q.kv - t.key0);
-      load_rows<D>(m.k, a.k, a.k_stride, krow + t.key0, t.head / a.G, t.keys);
-      load_rows<D>(m.v, a.v, a.v_stride, krow + t.key0, t.head / a.G, t.keys);
+  const CrossTile ct = a.k_tiles.list[w / a.Hkv];
+  const int g = int(w % a.Hkv);
+  const PagedReq q = paged_req(a, ct.seq);
+  Tile t;
+  t.seq = ct.seq;
+  t.key0 = ct.first;
+  t.keys = min(kB, q.kv - ct.first);
+  t.off = q.kv - q.nq;
+  const int64_t krow = paged_key_row(a, ct.seq) + ct.first;
+  const int qlo = cross_first_query(a, q, ct.first);
+  uint64_t dk[4][D / 32] = {}, dv[4][D / 32] = {};
+  __syncthreads();
+  load_rows<D>(m.k, a.k, a.k_stride, krow, g, t.keys);
+  load_rows<D>(m.v, a.v, a.v_stride, krow, g, t.keys);
+  for (int hj = 0; hj < a.G; ++hj) {
+    t.head = g * a.G + hj;
+    float sum = 0.f;  // thread b: the table's gradient of bucket b
+    int lo = 1, hi = 0;
+    if (a.rel && tid < a.buckets) rel_range(a.starts, tid, &lo, &hi);
+    for (t.query0 = qlo; t.query0 < q.nq; t.query0 += kB) {
+      t.queries = min(kB, q.nq - t.query0);
+      const int64_t row = q.q0 + t.query0;
+      load_rows<D>(m.q, a.q, a.q_stride, row, t.head, t.queries);
+      load_rows<D>(m.o, a.dout, a.do_stride, row, t.head, t.queries);
+      load_l_d(a, m.l, m.d, t.head, row, t.queries);
       __syncthreads();
       probabilities<D>(a, m, t, dkey);
       __syncthreads();
-      second<D>(dq, m.k, [&](int x, int i) { return m.s[x][ty + 16 * i]; });
+      second<D>(dv, m.o, [&](int x, int i) { return m.p[ty + 16 * i][x]; });
+      second<D>(dk, m.q, [&](int x, int i) { return m.s[ty + 16 * i][x]; });
+      if (a.rel) {  // diagonals of dS, then each bucket's of them
+        const int x0 = t.key0 - t.query0 - t.off - (kB - 1);  // relative position of diagonal 0
+        if (tid < 2 * kB - 1) {
+          float s = 0.f;
+          const int d = tid - (kB - 1);  // key - query
+          for (int i = max(0, -d); i < min(kB, kB - d); ++i) s += m.s[i + d][i];
+          m.diag[tid] = s;
+        }
+        __syncthreads();
+        const int d1 = min(hi - x0, 2 * kB - 2);
+        for (int d = max(lo - x0, 0); d <= d1; ++d) sum += m.diag[d];
+      }
       __syncthreads();
     }
-    store<D>(a.dq, row, a.H, t.head, t.queries, dq, a.scale * a.drop_scale);
+    if (a.rel && tid < a.bucket_stride) a.part[(int64_t(ct.id) * a.H + t.head) * a.bucket_stride + tid] = sum;
+  }
+  store<D>(a.dk, krow, a.Hkv, g, t.keys, dk, a.scale * a.drop_scale);
+  store<D>(a.dv, krow, a.Hkv, g, t.keys, dv, a.drop_scale);
+}
+
+// dQ of a tile of queries and a head.
+template <int D>
+__device__ __forceinline__ void query_item(const CrossBwd& a, Smem<D>& m, int64_t w, const DropKey& dkey) {
+  const int ty = threadIdx.x >> 4;
+  const CrossTile ct = a.q_tiles.list[w / a.H];
+  const PagedReq q = paged_req(a, ct.seq);
+  Tile t;
+  t.seq = ct.seq;
+  t.head = int(w % a.H);
+  t.query0 = ct.first;
+  t.queries = min(kB, q.nq - ct.first);
+  t.off = q.kv - q.nq;
+  const int64_t row = q.q0 + ct.first, krow = paged_key_row(a, ct.seq);
+  const int end = a.causal ? min(q.kv, ct.first + t.queries + t.off) : q.kv;  // keys that some query sees
+  uint64_t dq[4][D / 32] = {};
+  __syncthreads();
+  load_rows<D>(m.q, a.q, a.q_stride, row, t.head, t.queries);
+  load_rows<D>(m.o, a.dout, a.do_stride, row, t.head, t.queries);
+  load_l_d(a, m.l, m.d, t.head, row, t.queries);
+  for (t.key0 = 0; t.key0 < end; t.key0 += kB) {
+    t.keys = min(kB, q.kv - t.key0);
+    load_rows<D>(m.k, a.k, a.k_stride, krow + t.key0, t.head / a.G, t.keys);
+    load_rows<D>(m.v, a.v, a.v_stride, krow + t.key0, t.head / a.G, t.keys);
+    __syncthreads();
+    probabilities<D>(a, m, t, dkey);
+    __syncthreads();
+    second<D>(dq, m.k, [&](int x, int i) { return m.s[x][ty + 16 * i]; });
+    __syncthreads();
+  }
+  store<D>(a.dq, row, a.H, t.head, t.queries, dq, a.scale * a.drop_scale);
+}
+
+// Items of keys (the longer ones) in front of items of queries, in one launch: few short sequences fill
+// the SMs with neither alone (5 pairs of about 100 over 333, 8 heads over 2: 228 us as two launches).
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1) cross_bwd_f32_kernel(const __grid_constant__ CrossBwd a) {
+  extern __shared__ __align__(16) uint8_t raw[];
+  Smem<D>& m = *reinterpret_cast<Smem<D>*>(raw);
+  DropKey dkey{};
+  if (a.rng) dkey = drop_key(a.rng, a.drop_min);
+  const int64_t nk = int64_t(*a.k_tiles.count) * a.Hkv, n = nk + int64_t(*a.q_tiles.count) * a.H;
+  for (int64_t w = blockIdx.x; w < n; w += gridDim.x) {
+    if (w < nk)
+      key_item<D>(a, m, w, dkey);
+    else
+      query_item<D>(a, m, w - nk, dkey);
   }
 }
 
@@ -250,16 +255,13 @@ cp_status run(const CrossBwd& a, cudaStream_t s) {
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return CP_ERR_CUDA;
   const int bytes = int(sizeof(Smem<D>));
   if (!ready[dev].load(std::memory_order_acquire)) {
-    if (cudaFuncSetAttribute(cross_bwd_kv_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess ||
-        cudaFuncSetAttribute(cross_bwd_q_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
+    if (cudaFuncSetAttribute(cross_bwd_f32_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
       return CP_ERR_CUDA;
     ready[dev].store(true, std::memory_order_release);
   }
-  const int64_t sms = num_sms(), most_k = int64_t(a.k_tiles.most) * a.Hkv, most_q = int64_t(a.q_tiles.most) * a.H;
-  cross_bwd_kv_kernel<D><<<unsigned(most_k < sms ? most_k : sms), kThreads, bytes, s>>>(a);
-  const cp_status st = cuda_status(cudaGetLastError());
-  if (st != CP_OK) return st;
-  cross_bwd_q_kernel<D><<<unsigned(most_q < sms ? most_q : sms), kThreads, bytes, s>>>(a);
+  const int64_t blocks = num_sms();
+  const int64_t most = int64_t(a.k_tiles.most) * a.Hkv + int64_t(a.q_tiles.most) * a.H;
+  cross_bwd_f32_kernel<D><<<unsigned(most < blocks ? most : blocks), kThreads, bytes, s>>>(a);
   return cuda_status(cudaGetLastError());
 }
 
