@@ -319,7 +319,7 @@ cp_status cp_get_device_error(void* stream);
  * cp_get_device_error reports CP_ERR_TIMEOUT (the outputs of that call are
  * invalid).  The pages have no counterpart ("04 · Megatron-LM 实现" §7.2 shows
  * only the deadlock a missing barrier participant causes).  Not for production
- * use. */
+ * use.  (cp_cross_attn_fwd and cp_cross_attn_bwd keep the default budget.) */
 cp_status cp_debug_set_wait_limit(int64_t cycles);
 
 /* Host-only statistics of the task graph built for a descriptor (no GPU use):

@@ -192,6 +192,26 @@ def test_wide_groups():
     check(Case([(5, 300), (2, 7)], H=128, Hkv=1, d=64))
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("max_q", [0, 1, 5])
+def test_the_hint_does_not_change_results(max_q, dtype):
+    """max_q says less, or nothing, about the queries: every kernel computes any number."""
+    c = Case(RAGGED, H=4, Hkv=2, d=64, dtype=dtype, rel=REL["both"], max_q=max_q)
+    o, lse = api.cross_attn_fwd(c.problem, c.q, c.k, c.v, *c.dcu, **c.at)
+    check_forward(c, o, lse)
+
+
+def test_table_gradient_without_the_rest():
+    """Without what o lost to its rounding, D is off by u16 of the sum of |dO| |o|."""
+    c = Case(RAGGED, rel=REL["both"], d=64)
+    o, lse, _ = c.forward()
+    want = c.oracle()
+    _, f = c.rounding(want)
+    got = c.backward(o, lse, None)
+    near("dtable", f64(got[3]), want["dtable"], want["mag_dtable"], f + U16, U16)
+    near("dq", f64(got[0]), want["dq"], want["mag_dq"], f + 3 * U16, U16, 2 * U16)
+
+
 # ---------------------------------------------------- everything, each type ---
 @pytest.mark.parametrize("dtype", [BF, F32])
 @pytest.mark.parametrize("d", [64, 128])
