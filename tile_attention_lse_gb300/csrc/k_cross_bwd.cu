@@ -525,8 +525,8 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_kernel(const __grid_con
     const int j = quarter * 32 + lane;  // key row of the tile = TMEM lane
     const uint32_t lane_off = uint32_t(quarter * 32) << 16;
     const uint64_t sl2x2 = tc::f32x2(a.scale_log2, a.scale_log2);
-    DropKey dkey{};
-    if (kDrop) dkey = drop_key(a.rng, a.drop_min);
+    DropKeys dkey{};
+    if (kDrop) dkey = drop_keys(drop_key(a.rng, a.drop_min));
     const KeepTurn turn(lane);
     uint32_t gt = 0, ni = 0;
     bool ok = true;
