@@ -43,7 +43,8 @@ class Case:
     """Inputs of a call: sequences (nq, nk), places of the keys (pad: rows behind each sequence)."""
 
     def __init__(self, seqs, H=4, Hkv=2, d=128, dtype=BF, causal=False, rel=None, p=0.0, fused=False, pad=0, pad_q=0, tail=0,
-                 seed=0, max_q=None, junk=1.0):
+                 seed=0, max_q=None, junk=1.0,
+                 scale=0.0):
         g = torch.Generator().manual_seed(seed)
         nq, nk = [s[0] for s in seqs], [s[1] for s in seqs]
         pq, pk = [n + pad_q for n in nq], [n + pad for n in nk]
@@ -74,7 +75,8 @@ class Case:
         self.rng = torch.tensor([self.seed, self.offset], dtype=torch.int64, device=DEV) if p > 0 else None
         self.p, self.causal, self.dtype, self.d = p, causal, dtype, d
         self.problem = api.CrossProblem(H, Hkv, d, dtype=dtype, causal=causal, rel=rel, dropout=p,
-                                        max_q=max(nq, default=0) if max_q is None else max_q)
+                                        max_q=max(nq, default=0) if max_q is None else max_q, softmax_scale=scale)
+        self.scale = scale or d ** -0.5
         self.at = dict(len_q=i32(nq) if pad_q else None, len_k=i32(nk) if pad else None, bias=self.table, rng=self.rng)
         self.dcu = (i32(self.cu_q), i32(self.cu_k))
 
@@ -88,7 +90,7 @@ class Case:
         rel = None if self.rel is None else (self.rel.buckets, self.rel.max_distance, self.rel.both)
         return X.attention(f64(self.q), f64(self.k), f64(self.v), self.seqs, do=f64(self.do) if grads else None,
                            causal=self.causal, table=None if self.table is None else f64(self.table), rel=rel, p=self.p,
-                           rng=(self.seed, self.offset))
+                           rng=(self.seed, self.offset), scale=self.scale)
 
     def owned(self, keys):
         n = (self.k if keys else self.q).shape[0]
@@ -102,7 +104,7 @@ class Case:
         """e and f of the tolerances."""
         own_q, own_k = self.owned(False), self.owned(True)
         lens = [np.sqrt((f64(x)[own] ** 2).sum(-1)).max(initial=0) for x, own in ((self.q, own_q), (self.k, own_k))]
-        e = 2 * (6 * np.sqrt(self.d) * U32 * lens[0] * lens[1] / np.sqrt(self.d) + 8 * U32 * max(want["top"], 1.0))
+        e = 2 * (6 * np.sqrt(self.d) * U32 * lens[0] * lens[1] * self.scale + 8 * U32 * max(want["top"], 1.0))
         n = max([self.d] + [m for s in self.seqs for m in (s[1], s[3])]) * 8
         return e, 2 * e + 6 * np.sqrt(n) * U32
 
@@ -220,6 +222,24 @@ def test_table_gradient_without_the_rest():
 @pytest.mark.parametrize("causal", [False, True])
 def test_forward_and_backward(causal, p, rel, d, dtype):
     check(Case(RAGGED, d=d, dtype=dtype, causal=causal, rel=REL[rel], p=p, seed=3))
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_scale_of_the_scores(dtype):
+    """Scores without a scale: the largest weights of a row are nearly 1."""
+    check(Case([(140, 200), (3, 150)], d=64, dtype=dtype, rel=REL["both"], p=0.1, scale=1.0))
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_no_sequence_has_work(dtype):
+    c = Case([(0, 0), (0, 5), (7, 0), (0, 140)], dtype=dtype, rel=REL["both"], p=0.1, tail=3, max_q=0)
+    o, lse, rest = c.forward()
+    own = torch.from_numpy(c.owned(False)).to(DEV)
+    assert bool((o[own] == 0).all()) and bool(torch.isneginf(lse[own]).all())
+    assert all(bool((g == 0).all()) for g in c.backward(o, lse, rest))
+    few = Case([(0, 0), (0, 5), (2, 0)], dtype=dtype, rel=REL["both"], tail=3, max_q=2)
+    o, lse = api.cross_attn_fwd(few.problem, few.q, few.k, few.v, *few.dcu, **few.at)
+    assert bool((o[few.owned(False)] == 0).all())
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])

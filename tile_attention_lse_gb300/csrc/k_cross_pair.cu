@@ -20,7 +20,12 @@
 //    with their bias, so that the second pass (exponentials) loads no table.
 //  - Dropout clears halves of the packed bf16 pairs of P, 8 keys a draw; sums and
 //    maxima are of all probabilities.  A tile with a bias that varies, with dropout or
-//    cut by the mask is read from TMEM twice, 32 scores at a time, in loops.
+//    cut by the mask is read from TMEM twice, 32 scores at a time, in loops (under dropout all 128
+//    scores in registers gained 1 % without a bias and lost 15 % with one, to spills).
+// Measured, 8 sequences of 2048 queries and keys, 32 heads over 8 of 128 (16 over 16 of 64): 429 us, 1281 TFLOP/s
+// (212 us, 650); with a bias 602 (290); with dropout 826 (408); with both 933 (458).  The plain tile is bound by the
+// tensor pipe and the softmax as the paged kernel's is, dropout by the generator's integer instructions
+// (14 wide products and 14 logic instructions for 8 keys, on pipes that take a warp in 2 cycles or more).
 #include <cuda_bf16.h>
 
 #include <atomic>

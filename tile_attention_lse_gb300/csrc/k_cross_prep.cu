@@ -134,7 +134,7 @@ __device__ __forceinline__ int64_t quotient(int64_t x, int64_t y) {
 
 // ------------------------------------------------------------ D and L2 ---
 // A (row, head) of d elements is kLanes lanes of 16 bytes; a warp has two such groups
-// under way.  Bound by the bytes of o and dO (and of the sums' zeros).
+// under way.  Bound by the bytes of o and dO and of the sums' zeros (9335 rows of 32 heads of 128: 306 MB, 55 us).
 template <typename T, int D>
 __device__ __forceinline__ void delta_rows(const CrossBwd& a, int64_t warp, int64_t n_warps) {
   constexpr int kVec = 16 / int(sizeof(T)), kLanes = D / kVec, kRows = 32 / kLanes;

@@ -6,7 +6,7 @@
 // Of one draw's 128 bits every element takes 15: piece e is the low 15 bits
 // of half (e % 2) of word e / 2, so one draw serves 8 consecutive keys of a row
 // and a probability is met to 2^-16.  (The generator is what dropout costs, about 4
-// instructions an element; 7 bits each would halve that and miss p = 0.1 by 0.002.)
+// instructions an element; 7 bits each would halve that and meet a probability to 2^-8 only.)
 #pragma once
 
 #include <cstdint>
