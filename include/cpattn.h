@@ -613,9 +613,9 @@ size_t cp_cross_attn_workspace_bytes(const cp_cross_desc* desc, int32_t n_seqs, 
 /* Forward: o [rows_q][heads_q][head_dim], lse [rows_q][heads_q] float32, natural log (as cp_tile_attn_fwd gives
  * them, and without dropout fit to be merged by cp_merge_partials).  q [rows_q][heads_q][head_dim], k and v
  * [rows_k][heads_kv][head_dim] with row strides in elements (slices of one projection).  bias
- * [rel_buckets][heads_q] (NULL iff rel_buckets is 0).  rest (bf16 with a bias only, layout of o; NULL: not wanted): what o
- * lost to its rounding, o + rest being the output to 2^-17; cp_cross_attn_bwd needs it for an exact gradient of
- * the table.  Rows that no sequence owns are not read, and
+ * [rel_buckets][heads_q] (NULL iff rel_buckets is 0).  rest (bf16 only, layout of o, up to 128 q-heads a kv-head; NULL: not wanted): what o
+ * lost to its rounding, o + rest being the output to 2^-17; cp_cross_attn_bwd takes it for an exact gradient of
+ * the table, and for rows that see few keys.  Rows that no sequence owns are not read, and
  * left as they were in o, rest and lse.  o and lse must not overlap the inputs.  A K/V value that is not finite reaches
  * every row of its sequence whose tile of keys holds it, as in the other attention calls, but no
  * other sequence.  A row with a NaN score has NaN in o and lse.  Results do not depend on
@@ -632,7 +632,7 @@ cp_status cp_cross_attn_fwd(const cp_cross_desc* desc, int32_t n_seqs, int64_t r
  *   dq_i = softmax_scale sum_j dS_ij k_j,  dk_j = softmax_scale sum_i dS_ij q_i,  dv_j = sum_i P_ij keep_ij / (1 - p) dO_i,
  *   dbias[b][h] = sum of dS_ij over the pairs of bucket b, all sequences,
  * grouped heads summed into their kv-head.  o, rest and lse are the forward's for the same inputs and rng; without rest
- * (bf16) dbias has the error that the rounding of o makes in dO . o, up to 2^-9 of the sum over each bucket of P |dO| |o|.
+ * (bf16) dS has the error that the rounding of o makes in dO . o, up to 2^-8 P |dO| |o|, which a bucket's sum keeps.
  * dout has the layout of q (row stride in elements).
  * dq, dk and dv [rows][heads][head_dim] are contiguous; rows that no sequence owns (and keys that no query
  * sees) get zeros.  dbias [rel_buckets][heads_q], given iff bias is.  The outputs must not overlap the inputs.

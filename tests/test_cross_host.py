@@ -105,7 +105,6 @@ def test_call_refusals(call):
     assert call(r) == INVALID                                               # buckets without a bias
     assert call(problem(dropout=0.1)) == INVALID                            # no rng
     assert call(problem(dropout=0.1), rng=A + 4) == INVALID
-    assert call(p, rest=A) == INVALID                                       # without a bias there is none
     assert call(problem(dtype=torch.float32), rest=A) == INVALID
     assert call(problem(head_dim=96)) == UNSUP
 

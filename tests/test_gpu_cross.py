@@ -191,7 +191,10 @@ def test_wide_groups():
     c = Case([(5, 300), (2, 7)], H=160, Hkv=1, d=64)
     o, lse, _ = c.forward()
     check_forward(c, o, lse)
-    check(Case([(5, 300), (2, 7)], H=128, Hkv=1, d=64))
+    check(Case([(5, 300), (2, 7)], H=160, Hkv=1, d=64, causal=True, rel=REL["both"], dtype=F32))
+    wide = Case([(5, 300), (2, 7)], H=160, Hkv=1, d=64, causal=True, rel=REL["both"])
+    assert wide.forward()[2] is None       # the slices do not write it
+    check(Case([(5, 300), (2, 7)], H=128, Hkv=1, d=64, causal=True))
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
@@ -201,6 +204,18 @@ def test_the_hint_does_not_change_results(max_q, dtype):
     c = Case(RAGGED, H=4, Hkv=2, d=64, dtype=dtype, rel=REL["both"], max_q=max_q)
     o, lse = api.cross_attn_fwd(c.problem, c.q, c.k, c.v, *c.dcu, **c.at)
     check_forward(c, o, lse)
+
+
+def test_rows_that_see_few_keys():
+    """A causal row's first keys: dP - D nearly cancels, and the rest keeps it (dS of a row with one key is 0)."""
+    c = Case([(64, 64)], H=4, Hkv=4, d=128, causal=True)
+    o, lse, rest = c.forward()
+    with_rest, without = c.backward(o, lse, rest), c.backward(o, lse, None)
+    assert float(with_rest[0][0].float().abs().max()) <= float(without[0][0].float().abs().max())
+    # D to 2^-17, scores and P to f of |dO| |v|
+    want = c.oracle()
+    _, f = c.rounding(want)
+    assert np.all(np.abs(f64(with_rest[0][0])) <= (f + 2 * U16 ** 2) * want["mag_dq"][0] + 1e-30)
 
 
 def test_table_gradient_without_the_rest():

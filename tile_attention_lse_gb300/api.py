@@ -683,7 +683,7 @@ class CrossProblem:
                  causal: bool = False, max_q: int = 0, rel: RelBuckets | None = None, dropout: float = 0.0,
                  softmax_scale: float = 0.0):
         self.heads_q, self.heads_kv, self.head_dim, self.dtype = int(heads_q), int(heads_kv), int(head_dim), dtype
-        self.rel, self.dropout = rel, float(dropout)
+        self.rel, self.dropout, self.causal = rel, float(dropout), bool(causal)
         r = (rel.buckets, rel.max_distance, int(rel.both)) if rel is not None else (0, 0, 0)
         self._desc = CpCrossDesc(self.heads_q, self.heads_kv, self.head_dim, _dtype_code(dtype), int(bool(causal)),
                                  int(max_q), *r, self.dropout, float(softmax_scale))
@@ -750,7 +750,8 @@ def cross_attn_fwd(p: CrossProblem, q, k, v, cu_q, cu_k, len_q=None, len_k=None,
     """Attention of q [rows_q, heads_q, head_dim] over k and v [rows_k, heads_kv, head_dim],
     sequence by sequence (cp_cross_attn_fwd) -> (o, lse).  Rows that no sequence owns are
     left as they were (unset in a new o and lse).  for_backward: -> (o, lse, rest), rest what o lost
-    to its rounding (bf16 with a bias; None elsewhere), which cross_attn_bwd takes."""
+    to its rounding, which cross_attn_bwd takes (bf16 with a bias or causal, where it tells: the table's gradient
+    and rows that see few keys; None elsewhere)."""
     dev, n, rows_q, rows_k, qkv, cu, bias, rng = _cross_inputs(p, q, k, v, cu_q, cu_k, len_q, len_k, bias, rng)
     s = _stream_of(dev)
     ws = _cross_ws(p, ws, n, rows_q, rows_k, False, dev)
@@ -758,7 +759,7 @@ def cross_attn_fwd(p: CrossProblem, q, k, v, cu_q, cu_k, len_q=None, len_k=None,
     out = _new(out, "out", (rows_q, heads, d), p.dtype, dev)
     lse = _new(lse, "lse", (rows_q, heads), _F32, dev)
     rest = None
-    if for_backward and bias is not None and p.dtype is torch.bfloat16:
+    if for_backward and p.dtype is torch.bfloat16 and (bias is not None or p.causal) and heads <= 128 * p.heads_kv:
         rest = _new(None, "rest", (rows_q, heads, d), p.dtype, dev)
     _check(lib().cp_cross_attn_fwd(p._ref, n, rows_q, rows_k, *qkv, *cu, bias, rng, out.data_ptr(),
                                    None if rest is None else rest.data_ptr(), lse.data_ptr(), ws.data_ptr(), ws.nbytes, s),

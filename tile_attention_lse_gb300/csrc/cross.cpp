@@ -117,7 +117,7 @@ struct Layout {
 Layout layout(const cp_cross_desc& d, int64_t rows_q, int64_t rows_k, int32_t n_seqs, bool backward) {
   Layout l;
   l.states = up256(size_t(d.heads_q) * rel_layout(d).stride * 4);
-  const int64_t states = std::max(fwd_states(d, pick(d, false)), fwd_states(d, pick(d, d.rel_buckets > 0)));
+  const int64_t states = std::max(fwd_states(d, pick(d, false)), fwd_states(d, pick(d, true)));
   l.total = l.states + size_t(states) * (size_t(d.head_dim) + 1) * 4;
   if (!backward) return l;
   const bool bf16 = d.dtype == CP_BF16;
@@ -250,7 +250,7 @@ cp_status cp_cross_attn_fwd(const cp_cross_desc* desc, int32_t n_seqs, int64_t r
   st = check_call(desc, rows_q, rows_k, q, q_stride, k, k_stride, v, v_stride, cu_q, cu_k, bias, rng);
   if (st != CP_OK) return st;
   if (!o || !lse || !ws || !aligned(ws, 256)) return CP_ERR_INVALID_ARG;
-  if (rest && (desc->dtype != CP_BF16 || !bias)) return CP_ERR_INVALID_ARG;
+  if (rest && desc->dtype != CP_BF16) return CP_ERR_INVALID_ARG;
   if (rest && desc->heads_q / desc->heads_kv > kPairRows) return CP_ERR_UNSUPPORTED;
   if (!aligned(o, 16) || !aligned(rest, 16)) return CP_ERR_ALIGNMENT;
   const Layout l = layout(*desc, rows_q, rows_k, n_seqs, false);
@@ -307,7 +307,7 @@ cp_status cp_cross_attn_bwd(const cp_cross_desc* desc, int32_t n_seqs, int64_t r
   if ((rows_q > 0 && (!o || !lse || !dout || !dq)) || (rows_k > 0 && (!dk || !dv)) || (bias && !dbias) || !ws ||
       !aligned(ws, 256))
     return CP_ERR_INVALID_ARG;
-  if (rest && (desc->dtype != CP_BF16 || !bias)) return CP_ERR_INVALID_ARG;
+  if (rest && desc->dtype != CP_BF16) return CP_ERR_INVALID_ARG;
   if (rows_q > 0 && dout_stride < int64_t(desc->heads_q) * desc->head_dim) return CP_ERR_INVALID_ARG;
   if (dout_stride >= (int64_t(1) << 40) / 4) return CP_ERR_UNSUPPORTED;
   if (!aligned(o, 16) || !aligned(rest, 16) || (rows_q > 0 && !row_ok(dout, dout_stride, desc->dtype)) ||

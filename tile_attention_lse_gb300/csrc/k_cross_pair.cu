@@ -678,7 +678,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_pair_kernel(const __grid_co
               if (quarter * 32 + (lane & ~3) + j < rows_here)
                 *reinterpret_cast<uint4*>(out + at_j * D + c0 + cc * 32 + 8 * (lane & 3)) = v[j];
             }
-            if (!kBias || !a.rest || out == a.rest) break;
+            if (!a.rest || out == a.rest) break;
             out = static_cast<__nv_bfloat16*>(a.rest);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
