@@ -8,10 +8,10 @@ the value), element by element, times the sums of magnitudes that the oracle giv
   of the largest score; P is off by twice all that (its row's sum too): e;
 * a sum of n products in float32: 6 sqrt(n) u32 more: f = 2 e + 6 sqrt(n) u32;
 * bfloat16: P is rounded before its second product (u16); D's O is rounded (u16) and so
-  is dS, of a rounded P without a bias (3 u16 in all); the outputs are rounded (u16 of
-  the value).  The table's gradient takes P and dS in float32 and D to 2^-16.
-In the mean the roundings are independent: the 2-norm is held to 2 u16 (the three of dQ and
-dK are sqrt(3) u16 / sqrt(3), and the output's u16 / sqrt(3)).
+  is dS (2 u16 in all); the outputs are rounded (u16 of the value).  The table's gradient
+  takes P and dS in float32 and D to 2^-16.
+In the mean the roundings are independent: the 2-norm is held to 2 u16 (the two of dQ and
+dK are sqrt(2) u16 / sqrt(3), and the output's u16 / sqrt(3)).
 """
 
 import numpy as np
@@ -142,8 +142,8 @@ def check_backward(c, grads, want):
     _, f = c.rounding(want)
     bf = c.dtype is BF
     u, norm = (U16, 2 * U16) if bf else (2 * U32, None)
-    near("dq", f64(dq), want["dq"], want["mag_dq"], f + (3 * U16 if bf else 0), u, norm)
-    near("dk", f64(dk), want["dk"], want["mag_dk"], f + (3 * U16 if bf else 0), u, norm)
+    near("dq", f64(dq), want["dq"], want["mag_dq"], f + (2 * U16 if bf else 0), u, norm)
+    near("dk", f64(dk), want["dk"], want["mag_dk"], f + (2 * U16 if bf else 0), u, norm)
     near("dv", f64(dv), want["dv"], want["mag_dv"], f + (U16 if bf else 0), u, norm)
     if dtable is not None:
         near("dtable", f64(dtable), want["dtable"], want["mag_dtable"], f + (U16 ** 2 if bf else 0), u)
@@ -226,7 +226,7 @@ def test_table_gradient_without_the_rest():
     _, f = c.rounding(want)
     got = c.backward(o, lse, None)
     near("dtable", f64(got[3]), want["dtable"], want["mag_dtable"], f + U16, U16)
-    near("dq", f64(got[0]), want["dq"], want["mag_dq"], f + 3 * U16, U16, 2 * U16)
+    near("dq", f64(got[0]), want["dq"], want["mag_dq"], f + 2 * U16, U16, 2 * U16)
 
 
 # ---------------------------------------------------- everything, each type ---
@@ -309,7 +309,7 @@ def test_one_sequence_that_is_not_finite(dtype):
         x[row] = bad
     o, lse, rest = c.forward()
     dq, dk, dv, _ = c.backward(o, lse, rest)
-    share = f + (3 * U16 if dtype is BF else 0)
+    share = f + (2 * U16 if dtype is BF else 0)
     for i in (0, 2):
         a, n, b, m = c.seqs[i]
         for got, name, at in ((o, "o", slice(a, a + n)), (dq, "dq", slice(a, a + n)), (dk, "dk", slice(b, b + m)),
