@@ -132,6 +132,15 @@ def test_rest_wants_the_pair_kernel():
     assert fwd(p, bias=A, rest=A) == UNSUP
 
 
+def test_table_gradient_wants_the_rest():
+    """More heads a kv-head than the pair kernel packs: no forward leaves what dbias needs in bf16."""
+    rel = api.RelBuckets(32)
+    assert bwd(problem(heads_q=256, heads_kv=1, rel=rel), bias=A, dbias=A, wb=16) == UNSUP
+    assert bwd(problem(heads_q=128, heads_kv=1, rel=rel), bias=A, dbias=A, wb=16) == WORK
+    assert bwd(problem(heads_q=256, heads_kv=1, rel=rel, dtype=torch.float32), bias=A, dbias=A, wb=16) == WORK
+    assert bwd(problem(heads_q=256, heads_kv=1), wb=16) == WORK
+
+
 def test_python_refusals():
     p = problem()
     q, k = torch.zeros((4, 8, 128), dtype=torch.bfloat16), torch.zeros((6, 2, 128), dtype=torch.bfloat16)

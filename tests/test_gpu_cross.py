@@ -270,6 +270,47 @@ def test_few_queries_over_a_long_context(dtype):
     check(Case([(2, 6000), (3, 4001)], H=8, Hkv=4, d=64, dtype=dtype, rel=api.RelBuckets(16, 600, False), causal=True, p=0.1))
 
 
+# buckets, their distance, directions; a row's keys outside the bucket that holds most of them
+LONG = [(4, 16, False, 6), (16, 100, False, 73), (8, 40, True, 9), (32, 128, True, 91), (2, 1, False, 1)]
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("p", [0.0, 0.1])
+@pytest.mark.parametrize("buckets,distance,both,w", LONG)
+def test_table_gradient_where_one_bucket_holds_nearly_all_keys(buckets, distance, both, w, p, dtype):
+    """A row's dS sums to 0, and the far bucket keeps what D = dO . o is off by: sqrt(n / w) of the gradient times that.
+
+    float32: P is off by about 4 u32 (a score of d = 64 products 3, the exponent 2), in the forward's o and, by
+    other sums, in the backward's: D by 6 u32, 2^-21.4; five deviations: 2^-19.  bf16: P, and o with rest, are kept in two
+    parts of 8 bits, each off by u16^2 of the value at most: together 2^-15, half of which is more than their mean; and the
+    rounding of the gradient itself, u16 at most."""
+    rel, n = api.RelBuckets(buckets, distance, both), 30000
+    c = Case([(8, n), (3, n // 2)], H=4, Hkv=2, d=64, dtype=dtype, rel=rel, p=p, causal=not both, seed=5)
+    o, lse, rest = c.forward()
+    want = check_forward(c, o, lse, rest, c.oracle())
+    grads = c.backward(o, lse, rest)
+    check_backward(c, grads, want)
+    share = 2 ** -16 if dtype is BF else 2 ** -19
+    far = np.linalg.norm(f64(grads[3]) - want["dtable"]) / np.linalg.norm(want["dtable"])
+    assert far <= share * np.sqrt(n / w) + (U16 if dtype is BF else U32), far
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("p", [0.0, 0.3])
+@pytest.mark.parametrize("rel", ["back", "both", "short"])
+@pytest.mark.parametrize("seqs", [RAGGED, [(3, 9000), (1, 4000)], [(600, 700)]])
+def test_output_and_rest_under_a_bias(seqs, rel, p, d):
+    """P in two parts of 8 bits (u16^2 of P lost) and rest (u16^2 of o): whole tiles, cut ones, tiles far from the diagonal."""
+    c = Case(seqs, H=4, Hkv=2, d=d, rel=REL[rel], p=p, causal=rel == "back", seed=6)
+    o, lse, rest = c.forward()
+    want = check_forward(c, o, lse, rest)
+    own, (_, f) = c.owned(False), c.rounding(want)
+    full = f64(o)[own] + f64(rest)[own]
+    near("o + rest", full, want["o"][own], want["mag_o"][own], f + U16 ** 2, U16 ** 2, U16 ** 2)
+    o, lse = api.cross_attn_fwd(c.problem, c.q, c.k, c.v, *c.dcu, **c.at)  # the copies without rest
+    check_forward(c, o, lse, None, want)
+
+
 def test_fused_and_padded_inputs():
     for dtype in (BF, F32):
         check(Case(RAGGED, dtype=dtype, fused=True, pad=37, pad_q=11, tail=5, rel=REL["both"], p=0.2))

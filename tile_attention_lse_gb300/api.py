@@ -750,7 +750,7 @@ def cross_attn_fwd(p: CrossProblem, q, k, v, cu_q, cu_k, len_q=None, len_k=None,
     """Attention of q [rows_q, heads_q, head_dim] over k and v [rows_k, heads_kv, head_dim],
     sequence by sequence (cp_cross_attn_fwd) -> (o, lse).  Rows that no sequence owns are
     left as they were (unset in a new o and lse).  for_backward: -> (o, lse, rest), rest what o lost
-    to its rounding, which cross_attn_bwd takes (bf16 with a bias or causal, where it tells: the table's gradient
+    to rounding, which cross_attn_bwd takes (bf16 with a bias or causal, where it tells: the table's gradient
     and rows that see few keys; None elsewhere)."""
     dev, n, rows_q, rows_k, qkv, cu, bias, rng = _cross_inputs(p, q, k, v, cu_q, cu_k, len_q, len_k, bias, rng)
     s = _stream_of(dev)
@@ -770,8 +770,8 @@ def cross_attn_fwd(p: CrossProblem, q, k, v, cu_q, cu_k, len_q=None, len_k=None,
 def cross_attn_bwd(p: CrossProblem, q, k, v, o, lse, dout, cu_q, cu_k, len_q=None, len_k=None, bias=None, rng=None,
                    rest=None, ws: torch.Tensor | None = None, dq=None, dk=None, dv=None, dbias=None):
     """Gradients (cp_cross_attn_bwd) -> (dq, dk, dv, dbias); dbias is None without a bias.
-    o, lse and rest are cross_attn_fwd's for the same inputs and rng.  Rows that no
-    sequence owns get zeros."""
+    o, lse and rest are cross_attn_fwd's for the same inputs and rng (in bf16 without rest, dbias loses digits over
+    many keys).  Rows that no sequence owns get zeros."""
     dev, n, rows_q, rows_k, qkv, cu, bias, rng = _cross_inputs(p, q, k, v, cu_q, cu_k, len_q, len_k, bias, rng)
     s = _stream_of(dev)
     ws = _cross_ws(p, ws, n, rows_q, rows_k, True, dev)

@@ -308,6 +308,8 @@ cp_status cp_cross_attn_bwd(const cp_cross_desc* desc, int32_t n_seqs, int64_t r
       !aligned(ws, 256))
     return CP_ERR_INVALID_ARG;
   if (rest && desc->dtype != CP_BF16) return CP_ERR_INVALID_ARG;
+  // no forward leaves the rest that the table's gradient needs
+  if (bias && desc->dtype == CP_BF16 && desc->heads_q / desc->heads_kv > kPairRows) return CP_ERR_UNSUPPORTED;
   if (rows_q > 0 && dout_stride < int64_t(desc->heads_q) * desc->head_dim) return CP_ERR_INVALID_ARG;
   if (dout_stride >= (int64_t(1) << 40) / 4) return CP_ERR_UNSUPPORTED;
   if (!aligned(o, 16) || !aligned(rest, 16) || (rows_q > 0 && !row_ok(dout, dout_stride, desc->dtype)) ||

@@ -23,7 +23,7 @@ struct CrossArgs : PagedArgs {
   int64_t k_stride, v_stride, rows_k;
   const float* rel;  // null: no bias
   int32_t rel_stride, rel_zero, reach;
-  void* rest;  // bf16: what o lost to its rounding, [rows][H][d]; null: not asked for
+  void* rest;  // bf16: what o lost, [rows][H][d]: with a bias to both roundings (P's and its own), else to its own; null: not asked for
   const uint64_t* rng;  // {seed, offset}; null: no dropout
   uint32_t drop_min;    // pieces below it drop their probability
   float drop_scale;     // 1 / (1 - drop_min / 2^15)

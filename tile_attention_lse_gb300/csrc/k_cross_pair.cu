@@ -22,6 +22,11 @@
 //    maxima are of all probabilities.  A tile with a bias that varies, with dropout or
 //    cut by the mask is read from TMEM twice, 32 scores at a time, in loops (under dropout all 128
 //    scores in registers gained 1 % without a bias and lost 15 % with one, to spills).
+//  - kFine, where `rest` is asked for under a bias: P goes into the second product in two parts, P rounded to bf16
+//    and what that lost, rounded to bf16 (2^-18 of P remain).  The backward takes D from o + rest, and a row's dS has to sum to 0
+//    with the float32 P that it forms again: an O of the rounded P alone leaves about 2^-9 |D| in every row, all of which a
+//    bucket that holds nearly all keys keeps.  The second part lies in the score columns of its
+//    tile, which are free for the next scores only behind that product then.
 // Measured, 8 sequences of 2048 queries and keys, 32 heads over 8 of 128 (16 over 16 of 64): 429 us, 1281 TFLOP/s
 // (212 us, 650); with a bias 602 (290); with dropout 826 (408); with both 933 (458).  The plain tile is bound by the
 // tensor pipe and the softmax as the paged kernel's is, dropout by the generator's integer instructions
@@ -113,7 +118,7 @@ __device__ __forceinline__ void arrive_cluster(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 
-template <int D, bool kBias, bool kDrop>
+template <int D, bool kBias, bool kDrop, bool kFine>
 __global__ void __launch_bounds__(kThreads, 1) cross_pair_kernel(const __grid_constant__ Params p) {
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t sbase = tc::smem_u32(smem);
@@ -297,9 +302,9 @@ __global__ void __launch_bounds__(kThreads, 1) cross_pair_kernel(const __grid_co
         const uint64_t qd = tc::kmajor_desc(sQ + qb * kQBytes);
         for (int t = 0; t < n && ok; ++t, ++g, ++kg) {
           const uint32_t sb = g % kSBufs;
-          // S buffer sb was last read by the softmax of tile g - 2
+          // S buffer sb was last read by the softmax of tile g - 2 (kFine: by the PV of its second part)
           if (g >= uint32_t(kSBufs)) {
-            ok = wt(B_SEMPTY0 + sb, ((g / kSBufs) - 1) & 1);
+            ok = wt((kFine ? B_PVDONE0 : B_SEMPTY0) + sb, ((g / kSBufs) - 1) & 1);
             if (!ok) break;
           }
           const uint32_t st = kg % kKStages;
@@ -345,6 +350,11 @@ __global__ void __launch_bounds__(kThreads, 1) cross_pair_kernel(const __grid_co
           for (int kk = 0; kk < 8; ++kk)  // P (bf16 pairs in TMEM) x V (MN-major smem)
             tc::mma_pair_ts(tmem + kColO, tmem + kColP + sb * 64 + kk * 8, tc::mnmajor_step(vd, kk), kIdescPV,
                             (t > 0 || kk > 0) ? 1u : 0u);
+          if (kFine) {
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk)  // what P lost to its rounding
+              tc::mma_pair_ts(tmem + kColO, tmem + sb * 128 + kk * 8, tc::mnmajor_step(vd, kk), kIdescPV, 1u);
+          }
           tc::mma_commit_pair(bar(B_PVDONE0 + sb), kBothCtas);
           tc::mma_commit_pair(bar(B_VEMPTY0 + vs), kBothCtas);
           if (t == n - 1) tc::mma_commit_pair(bar(B_ODONE), kBothCtas);
@@ -437,9 +447,11 @@ __global__ void __launch_bounds__(kThreads, 1) cross_pair_kernel(const __grid_co
             tc::tmem_wait_ld();
           }
           if (once || idle) {  // the scores are in registers: S_sb may take the next tile's scores
-            tc::fence_before_sync();
-            __syncwarp();
-            if (lane == 0) tc::mbar_arrive_remote(bar_even(B_SEMPTY0 + sb));
+            if (!kFine) {
+              tc::fence_before_sync();
+              __syncwarp();
+              if (lane == 0) tc::mbar_arrive_remote(bar_even(B_SEMPTY0 + sb));
+            }
             if (!idle) mx = fmaf(row_max<false>(sr, 0, kTile), sl2, add);
           } else {
 #pragma unroll 1
@@ -506,7 +518,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_pair_kernel(const __grid_co
           if (!idle) {
             const uint32_t tP = tmem + lane_off + kColP + sb * 64;
             if (once) {
-              l += p_pass<false>(sr, 0, kTile, mu - add, sl2x2, tP);
+              l += p_pass<false, kFine>(sr, 0, kTile, mu - add, sl2x2, tP, tS);
             } else {
               const float mul = kBias && near ? 1.f : sl2;
               const uint64_t mul2 = tc::f32x2(mul, mul), sub2 = tc::f32x2(add - mu, add - mu);
@@ -514,7 +526,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_pair_kernel(const __grid_co
               uint64_t sum2[2] = {0, 0};
 #pragma unroll 1
               for (int c = 0; c < 4; ++c) {
-                uint32_t s32[32], pk[16];
+                uint32_t s32[32], pk[16], low[16];
                 tc::tmem_ld32(tS + 32 * c, s32);
                 tc::tmem_wait_ld();
 #pragma unroll
@@ -534,17 +546,25 @@ __global__ void __launch_bounds__(kThreads, 1) cross_pair_kernel(const __grid_co
                     const float p0 = tc::ex2(x0), p1 = tc::ex2(x1);
                     sum2[w & 1] = tc::fadd2(sum2[w & 1], tc::f32x2(p0, p1));
                     pk[4 * u + w] = tc::pack_bf16x2(p0, p1);
-                    if (kDrop) pk[4 * u + w] &= keep_mask(dr.w[w], dkey.add);
+                    if (kFine) low[4 * u + w] = tc::rest_bf16x2(p0, p1);
+                    if (kDrop) {
+                      const uint32_t m = keep_mask(dr.w[w], dkey.add);
+                      pk[4 * u + w] &= m;
+                      if (kFine) low[4 * u + w] &= m;
+                    }
                   }
                 }
                 tc::tmem_st16(tP + 16 * c, pk);
+                if (kFine) tc::tmem_st16(tS + 16 * c, low);  // over scores of this pass that are read
               }
               float y0, y1;
               tc::f32x2_split(tc::fadd2(sum2[0], sum2[1]), y0, y1);
               l += y0 + y1;
-              tc::fence_before_sync();
-              __syncwarp();
-              if (lane == 0) tc::mbar_arrive_remote(bar_even(B_SEMPTY0 + sb));
+              if (!kFine) {
+                tc::fence_before_sync();
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive_remote(bar_even(B_SEMPTY0 + sb));
+              }
             }
             if (t > 0 && __any_sync(0xffffffffu, grow)) {
               // O holds the sum up to tile g - 1 against m_in once the PV that
@@ -755,12 +775,15 @@ cudaLaunchConfig_t pair_config(cudaLaunchAttribute* attr, int pairs, bool early,
 using Kernel = void (*)(Params);
 template <int D>
 Kernel pair_kernel_of(int copy) {
-  return copy == 3   ? cross_pair_kernel<D, true, true>
-         : copy == 2 ? cross_pair_kernel<D, true, false>
-         : copy == 1 ? cross_pair_kernel<D, false, true>
-                     : cross_pair_kernel<D, false, false>;
+  return copy == 5   ? cross_pair_kernel<D, true, true, true>
+         : copy == 4 ? cross_pair_kernel<D, true, false, true>
+         : copy == 3 ? cross_pair_kernel<D, true, true, false>
+         : copy == 2 ? cross_pair_kernel<D, true, false, false>
+         : copy == 1 ? cross_pair_kernel<D, false, true, false>
+                     : cross_pair_kernel<D, false, false, false>;
 }
-int copy_of(const CrossArgs& a) { return (a.rel ? 2 : 0) + (a.rng ? 1 : 0); }
+constexpr int kCopies = 6;
+int copy_of(const CrossArgs& a) { return (a.rel ? a.rest ? 4 : 2 : 0) + (a.rng ? 1 : 0); }
 Kernel pair_kernel(const CrossArgs& a) { return a.d == 128 ? pair_kernel_of<128>(copy_of(a)) : pair_kernel_of<64>(copy_of(a)); }
 
 }  // namespace
@@ -769,8 +792,8 @@ Kernel pair_kernel(const CrossArgs& a) { return a.d == 128 ? pair_kernel_of<128>
 cp_status cross_pair_grid(const CrossArgs& a, int32_t* pairs) {
   const Kernel kern = pair_kernel(a);
   // per copy and device, set up by the first launch (under a lock: host threads may race on it)
-  static std::atomic<int> max_pairs[8][64] = {};
-  const int copy = (a.d == 128 ? 4 : 0) + copy_of(a);
+  static std::atomic<int> max_pairs[2 * kCopies][64] = {};
+  const int copy = (a.d == 128 ? kCopies : 0) + copy_of(a);
   static std::mutex setup_mu;
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return CP_ERR_CUDA;
