@@ -218,6 +218,13 @@ def test_rows_that_see_few_keys():
     assert np.all(np.abs(f64(with_rest[0][0])) <= (f + 2 * U16 ** 2) * want["mag_dq"][0] + 1e-30)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("nk", [2, 3, 4])
+def test_every_row_over_few_keys(nk, d):
+    """Without a causal mask or a bias too: scores without a scale lie on one key nearly, where dP - D cancels."""
+    check(Case([(9, nk)] * 40, H=8, Hkv=2, d=d, p=0.1, scale=1.0))
+
+
 def test_table_gradient_without_the_rest():
     """Without what o lost to its rounding, D is off by u16 of the sum of |dO| |o|."""
     c = Case(RAGGED, rel=REL["both"], d=64)
