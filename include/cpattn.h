@@ -582,7 +582,8 @@ cp_status cp_paged_schedule(const cp_paged_desc* desc, int32_t n_reqs, int64_t r
  * again wherever it is needed and never stored: counter words (j / 8, i,
  * b * heads_q + h, low half of rng[1]), key rng[0] (low half first); of the four words of a draw,
  * element e = j % 8 takes the low 15 bits of half e % 2 (0: low) of word e / 2, and is
- * kept iff that number >= round(dropout * 2^15).  1 - p is taken after
+ * kept iff that number >= round(dropout * 2^15) (to the nearest, halves to even; dropout is a float: a caller who holds a
+ * double rounds it to a multiple of 2^-15 first, which a float holds exactly).  1 - p is taken after
  * that rounding.  rng [2] (seed, offset) lies in device memory; the backward takes the same two numbers.
  * ------------------------------------------------------------------------ */
 typedef struct {

@@ -42,7 +42,7 @@ def philox(ctr, key, rounds=7):
 
 def keep(nq, nk, seq_head, p, seed, offset):
     """Which pairs dropout keeps, and the probability that it drops with."""
-    cut = int(math.floor(p * 32768 + 0.5))
+    cut = round(p * 32768)  # halves to even
     i, j = np.meshgrid(np.arange(nq), np.arange(nk), indexing="ij")
     words = philox((j // 8, i, np.full_like(i, seq_head), np.full_like(i, offset % 2 ** 32)),
                    (seed % 2 ** 32, (seed >> 32) % 2 ** 32))

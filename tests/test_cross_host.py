@@ -49,6 +49,16 @@ def test_bucket_refusals(buckets, distance, both, want):
     assert api.validate_cross(problem(rel=api.RelBuckets(buckets, distance, both))) == want
 
 
+def test_dropout_is_rounded_once():
+    """The nearest multiple of 2^-15 of the caller's double, halves to even, which the descriptor's float holds."""
+    for k in (0, 1, 2, 3276, 3277, 9830, 20000, 20001, 32766):
+        for p in (k / 32768, (k + 0.5) / 32768, np.nextafter((k + 0.5) / 32768, 0), np.nextafter((k + 0.5) / 32768, 1)):
+            got = problem(dropout=p)
+            assert got._desc.dropout * 32768 == round(p * 32768) == round(got.dropout * 32768), p
+    near = problem(dropout=1e-6)                                            # as none: no rng is asked for
+    assert near.dropout == 0.0 and fwd(near, wb=16) == WORK
+
+
 def test_workspace_sizes():
     w = api.cross_workspace_bytes
     p = problem()

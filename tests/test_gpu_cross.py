@@ -398,6 +398,25 @@ def test_dropped_share_and_seeds():
     assert torch.equal(o, c.forward()[0])
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("k", [3276, 9831])
+@pytest.mark.parametrize("side", [-1, 0, 1])
+def test_dropout_next_to_a_border(side, k, dtype):
+    """p at (k + 1/2) / 2^15 and the doubles beside it: which pairs are kept, counted row by row."""
+    p = np.nextafter((k + 0.5) / 32768, (0, 1)[side > 0]) if side else (k + 0.5) / 32768
+    c = Case([(1500, 64)], H=16, Hkv=16, d=64, dtype=dtype, p=p)  # 1.5 million pairs: 47 for each threshold
+    c.q.zero_()
+    c.v.fill_(1.0)                                                # o: the kept of 64 keys / (64 (1 - p))
+    counts = np.stack([X.keep(1500, 64, h, p, c.seed, c.offset)[0].sum(1) for h in range(16)], 1)
+    pe = round(p * 32768) / 32768
+    rows = lambda o: np.rint(f64(o[:, :, 0]) * 64 * (1 - pe))     # noqa: E731  (a step of 64 is 4 u16 and more)
+    assert np.array_equal(rows(c.forward()[0]), counts)
+    c.problem._desc.dropout = (k + 0.5) / 32768                   # a float's half, past the binding
+    cut = round(k + 0.5)
+    counts = np.stack([X.keep(1500, 64, h, cut / 32768, c.seed, c.offset)[0].sum(1) for h in range(16)], 1)
+    assert np.array_equal(rows(c.forward()[0]), counts)
+
+
 def test_dropout_of_nearly_nothing_and_nearly_all():
     for p in (1e-6, 0.999):
         for dtype in (BF, F32):

@@ -677,13 +677,16 @@ class CrossProblem:
     """Attention of packed query sequences over packed key sequences (cp_cross_desc).
 
     max_q: about how many queries a sequence has at most (chooses the forward's
-    kernel; 0: many); rel: a bias by buckets of the relative position; dropout: of the probabilities."""
+    kernel; 0: many); rel: a bias by buckets of the relative position; dropout: of the probabilities, to the
+    nearest multiple of 2^-15 (halves to even)."""
 
     def __init__(self, heads_q: int, heads_kv: int, head_dim: int, dtype: torch.dtype = torch.bfloat16,
                  causal: bool = False, max_q: int = 0, rel: RelBuckets | None = None, dropout: float = 0.0,
                  softmax_scale: float = 0.0):
         self.heads_q, self.heads_kv, self.head_dim, self.dtype = int(heads_q), int(heads_kv), int(head_dim), dtype
         self.rel, self.dropout, self.causal = rel, float(dropout), bool(causal)
+        if 0.0 < self.dropout < 1.0:  # here, in 64 bits: a float next to a border rounds to the other side
+            self.dropout = round(self.dropout * 32768) / 32768
         r = (rel.buckets, rel.max_distance, int(rel.both)) if rel is not None else (0, 0, 0)
         self._desc = CpCrossDesc(self.heads_q, self.heads_kv, self.head_dim, _dtype_code(dtype), int(bool(causal)),
                                  int(max_q), *r, self.dropout, float(softmax_scale))

@@ -19,8 +19,11 @@ int64_t elem(cp_dtype t) { return t == CP_BF16 ? 2 : 4; }
 bool row_ok(const void* p, int64_t stride, cp_dtype t) { return aligned(p, 16) && stride * elem(t) % 16 == 0; }
 size_t up256(size_t n) { return (n + 255) & ~size_t(255); }
 
-// Pieces of 15 bits below this one drop their probability.
-uint32_t drop_min(const cp_cross_desc& d) { return uint32_t(std::lround(double(d.dropout) * 32768.0)); }
+// Pieces of 15 bits below this one drop their probability: p 2^15 to the nearest, halves to even.
+uint32_t drop_min(const cp_cross_desc& d) {
+  const double x = double(d.dropout) * 32768.0, low = std::floor(x), over = x - low;
+  return uint32_t(low) + (over > 0.5 || (over == 0.5 && (int64_t(low) & 1)) ? 1 : 0);
+}
 
 cp_status check(const cp_cross_desc* d) {
   if (!d || d->heads_q < 1 || d->heads_kv < 1 || d->max_q < 0) return CP_ERR_INVALID_ARG;
