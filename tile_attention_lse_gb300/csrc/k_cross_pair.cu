@@ -25,8 +25,9 @@
 //  - kFine, where `rest` is asked for under a bias: P goes into the second product in two parts, P rounded to bf16
 //    and what that lost, rounded to bf16 (2^-18 of P remain).  The backward takes D from o + rest, and a row's dS has to sum to 0
 //    with the float32 P that it forms again: an O of the rounded P alone leaves about 2^-9 |D| in every row, all of which a
-//    bucket that holds nearly all keys keeps.  The second part lies in the score columns of its
-//    tile, which are free for the next scores only behind that product then.
+//    bucket that holds nearly all keys keeps.  Both parts lie over the scores that they come from, 32 columns for
+//    32 keys, so that the columns of P_0 and P_1 hold a third tile's scores: a tile's are free for the next ones behind its
+//    second product only, and with two of them the softmax waited for that (8 x 2048 with a bias 912 and 427 us).
 // Measured, 8 sequences of 2048 queries and keys, 32 heads over 8 of 128 (16 over 16 of 64): 429 us, 1281 TFLOP/s
 // (212 us, 650); with a bias 602 (290); with dropout 826 (408); with both 933 (458).  The plain tile is bound by the
 // tensor pipe and the softmax as the paged kernel's is, dropout by the generator's integer instructions
@@ -64,7 +65,8 @@ static_assert(128 * kSmallRegs + 256 * kSoftmaxRegs == kThreads * kLaunchRegs,
 constexpr uint32_t kQBytes = 128 * 128 * 2, kQHalf = kQBytes / 2;  // this CTA's Q tile, one 64-column box of it
 constexpr uint32_t kKBytes = 64 * 128 * 2;                         // its half of a key tile (64 keys), head_dim 128
 constexpr uint32_t kVBytes = 128 * 64 * 2;                         // its half of a value tile (64 columns)
-constexpr int kQBufs = 2, kKStages = 4, kVStages = 4, kSBufs = 2;
+constexpr int kQBufs = 2, kKStages = 4, kVStages = 4;
+constexpr int kSBufs = 3;  // places for a tile's scores: 2, and 3 with kFine
 constexpr int kOffQ = 0;
 constexpr int kOffK = kOffQ + kQBufs * kQBytes;
 constexpr int kOffV = kOffK + kKStages * kKBytes;
@@ -101,9 +103,10 @@ static_assert(8 * B_COUNT + 8 <= 512, "barrier area");
 
 constexpr uint32_t kIdescS = tc::idesc_bf16(256, 128, /*b_mn_major=*/0);
 constexpr uint32_t kIdescPV = tc::idesc_bf16(256, 128, /*b_mn_major=*/1);
-// TMEM columns: S_0, S_1 (128 each), P_0, P_1 (64 each), O (128): 512.
-constexpr uint32_t kColP = kSBufs * 128;
-constexpr uint32_t kColO = kColP + kSBufs * 64;
+// TMEM columns: S_0, S_1 (128 each), P_0, P_1 (64 each), O (128): 512.  kFine: S_0, S_1, S_2, O.
+constexpr uint32_t kColP = 2 * 128;
+constexpr uint32_t kColO = kColP + 2 * 64;
+static_assert(kSBufs * 128 == kColO, "three places for scores");
 static_assert(kColO + 128 == 512, "TMEM columns");
 constexpr uint16_t kBothCtas = 0x3;
 
@@ -120,6 +123,7 @@ __device__ __forceinline__ void arrive_cluster(uint32_t cluster_addr) {
 
 template <int D, bool kBias, bool kDrop, bool kFine>
 __global__ void __launch_bounds__(kThreads, 1) cross_pair_kernel(const __grid_constant__ Params p) {
+  constexpr uint32_t kBufs = kFine ? 3 : 2;  // places for a tile's scores
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t sbase = tc::smem_u32(smem);
   if (sbase & 1023) {  // the swizzled layouts need a 1 KB aligned base (the same in both CTAs)
@@ -301,10 +305,10 @@ __global__ void __launch_bounds__(kThreads, 1) cross_pair_kernel(const __grid_co
         tc::fence_after_sync();
         const uint64_t qd = tc::kmajor_desc(sQ + qb * kQBytes);
         for (int t = 0; t < n && ok; ++t, ++g, ++kg) {
-          const uint32_t sb = g % kSBufs;
-          // S buffer sb was last read by the softmax of tile g - 2 (kFine: by the PV of its second part)
-          if (g >= uint32_t(kSBufs)) {
-            ok = wt((kFine ? B_PVDONE0 : B_SEMPTY0) + sb, ((g / kSBufs) - 1) & 1);
+          const uint32_t sb = g % kBufs;
+          // S buffer sb was last read by the softmax of tile g - 2 (kFine: by the PV of tile g - 3)
+          if (g >= kBufs) {
+            ok = wt((kFine ? B_PVDONE0 : B_SEMPTY0) + sb, ((g / kBufs) - 1) & 1);
             if (!ok) break;
           }
           const uint32_t st = kg % kKStages;
@@ -338,22 +342,24 @@ __global__ void __launch_bounds__(kThreads, 1) cross_pair_kernel(const __grid_co
         }
         ++items;
         for (int t = 0; t < n && ok; ++t, ++g, ++vg) {
-          const uint32_t sb = g % kSBufs;
-          ok = wt(B_PFULL0 + sb, (g / kSBufs) & 1);
+          const uint32_t sb = g % kBufs;
+          ok = wt(B_PFULL0 + sb, (g / kBufs) & 1);
           if (!ok) break;
           const uint32_t vs = vg % kVStages;
           ok = wt(B_VFULL0 + vs, (vg / kVStages) & 1);
           if (!ok) break;
           tc::fence_after_sync();
           const uint64_t vd = tc::mnmajor_desc(sV + vs * kVBytes);
+          // P (bf16 pairs in TMEM) x V (MN-major smem); kFine: 16 columns of P and 16 of what it lost in turn
 #pragma unroll
-          for (int kk = 0; kk < 8; ++kk)  // P (bf16 pairs in TMEM) x V (MN-major smem)
-            tc::mma_pair_ts(tmem + kColO, tmem + kColP + sb * 64 + kk * 8, tc::mnmajor_step(vd, kk), kIdescPV,
-                            (t > 0 || kk > 0) ? 1u : 0u);
+          for (int kk = 0; kk < 8; ++kk)
+            tc::mma_pair_ts(tmem + kColO, tmem + (kFine ? sb * 128 + (kk >> 1) * 32 + (kk & 1) * 8 : kColP + sb * 64 + kk * 8),
+                            tc::mnmajor_step(vd, kk), kIdescPV, (t > 0 || kk > 0) ? 1u : 0u);
           if (kFine) {
 #pragma unroll
-            for (int kk = 0; kk < 8; ++kk)  // what P lost to its rounding
-              tc::mma_pair_ts(tmem + kColO, tmem + sb * 128 + kk * 8, tc::mnmajor_step(vd, kk), kIdescPV, 1u);
+            for (int kk = 0; kk < 8; ++kk)
+              tc::mma_pair_ts(tmem + kColO, tmem + sb * 128 + (kk >> 1) * 32 + (kk & 1) * 8 + 16, tc::mnmajor_step(vd, kk),
+                              kIdescPV, 1u);
           }
           tc::mma_commit_pair(bar(B_PVDONE0 + sb), kBothCtas);
           tc::mma_commit_pair(bar(B_VEMPTY0 + vs), kBothCtas);
@@ -419,8 +425,8 @@ __global__ void __launch_bounds__(kThreads, 1) cross_pair_kernel(const __grid_co
         float m_own = -INFINITY, l = 0.f;  // this warp's row sum and the max it is taken against
         for (int t = 0; t < n && ok; ++t, ++g) {
           if (int(g & 1) != half) continue;  // the other warp's tile
-          const uint32_t sb = g % kSBufs;
-          ok = __all_sync(0xffffffffu, wt(B_SFULL0 + sb, (g / kSBufs) & 1));
+          const uint32_t sb = g % kBufs;
+          ok = __all_sync(0xffffffffu, wt(B_SFULL0 + sb, (g / kBufs) & 1));
           if (!ok) break;
           tc::fence_after_sync();
           // visible keys of this row in this tile: lo <= j < limit
@@ -509,16 +515,18 @@ __global__ void __launch_bounds__(kThreads, 1) cross_pair_kernel(const __grid_co
           }
           const float mu = (m == -INFINITY) ? 0.f : m;
           // P buffer sb was last read by the PV of tile g - 2 (this warp waits
-          // for every such phase, in order)
-          if (g >= uint32_t(kSBufs)) {
-            ok = __all_sync(0xffffffffu, wt(B_PVDONE0 + sb, ((g / kSBufs) - 1) & 1));
+          // for every such phase, in order).  kFine: of tile g - 3, behind which the scores came already; this warp waits for
+          // every second phase of a barrier then, and the one between is complete: PV(g - 6) as PV(g - 5) is, waited for at
+          // tile g - 2.  (S(g - 3), the phase before S(g)'s, likewise: tile g - 2 waited for the max after it.)
+          if (g >= kBufs) {
+            ok = __all_sync(0xffffffffu, wt(B_PVDONE0 + sb, ((g / kBufs) - 1) & 1));
             if (!ok) break;
             tc::fence_after_sync();
           }
           if (!idle) {
             const uint32_t tP = tmem + lane_off + kColP + sb * 64;
             if (once) {
-              l += p_pass<false, kFine>(sr, 0, kTile, mu - add, sl2x2, tP, tS);
+              l += p_pass<false, kFine>(sr, 0, kTile, mu - add, sl2x2, kFine ? tS : tP);
             } else {
               const float mul = kBias && near ? 1.f : sl2;
               const uint64_t mul2 = tc::f32x2(mul, mul), sub2 = tc::f32x2(add - mu, add - mu);
@@ -526,7 +534,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_pair_kernel(const __grid_co
               uint64_t sum2[2] = {0, 0};
 #pragma unroll 1
               for (int c = 0; c < 4; ++c) {
-                uint32_t s32[32], pk[16], low[16];
+                uint32_t s32[32], pk[32];  // 16 pairs, and with kFine what they lost
                 tc::tmem_ld32(tS + 32 * c, s32);
                 tc::tmem_wait_ld();
 #pragma unroll
@@ -546,16 +554,18 @@ __global__ void __launch_bounds__(kThreads, 1) cross_pair_kernel(const __grid_co
                     const float p0 = tc::ex2(x0), p1 = tc::ex2(x1);
                     sum2[w & 1] = tc::fadd2(sum2[w & 1], tc::f32x2(p0, p1));
                     pk[4 * u + w] = tc::pack_bf16x2(p0, p1);
-                    if (kFine) low[4 * u + w] = tc::rest_bf16x2(p0, p1);
+                    if (kFine) pk[16 + 4 * u + w] = tc::rest_bf16x2(p0, p1);
                     if (kDrop) {
                       const uint32_t m = keep_mask(dr.w[w], dkey.add);
                       pk[4 * u + w] &= m;
-                      if (kFine) low[4 * u + w] &= m;
+                      if (kFine) pk[16 + 4 * u + w] &= m;
                     }
                   }
                 }
-                tc::tmem_st16(tP + 16 * c, pk);
-                if (kFine) tc::tmem_st16(tS + 16 * c, low);  // over scores of this pass that are read
+                if (kFine)
+                  tc::tmem_st32(tS + 32 * c, pk);
+                else
+                  tc::tmem_st16(tP + 16 * c, pk);
               }
               float y0, y1;
               tc::f32x2_split(tc::fadd2(sum2[0], sum2[1]), y0, y1);
@@ -571,9 +581,10 @@ __global__ void __launch_bounds__(kThreads, 1) cross_pair_kernel(const __grid_co
               // read P of tile g - 1 is complete (the next PV waits for this P).
               // That phase is the latest one of its barrier: PV(g - 3) is
               // complete (PV(g - 2) is, see above) and PV(g + 1) waits for PV(g).
+              // (kFine: PV(g - 4) is, as PV(g - 3) is, and PV(g + 2) waits for PV(g).)
               const float corr = (m_in == -INFINITY) ? 0.f : tc::ex2(m_in - m);
-              const uint32_t pb = (g - 1) % kSBufs;
-              ok = __all_sync(0xffffffffu, wt(B_PVDONE0 + pb, ((g - 1) / kSBufs) & 1));
+              const uint32_t pb = (g - 1) % kBufs;
+              ok = __all_sync(0xffffffffu, wt(B_PVDONE0 + pb, ((g - 1) / kBufs) & 1));
               if (!ok) break;
               tc::fence_after_sync();
 #pragma unroll

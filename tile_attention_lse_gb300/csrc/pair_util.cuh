@@ -35,15 +35,15 @@ __device__ __forceinline__ float row_max(const uint32_t* sr, int lo, uint32_t sp
 // P = exp2(s * scale_log2 - mu) over the 128 scores of a row: bf16 pairs are
 // written over the row's S columns (keys 2c, 2c+1 -> column c) and the row
 // sum of the fp32 values is returned.  kMasked keeps keys lo <= j < lo + span.
-// kRest: what the pairs lost to their rounding is written to tR's columns.
+// kRest: the pairs of 32 keys, then what these lost to their rounding, over the same 32 columns.
 template <bool kMasked, bool kRest = false>
 __device__ __forceinline__ float p_pass(const uint32_t* sr, int lo, uint32_t span, float mu, uint64_t sl2x2,
-                                        uint32_t tS, uint32_t tR = 0) {
+                                        uint32_t tS) {
   const uint64_t nmu = tc::f32x2(-mu, -mu);
   uint64_t ls[4] = {tc::f32x2(0.f, 0.f), tc::f32x2(0.f, 0.f), tc::f32x2(0.f, 0.f), tc::f32x2(0.f, 0.f)};
 #pragma unroll
   for (int cc = 0; cc < 4; ++cc) {
-    uint32_t pk[16], low[16];
+    uint32_t pk[32];
 #pragma unroll
     for (int e = 0; e < 16; ++e) {
       const int j0 = cc * 32 + 2 * e;
@@ -57,10 +57,12 @@ __device__ __forceinline__ float p_pass(const uint32_t* sr, int lo, uint32_t spa
       const float p0 = tc::ex2(x0), p1 = tc::ex2(x1);
       ls[e & 3] = tc::fadd2(ls[e & 3], tc::f32x2(p0, p1));
       pk[e] = tc::pack_bf16x2(p0, p1);
-      if (kRest) low[e] = tc::rest_bf16x2(p0, p1);
+      if (kRest) pk[16 + e] = tc::rest_bf16x2(p0, p1);
     }
-    tc::tmem_st16(tS + cc * 16, pk);
-    if (kRest) tc::tmem_st16(tR + cc * 16, low);
+    if (kRest)
+      tc::tmem_st32(tS + cc * 32, pk);
+    else
+      tc::tmem_st16(tS + cc * 16, pk);
   }
   float x, y;
   tc::f32x2_split(tc::fadd2(tc::fadd2(ls[0], ls[1]), tc::fadd2(ls[2], ls[3])), x, y);
