@@ -614,7 +614,7 @@ size_t cp_cross_attn_workspace_bytes(const cp_cross_desc* desc, int32_t n_seqs, 
 /* Forward: o [rows_q][heads_q][head_dim], lse [rows_q][heads_q] float32, natural log (as cp_tile_attn_fwd gives
  * them, and without dropout fit to be merged by cp_merge_partials).  q [rows_q][heads_q][head_dim], k and v
  * [rows_k][heads_kv][head_dim] with row strides in elements (slices of one projection).  bias
- * [rel_buckets][heads_q] (NULL iff rel_buckets is 0).  rest (bf16 only, layout of o, up to 128 q-heads a kv-head; NULL: not wanted): what o
+ * [rel_buckets][heads_q] (NULL iff rel_buckets is 0).  rest (bf16 only, layout of o, with a bias up to 128 q-heads a kv-head; NULL: not wanted): what o
  * lost, for cp_cross_attn_bwd.  With a bias o + rest is the output to at most 2^-16 of sum_j P_ij keep_ij / (1 - p) |v_j|
  * (in the mean 2^-17 of the output): P goes into the second product in two parts.  Without one P is rounded to bf16 there (2^-8 of
  * P at most, as in every call without rest) and rest is what o's own rounding took.  Rows that no sequence owns are not read, and

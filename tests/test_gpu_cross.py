@@ -225,6 +225,20 @@ def test_every_row_over_few_keys(nk, d):
     check(Case([(9, nk)] * 40, H=8, Hkv=2, d=d, p=0.1, scale=1.0))
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("H,Hkv,nq", [(8, 2, 1), (8, 2, 4), (8, 2, 7), (16, 16, 2), (160, 1, 2)])
+def test_rest_of_few_rows(H, Hkv, nq, d):
+    """The slices leave rest too: whole tiles, cut ones (joined by the merge), rows of padding and more heads than a tile has."""
+    c = Case([(nq, n) for n in (2, 777, 1, 0, 64, 3, 9000)], H=H, Hkv=Hkv, d=d, max_q=nq, scale=1.0, pad_q=1, tail=2)
+    o, lse, rest = c.forward()
+    assert rest is not None
+    want = check_forward(c, o, lse, rest, c.oracle())
+    check_backward(c, c.backward(o, lse, rest), want)
+    own = torch.from_numpy(c.owned(False)).to(DEV)
+    plain = api.cross_attn_fwd(c.problem, c.q, c.k, c.v, *c.dcu, **c.at)
+    assert torch.equal(o[own], plain[0][own]) and torch.equal(lse[own], plain[1][own])
+
+
 def test_table_gradient_without_the_rest():
     """Without what o lost to its rounding, D is off by u16 of the sum of |dO| |o|."""
     c = Case(RAGGED, rel=REL["both"], d=64)

@@ -754,7 +754,7 @@ def cross_attn_fwd(p: CrossProblem, q, k, v, cu_q, cu_k, len_q=None, len_k=None,
     sequence by sequence (cp_cross_attn_fwd) -> (o, lse).  Rows that no sequence owns are
     left as they were (unset in a new o and lse).  for_backward: -> (o, lse, rest), rest what o lost
     to rounding, which cross_attn_bwd takes (the gradients of rows whose weight lies on few keys, and a bias table's; None
-    in float32 and for more than 128 q-heads a kv-head)."""
+    in float32, and with a bias for more than 128 q-heads a kv-head)."""
     dev, n, rows_q, rows_k, qkv, cu, bias, rng = _cross_inputs(p, q, k, v, cu_q, cu_k, len_q, len_k, bias, rng)
     s = _stream_of(dev)
     ws = _cross_ws(p, ws, n, rows_q, rows_k, False, dev)
@@ -762,7 +762,7 @@ def cross_attn_fwd(p: CrossProblem, q, k, v, cu_q, cu_k, len_q=None, len_k=None,
     out = _new(out, "out", (rows_q, heads, d), p.dtype, dev)
     lse = _new(lse, "lse", (rows_q, heads), _F32, dev)
     rest = None
-    if for_backward and p.dtype is torch.bfloat16 and heads <= 128 * p.heads_kv:
+    if for_backward and p.dtype is torch.bfloat16 and (bias is None or heads <= 128 * p.heads_kv):
         rest = _new(None, "rest", (rows_q, heads, d), p.dtype, dev)
     _check(lib().cp_cross_attn_fwd(p._ref, n, rows_q, rows_k, *qkv, *cu, bias, rng, out.data_ptr(),
                                    None if rest is None else rest.data_ptr(), lse.data_ptr(), ws.data_ptr(), ws.nbytes, s),

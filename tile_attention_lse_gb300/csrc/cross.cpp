@@ -94,12 +94,13 @@ RelLayout rel_layout(const cp_cross_desc& d) {
 // bf16: up to 16 and up to 32 rows are bound by the bytes of their keys and run on the slice
 // kernel, more on the pair kernel, as in the paged attention (serve.cpp has both sides
 // measured), and so does all dropout.  Groups wider than the pair kernel's tile stay on slices.
-// What o loses to its rounding is written by the pair kernel only.
+// With rest under a bias P goes into its product in two parts, which is the pair kernel's
+// (64 sequences of 2 queries over 2000 keys, 16 heads of 64, with a bias: 95 us on slices, 352 so).
 // float32 is all the slice kernel's.
 PagedKernel pick(const cp_cross_desc& d, bool rest) {
   const int64_t G = d.heads_q / d.heads_kv, rows = d.max_q > 0 ? G * d.max_q : INT64_MAX;
   if (d.dtype == CP_F32) return rows <= 4 ? kPagedSlice4 : kPagedSlice16;
-  if (d.dropout > 0.f || (rest && G <= kPairRows)) return kPagedPair;
+  if (d.dropout > 0.f || (rest && d.rel_buckets)) return kPagedPair;
   if (rows <= 16 || G > kPairRows) return kPagedSlice16;
   return rows <= 32 ? kPagedSlice32 : kPagedPair;
 }
@@ -120,7 +121,8 @@ struct Layout {
 Layout layout(const cp_cross_desc& d, int64_t rows_q, int64_t rows_k, int32_t n_seqs, bool backward) {
   Layout l;
   l.states = up256(size_t(d.heads_q) * rel_layout(d).stride * 4);
-  const int64_t states = std::max(fwd_states(d, pick(d, false)), fwd_states(d, pick(d, true)));
+  const bool fine = d.dtype == CP_BF16 && d.heads_q / d.heads_kv <= kPairRows;  // a rest may be asked for
+  const int64_t states = std::max(fwd_states(d, pick(d, false)), fwd_states(d, pick(d, fine)));
   l.total = l.states + size_t(states) * (size_t(d.head_dim) + 1) * 4;
   if (!backward) return l;
   const bool bf16 = d.dtype == CP_BF16;
@@ -254,7 +256,7 @@ cp_status cp_cross_attn_fwd(const cp_cross_desc* desc, int32_t n_seqs, int64_t r
   if (st != CP_OK) return st;
   if (!o || !lse || !ws || !aligned(ws, 256)) return CP_ERR_INVALID_ARG;
   if (rest && desc->dtype != CP_BF16) return CP_ERR_INVALID_ARG;
-  if (rest && desc->heads_q / desc->heads_kv > kPairRows) return CP_ERR_UNSUPPORTED;
+  if (rest && bias && desc->heads_q / desc->heads_kv > kPairRows) return CP_ERR_UNSUPPORTED;
   if (!aligned(o, 16) || !aligned(rest, 16)) return CP_ERR_ALIGNMENT;
   const Layout l = layout(*desc, rows_q, rows_k, n_seqs, false);
   if (ws_bytes < l.total) return CP_ERR_WORKSPACE;

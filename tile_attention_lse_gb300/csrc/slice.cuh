@@ -92,6 +92,7 @@ template <typename T, int D, int R>
 struct SliceOut {
   T* o;         // final O, or
   float* part;  // partial O
+  T* rest;      // what a final O in bf16 lost to its rounding; null: not asked for
   float* lse;
   bool in, whole;
   template <class A>
@@ -103,15 +104,21 @@ struct SliceOut {
     const int64_t row = int64_t(p.q0 + t) * a.H + p.h * a.G + (x - t * a.G), prow = int64_t(p.slot) * R + r;
     o = static_cast<T*>(a.o) + row * D;
     part = a.part_o + prow * D;
+    rest = nullptr;
+    if constexpr (A::kDense && sizeof(T) == 2) {
+      if (a.rest) rest = static_cast<T*>(a.rest) + row * D;
+    }
     lse = whole ? a.lse + row : a.part_l + prow;
   }
   template <int N>
   __device__ __forceinline__ void put(int c, const float* x) const {
     if (!in) return;
-    if (whole)
-      store_vec<T, N>(o + c, x);
-    else
-      store_vec<float, N>(part + c, x);
+    if (!whole) return store_vec<float, N>(part + c, x);
+    store_vec<T, N>(o + c, x);
+    if constexpr (sizeof(T) == 2) {
+      if (rest) *reinterpret_cast<uint32_t*>(rest + c) = tc::rest_bf16x2(x[0], x[1]);
+      static_assert(N == 2, "a pair");
+    }
   }
   __device__ __forceinline__ void put_lse(float log2_sum) const {
     if (in) *lse = whole ? log2_sum * 0.69314718055994531f : log2_sum;
