@@ -332,6 +332,20 @@ def test_output_and_rest_under_a_bias(seqs, rel, p, d):
     check_forward(c, o, lse, None, want)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("nq,nk", [(2, 60000), (20000, 70)])
+def test_long_sums_in_float32(nq, nk, d):
+    """dQ over many keys, dK and dV over many queries: tiles of 64 are summed apart, then n / 64 of them.
+
+    A chain of t sums of mixed sign is off by sqrt(t / 2) roundings of 0.42 u32 (a half step's root mean square) of its end:
+    9 u32 for 940 tiles; P and dS by 6 u32 in the mean (scores 3, exponents 2, D): 11 u32 together, doubled."""
+    c = Case([(nq, nk)], H=2, Hkv=1, d=d, dtype=F32)
+    o, lse, rest = c.forward()
+    want = c.oracle()
+    for got, name in zip(c.backward(o, lse, rest), ("dq", "dk", "dv")):
+        assert np.linalg.norm(f64(got) - want[name]) <= 22 * U32 * np.linalg.norm(want[name]), name
+
+
 def test_fused_and_padded_inputs():
     for dtype in (BF, F32):
         check(Case(RAGGED, dtype=dtype, fused=True, pad=37, pad_q=11, tail=5, rel=REL["both"], p=0.2))
