@@ -576,7 +576,7 @@ cp_status cp_paged_schedule(const cp_paged_desc* desc, int32_t n_reqs, int64_t r
  * ceil(e (rel_max_distance / e)^(t / (per - e)) (1 - 1e-12)), t = 0 .. per - e - 1
  * (floating point; the last factor puts a distance that lies on a border behind it).
  * Table entries below -1e30 mask their pairs (a row of only such sees no key, and
- * their gradient is 0); the others are finite.
+ * their gradient is 0); the others are 1e30 at most.
  *
  * Dropout: keep_ij comes from Philox4x32 with 7 rounds (Salmon et al., 2011), drawn
  * again wherever it is needed and never stored: counter words (j / 8, i,
@@ -614,10 +614,11 @@ size_t cp_cross_attn_workspace_bytes(const cp_cross_desc* desc, int32_t n_seqs, 
 /* Forward: o [rows_q][heads_q][head_dim], lse [rows_q][heads_q] float32, natural log (as cp_tile_attn_fwd gives
  * them, and without dropout fit to be merged by cp_merge_partials).  q [rows_q][heads_q][head_dim], k and v
  * [rows_k][heads_kv][head_dim] with row strides in elements (slices of one projection).  bias
- * [rel_buckets][heads_q] (NULL iff rel_buckets is 0).  rest (bf16 only, layout of o, with a bias up to 128 q-heads a kv-head; NULL: not wanted): what o
- * lost, for cp_cross_attn_bwd.  With a bias o + rest is the output to at most 2^-16 of sum_j P_ij keep_ij / (1 - p) |v_j|
- * (in the mean 2^-17 of the output): P goes into the second product in two parts.  Without one P is rounded to bf16 there (2^-8 of
- * P at most, as in every call without rest) and rest is what o's own rounding took.  Rows that no sequence owns are not read, and
+ * [rel_buckets][heads_q] (NULL iff rel_buckets is 0).  rest (bf16 only, layout of o, with a bias up to 128 q-heads
+ * a kv-head; NULL: not wanted): what o lost, for cp_cross_attn_bwd.  With a bias o + rest is the output to at most
+ * 2^-16 of sum_j P_ij keep_ij / (1 - p) |v_j| (in the mean 2^-17 of the output): P goes into the second product in
+ * two parts.  Without one P is rounded to bf16 there (2^-8 of P at most, as in every call without rest) and rest is
+ * what o's own rounding took.  Rows that no sequence owns are not read, and
  * left as they were in o, rest and lse.  o and lse must not overlap the inputs.  A K/V value that is not finite reaches
  * every row of its sequence whose tile of keys holds it, as in the other attention calls, but no
  * other sequence.  A row with a NaN score has NaN in o and lse.  Results do not depend on
@@ -633,14 +634,17 @@ cp_status cp_cross_attn_fwd(const cp_cross_desc* desc, int32_t n_seqs, int64_t r
 /* Backward: with dS_ij = P_ij (keep_ij / (1 - p) dO_i . v_j - dO_i . o_i),
  *   dq_i = softmax_scale sum_j dS_ij k_j,  dk_j = softmax_scale sum_i dS_ij q_i,  dv_j = sum_i P_ij keep_ij / (1 - p) dO_i,
  *   dbias[b][h] = sum of dS_ij over the pairs of bucket b, all sequences,
- * grouped heads summed into their kv-head.  o, rest and lse are the forward's for the same inputs and rng.  A row's dS sums to
- * 0, so that a bucket that holds all but w of n keys keeps what dO . o is off by: dbias is off, beyond its own rounding, by
- * sqrt(n / w) of its norm times 2^-18 in bf16 with rest and 2^-21 in float32, as a rule (at most four times that), and by
- * 2^-9 sqrt(n / w) in bf16 without rest, whose dS has the error that the roundings of P and of o make in dO . o, up to 2^-8 P_ij
- * (|dO_i| |o_i| + sum_j P_ij |dO_i . v_j|).
+ * grouped heads summed into their kv-head.  o, rest and lse are the forward's for the same inputs and rng.  A row's
+ * dS sums to 0, so that a bucket that holds all but w of n pairs keeps what dO . o is off by: dbias is off, beyond
+ * its own rounding, by sqrt(n / w) of its norm times 2^-18 in bf16 with rest and 2^-21 in float32, as a rule (at
+ * most four times that), and by 2^-9 sqrt(n / w) in bf16 without rest, whose dS has the error that the roundings
+ * of P and of o make in dO . o, up to 2^-8 P_ij (|dO_i| |o_i| + sum_j P_ij |dO_i . v_j|).
  * dout has the layout of q (row stride in elements).
  * dq, dk and dv [rows][heads][head_dim] are contiguous; rows that no sequence owns (and keys that no query
  * sees) get zeros.  dbias [rel_buckets][heads_q], given iff bias is.  The outputs must not overlap the inputs.
+ * In bf16 P is rounded before dv's product, and dS before dq's and dk's.  A value of q, k, v or dout that is not
+ * finite reaches the gradients of its sequence whose tiles hold it, and dbias, but no other sequence's dq, dk and
+ * dv.
  * In bf16 the dq contributions of the key tiles are added in float32 by hardware reductions whose order is not
  * fixed, so dq may differ in the last bits between calls; all other sums have a fixed order.  ws: as for the
  * forward, with backward = 1.  Errors: as for the forward; CP_ERR_UNSUPPORTED for a bias in bf16 with more than

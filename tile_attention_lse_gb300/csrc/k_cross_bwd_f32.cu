@@ -7,7 +7,9 @@
 // steps on packed pairs (two FMAs an instruction); rows in shared memory are D + 4 floats apart, so that
 // 8 lanes' rows fall on different banks.  P and dS change hands through shared memory, and in the second
 // products a thread owns 4 rows and D / 16 columns.  dQ forms S and dP again (7 products instead of 5)
-// rather than adding up in memory.  The bound is the FFMA rate, and for short sequences the launches.
+// rather than adding up in memory.  Measured, 4 sequences of 2048, 16 heads of 64: 8465 us, 28 TFLOP/s of the 7 products (FFMA
+// about 78); 5 pairs of about 100 over 333, 8 heads over 2: 124 us.  The bound is the wait for a tile's rows, which come
+// between two barriers with nothing under way, and in small calls items that are fewer than the SMs.
 #include <atomic>
 
 #include "cross.h"

@@ -28,10 +28,12 @@
 //    bucket that holds nearly all keys keeps.  Both parts lie over the scores that they come from, 32 columns for
 //    32 keys, so that the columns of P_0 and P_1 hold a third tile's scores: a tile's are free for the next ones behind its
 //    second product only, and with two of them the softmax waited for that (8 x 2048 with a bias 912 and 427 us).
-// Measured, 8 sequences of 2048 queries and keys, 32 heads over 8 of 128 (16 over 16 of 64): 429 us, 1281 TFLOP/s
-// (212 us, 650); with a bias 602 (290); with dropout 826 (408); with both 933 (458).  The plain tile is bound by the
-// tensor pipe and the softmax as the paged kernel's is, dropout by the generator's integer instructions
-// (14 wide products and 14 logic instructions for 8 keys, on pipes that take a warp in 2 cycles or more).
+// Measured, 8 sequences of 2048 queries and keys, 32 heads over 8 of 128 (16 over 16 of 64): 439 us, 1251 TFLOP/s
+// (217 us, 634); with a bias 581 (282); with dropout 821 (410); with both 909 (448); with rest 463 (226), 759 (392), 841
+// (420) and 988 (496).  The plain tile of head_dim 128 is bound by the tensor pipe and the softmax as the paged kernel's is.  Elsewhere no
+// pipe is full (8 x 1024, 16 heads of 64: tensor pipe 28 %, XU 21 %, issue slots 33 %; with bias and dropout ALU 43 %, FMA 29 %,
+// issue slots 43 %): the bound is the chain of a tile, whose second reading waits for every 32 columns and draws (14 wide products and 14 logic
+// instructions for 8 keys) behind the maximum.
 #include <cuda_bf16.h>
 
 #include <atomic>
